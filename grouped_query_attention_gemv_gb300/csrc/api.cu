@@ -4,8 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "gqa.h"
-#include "kernels.h"
+#include "api_internal.h"
 
 using namespace gqa;
 
@@ -19,67 +18,7 @@ thread_local int t_prof_count = 0;
 thread_local int t_fused = 1;
 thread_local int t_attn_split = 0;  // fused decode attention: 0 chosen per call, 1 position-major, 2 head-major
 thread_local unsigned long long t_wait_ns = WAIT_LIMIT_NS;  // grid-wide waits of the decode kernels
-
 thread_local int t_prof_base = 0;  // 1 while a layer call's norm kernel occupies events[0..1]
-void prof_mark(int i, cudaStream_t s) {
-  i += t_prof_base;
-  if (t_prof_events && i < t_prof_count && t_prof_events[i])
-    cudaEventRecord(static_cast<cudaEvent_t>(t_prof_events[i]), s);
-}
-
-// Workspace regions, each 256-byte aligned. The status region is always
-// first: the status word at offset 0, the fused decode grid's progress
-// counters at COUNTERS_OFFSET.
-constexpr size_t COUNTERS_OFFSET = 16;
-struct Layout {
-  size_t status = 0, q = 0, o = 0, proj_part = 0, proj_tickets = 0, part_o = 0, part_ml = 0;
-  size_t total = 0;
-  int np = 0;            // padded tokens of the few-token projection (0: tensor-core GEMM path)
-  int proj_slots = 0;    // partial slots of the few-token projection
-  int att_slots = 0;     // partial slots of the decode attention
-};
-
-// SM count the workspace sizing assumes (GB300); launches use at most this many.
-constexpr int REF_SMS = 152;
-
-bool make_layout(int B, int T, int max_keys, Layout* L) {
-  if (B <= 0 || T <= 0 || max_keys < T) return false;
-  const long long M = static_cast<long long>(B) * T;
-  if (M > (1LL << 24)) return false;
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t r = off;
-    off += (bytes + 255) & ~static_cast<size_t>(255);
-    return r;
-  };
-  L->status = take(256);
-  L->q = take(static_cast<size_t>(M) * D_MODEL * 2);
-  L->o = take(static_cast<size_t>(M) * D_MODEL * 2);
-  L->np = proj_stream_np(static_cast<int>(M));
-  if (L->np) {
-    const int segmax = proj_stream_segmax(QKV_ROWS_MAX, REF_SMS) > proj_stream_segmax(D_MODEL, REF_SMS)
-                           ? proj_stream_segmax(QKV_ROWS_MAX, REF_SMS) : proj_stream_segmax(D_MODEL, REF_SMS);
-    L->proj_slots = REF_SMS * segmax;
-    L->proj_part = take(static_cast<size_t>(L->proj_slots) * 128 * L->np * 4);
-    L->proj_tickets = take(static_cast<size_t>(QKV_ROWS_MAX / 128) * 4);
-  }
-  if (T == 1) {
-    if (B > DECODE_MAX_B) return false;
-    L->att_slots = attn_decode_slots(attn_decode_ctas(REF_SMS));
-    const size_t slots = static_cast<size_t>(L->att_slots) * N_REP;
-    L->part_o = take(slots * HEAD_DIM * 4);
-    L->part_ml = take(slots * 2 * 4);
-  }
-  L->total = off;
-  return true;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int fail_cuda(cudaError_t e) {
-  t_last_cuda = e;
-  return GQA_ECUDA;
-}
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -123,6 +62,33 @@ struct MapCacheEntry {
   bool used;
 };
 
+}  // namespace
+
+namespace gqa {
+
+void prof_mark(int i, cudaStream_t s) {
+  i += t_prof_base;
+  if (t_prof_events && i < t_prof_count && t_prof_events[i])
+    cudaEventRecord(static_cast<cudaEvent_t>(t_prof_events[i]), s);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int fail_cuda(cudaError_t e) {
+  t_last_cuda = e;
+  return GQA_ECUDA;
+}
+
+void begin_call() {
+  t_launches = 0;
+  t_prof_base = 0;
+}
+int launched(cudaError_t e) {
+  if (e != cudaSuccess) return fail_cuda(e);
+  ++t_launches;
+  return GQA_OK;
+}
+
 bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box) {
   EncodeTiledFn enc = encode_fn();
@@ -155,6 +121,71 @@ bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint6
   e.key = k;
   e.map = *m;
   e.used = true;
+  return true;
+}
+
+int sm_count() {
+  static int cached[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return REF_SMS;
+  if (!cached[dev]) {
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = REF_SMS;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+int launch_sms() {
+  const int n = sm_count();
+  return n < REF_SMS ? n : REF_SMS;
+}
+
+}  // namespace gqa
+
+namespace {
+
+// Workspace regions, each 256-byte aligned. The status region is always
+// first: the status word at offset 0, the fused decode grid's progress
+// counters at COUNTERS_OFFSET.
+constexpr size_t COUNTERS_OFFSET = 16;
+struct Layout {
+  size_t status = 0, q = 0, o = 0, proj_part = 0, proj_tickets = 0, part_o = 0, part_ml = 0;
+  size_t total = 0;
+  int np = 0;            // padded tokens of the few-token projection (0: tensor-core GEMM path)
+  int proj_slots = 0;    // partial slots of the few-token projection
+  int att_slots = 0;     // partial slots of the decode attention
+};
+
+bool make_layout(int B, int T, int max_keys, Layout* L) {
+  if (B <= 0 || T <= 0 || max_keys < T) return false;
+  const long long M = static_cast<long long>(B) * T;
+  if (M > (1LL << 24)) return false;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = off;
+    off += (bytes + 255) & ~static_cast<size_t>(255);
+    return r;
+  };
+  L->status = take(256);
+  L->q = take(static_cast<size_t>(M) * D_MODEL * 2);
+  L->o = take(static_cast<size_t>(M) * D_MODEL * 2);
+  L->np = proj_stream_np(static_cast<int>(M));
+  if (L->np) {
+    const int segmax = proj_stream_segmax(QKV_ROWS_MAX, REF_SMS) > proj_stream_segmax(D_MODEL, REF_SMS)
+                           ? proj_stream_segmax(QKV_ROWS_MAX, REF_SMS) : proj_stream_segmax(D_MODEL, REF_SMS);
+    L->proj_slots = REF_SMS * segmax;
+    L->proj_part = take(static_cast<size_t>(L->proj_slots) * 128 * L->np * 4);
+    L->proj_tickets = take(static_cast<size_t>(QKV_ROWS_MAX / 128) * 4);
+  }
+  if (T == 1) {
+    if (B > DECODE_MAX_B) return false;
+    L->att_slots = attn_decode_slots(attn_decode_ctas(REF_SMS));
+    const size_t slots = static_cast<size_t>(L->att_slots) * N_REP;
+    L->part_o = take(slots * HEAD_DIM * 4);
+    L->part_ml = take(slots * 2 * 4);
+  }
+  L->total = off;
   return true;
 }
 
@@ -210,18 +241,6 @@ bool map_q_prefill(CUtensorMap* m, const void* ptr, int B, int T, int n_rep) {
   const cuuint64_t strides[3] = {HEAD_DIM * 2, D_MODEL * 2, static_cast<cuuint64_t>(T) * D_MODEL * 2};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(n_rep), static_cast<cuuint32_t>(128 / n_rep), 1};
   return encode_bf16(m, 4, ptr, dims, strides, box);
-}
-
-int sm_count() {
-  static int cached[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return REF_SMS;
-  if (!cached[dev]) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = REF_SMS;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 struct Call {
@@ -294,11 +313,6 @@ ProjParams proj_params(const Call& c, bool qkv, bool fold_norm = false) {
   p.sp = c.sp;
   p.status = reinterpret_cast<int*>(c.ws + c.L.status);
   return p;
-}
-
-int launch_sms() {
-  const int n = sm_count();
-  return n < REF_SMS ? n : REF_SMS;
 }
 
 // Tensor maps of the few-token projection: boxes of 1..4 k blocks of the

@@ -1,0 +1,638 @@
+// Causal attention of packed tokens of different sequences on the
+// 5th-generation tensor cores, keys and values in a paged cache or packed
+// beside the queries ("Llama 3.1 8B · Grouped-query attention": query t sees
+// keys 0..start_pos + t, softmax in fp32, output heads merged h * 128 + d).
+//
+// The tile scheme is that of the dense prefill attention (attn_prefill.cu):
+// a work item is two 128-row Q tiles of one KV head and one sequence, each
+// 128 / n_rep positions x n_rep query heads (row r: position r / n_rep, head
+// r % n_rep; n_rep need not divide 128, the last rows then stay unused), and
+// every 64-key K/V tile is staged once for both. What differs:
+//   * sequences start anywhere in the packed rows and end anywhere in a tile:
+//     items come from a prefix sum over the sequences' tile counts that every
+//     CTA makes for itself, and Q boxes may reach into the next sequence
+//     (rows that are never stored);
+//   * a K/V tile is 64 / min(page, 64) TMA boxes, one lane of the producer
+//     warp each, so that the table look-ups of a tile are one load wide;
+//   * key rows behind the item's last position may hold anything (the next
+//     sequence, a page's unwritten rows): scores there are masked, and the
+//     issuers clear those value rows in shared memory before the product,
+//     because 0 x NaN is NaN. A NaN among the values of an item's own later
+//     positions, which only its earlier rows mask, cannot be cleared for
+//     some rows of a tile and not for others: a row whose result holds a NaN
+//     is computed again by a warp from its visible keys alone.
+//   warp 8        TMA producer
+//   warps 9, 10   MMA issuers, one per Q tile
+//   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
+// Every barrier wait is bounded; a wait that gives up records
+// DEV_WAIT_TIMEOUT, lets issued copies and products finish (bounded) and frees
+// TMEM before the CTA exits.
+#include <math.h>
+
+#include "kernels.h"
+
+namespace gqa {
+
+namespace {
+
+constexpr int ROWS = 128;                 // rows of a Q tile = MMA M
+constexpr int NQ = 2;                     // Q tiles per CTA
+constexpr int KT = PREFILL_TILE;          // keys per tile
+constexpr int STAGES = 4;                 // K tiles and V tiles in flight
+constexpr int Q_HALF = ROWS * 128;        // 128 rows x 64 dims
+constexpr int Q_TILE = 2 * Q_HALF;
+constexpr int KV_HALF = KT * 128;         // 64 keys x 64 dims
+constexpr int KV_TILE = 2 * KV_HALF;
+constexpr int K_OFF = NQ * Q_TILE;
+constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
+constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
+constexpr int PRE_OFF = BAR_OFF + 512;
+constexpr int SMEM_BYTES = PRE_OFF + (PAGED_MAX_SEQS + 1) * 4 + 1024;
+constexpr int THREADS = 352;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TILE_COLS = 256;       // TMEM columns of one Q tile
+constexpr uint32_t O_COL = 128;
+constexpr float RESCALE_LOG2 = 8.f;
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t kv_full[STAGES], kv_empty[STAGES];  // stage j of an item: K_j and V_{j-1}
+  uint64_t s_full[NQ][2], p_full[NQ][2];
+  uint64_t o_done[NQ], mma_done[NQ];
+  uint32_t tmem_slot;
+  int abort;
+  int q_issued, kv_issued;
+  int warp_sum[THREADS / 32];
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ bool aborted(const Bars& bs) { return *reinterpret_cast<const volatile int*>(&bs.abort) != 0; }
+
+// The packed rows of sequence b: those of cu[b] .. cu[b+1]-1 that exist.
+struct Seq {
+  int row0, T;
+};
+__device__ __forceinline__ Seq seq_at(const PackedPrefillParams& a, int b) {
+  const int r = a.cu[b], e = min(a.cu[b + 1], a.N);
+  return {r, r >= 0 && e > r ? e - r : 0};
+}
+
+// One work item: 2 Q tiles (NQ x qp query positions) of one KV head g of
+// sequence b, and the key tiles they see.
+struct Item {
+  int g, b, q0, row0, T;
+  int start, kv_end;  // cached rows before the sequence's tokens; keys behind kv_end are not the item's
+  int n;              // key tiles of the item (the longer of its Q tiles); 0: the rows are zero
+  int nt[NQ];         // key tiles of each Q tile (0: the tile is past T)
+};
+
+// Items in the order of the sequences, the last pair of Q tiles of each first.
+__device__ __forceinline__ Item item_at(int idx, const int* pre, int qp, const PackedPrefillParams& a) {
+  const int e = idx / a.n_kv;
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= e) lo = mid; else hi = mid;
+  }
+  Item it;
+  it.g = idx - e * a.n_kv;
+  it.b = lo;
+  const Seq s = seq_at(a, lo);
+  it.row0 = s.row0;
+  it.T = s.T;
+  it.q0 = (pre[lo + 1] - 1 - e) * NQ * qp;
+  it.start = a.start ? a.start[lo] : 0;
+  const bool ok = it.start >= 0 && (!a.start || it.start + static_cast<long long>(s.T) <= a.pages.capacity());
+  it.n = 0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int qt = it.q0 + t * qp;
+    it.nt[t] = ok && qt < s.T ? (it.start + min(qt + qp, s.T) + KT - 1) / KT : 0;
+    it.n = max(it.n, it.nt[t]);
+  }
+  it.kv_end = it.start + min(it.q0 + NQ * qp, s.T);
+  return it;
+}
+
+// The items of this CTA in order: round k takes item k * G + c on even rounds
+// and k * G + G - 1 - c on odd ones (G CTAs, c = blockIdx.x).
+struct ItemWalk {
+  int k, nitems, qp;
+  const int* pre;
+  __device__ __forceinline__ ItemWalk(const PackedPrefillParams& a, const int* pre, int qp)
+      : k(0), nitems(pre[a.B] * a.n_kv), qp(qp), pre(pre) {}
+  __device__ __forceinline__ bool next(const PackedPrefillParams& a, Item& it) {
+    const int G = gridDim.x, c = blockIdx.x;
+    for (; k * G < nitems; ++k) {
+      const int idx = k * G + ((k & 1) ? G - 1 - c : c);
+      if (idx >= nitems) continue;
+      it = item_at(idx, pre, qp, a);
+      ++k;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Element offset of key (value) row `key` of the item's sequence and KV head
+// (a table entry out of range, reported by the producer, reads page 0).
+__device__ __forceinline__ long long key_row(const PackedPrefillParams& a, const Item& it, int key, bool value) {
+  if (!a.start)
+    return (static_cast<long long>(it.row0) + key) * (value ? a.v_row_stride : a.pages.row_stride) +
+           it.g * a.pages.head_stride;
+  const int page = a.pages.table[static_cast<long long>(it.b) * a.pages.table_stride + (key >> a.pages.page_shift)];
+  return (page < 0 || page >= a.pages.num_pages ? 0 : page) * a.pages.page_stride +
+         (key & ((1 << a.pages.page_shift) - 1)) * a.pages.row_stride + it.g * a.pages.head_stride;
+}
+
+// One output row from its visible keys 0..lim alone, by a whole warp, in
+// fp32: 32 keys at a time, a key a lane for the scores, 4 dims a lane for the
+// values. For rows that share a tile with non-finite values they do not see.
+__device__ __noinline__ void masked_row(const PackedPrefillParams& a, const Item& it, const __nv_bfloat16* q, int lim,
+                                        __nv_bfloat16* dst) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 <= lim; j0 += 32) {
+    float s = -INFINITY;
+    if (j0 + lane <= lim) {
+      const uint4* k4 = reinterpret_cast<const uint4*>(a.pages.k + key_row(a, it, j0 + lane, false));
+      const uint4* q4 = reinterpret_cast<const uint4*>(q);
+      float x = 0.f;
+#pragma unroll 2
+      for (int i = 0; i < HEAD_DIM / 8; ++i) {
+        const uint4 u = k4[i], w = q4[i];
+        const uint32_t ku[4] = {u.x, u.y, u.z, u.w}, qu[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x += bf16_lo(ku[e]) * bf16_lo(qu[e]) + bf16_hi(ku[e]) * bf16_hi(qu[e]);
+      }
+      s = x * a.scale_log2;
+    }
+    float mx = s;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    mx = fmaxf(mx, m);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float al = ex2_approx(m - ref), pr = ex2_approx(s - ref);
+    float sum = pr;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = l * al + sum;
+    m = mx;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= al;
+    for (int j = j0; j <= min(lim, j0 + 31); ++j) {
+      const float w = __shfl_sync(0xffffffffu, pr, j - j0);
+      const uint2 v = *(reinterpret_cast<const uint2*>(a.pages.v + key_row(a, it, j, true)) + lane);
+      o[0] += w * bf16_lo(v.x);
+      o[1] += w * bf16_hi(v.x);
+      o[2] += w * bf16_lo(v.y);
+      o[3] += w * bf16_hi(v.y);
+    }
+  }
+  const float inv = 1.f / l;
+  *(reinterpret_cast<uint2*>(dst) + lane) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    packed_prefill_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ PackedPrefillParams a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bs = *reinterpret_cast<Bars*>(smem + BAR_OFF);
+  int* pre = reinterpret_cast<int*>(smem + PRE_OFF);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nrep = a.n_heads / a.n_kv;
+  const int qp = ROWS / nrep;  // query positions per Q tile
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bs.q_full), 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&bs.kv_full[s]), 1);
+      mbar_init(smem_u32(&bs.kv_empty[s]), NQ);  // one arrival per MMA issuer
+    }
+    for (int t = 0; t < NQ; ++t) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(smem_u32(&bs.s_full[t][s]), 1);
+        mbar_init(smem_u32(&bs.p_full[t][s]), 4);
+      }
+      mbar_init(smem_u32(&bs.o_done[t]), 1);
+      mbar_init(smem_u32(&bs.mma_done[t]), 1);
+    }
+    bs.abort = 0;
+    bs.q_issued = 0;
+    bs.kv_issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&bs.tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  // pairs of Q tiles per sequence, prefix-summed
+  {
+    const int per = (a.B + THREADS - 1) / THREADS;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, a.B), b1 = min(b0 + per, a.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = seq_at(a, b);
+      if (a.start && blockIdx.x == 0 && s.T > 0) {
+        const int st = a.start[b];
+        if (st < -1 || st + static_cast<long long>(s.T) > a.pages.capacity()) report(a.status, DEV_BAD_POSITION);
+      }
+      const int n = (s.T + NQ * qp - 1) / (NQ * qp);
+      pre[b + 1] = n;
+      sum += n;
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    if (lane == 31) bs.warp_sum[warp] = run;
+    if (threadIdx.x == 0) pre[0] = 0;
+    __syncthreads();
+    run -= sum;
+    for (int w = 0; w < warp; ++w) run += bs.warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      run += pre[b + 1];
+      pre[b + 1] = run;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bs.tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  ItemWalk walk(a, pre, qp);
+  Item it;
+
+  if (warp == PRODUCER_WARP) {
+    if (lane == 0) {
+      tma_prefetch_desc(&mq);
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
+    // stage j of an item holds K_j (j < n) and V_{j-1} (j >= 1), the tiles
+    // its two issuers' iteration j reads: one full and one empty barrier a
+    // stage. u counts stages over the CTA's items, ring slot u % STAGES.
+    // Lane x < boxes handles box x of every tile.
+    const int box = a.start ? prefill_box_rows(1 << a.pages.page_shift) : KT;
+    const int boxes = KT / box;
+    const uint32_t q_bytes = static_cast<uint32_t>(qp * nrep) * 128;
+    int u0 = 0, kvn = 0, qn = 0;
+    int cs[NQ] = {};  // score tiles of each Q tile so far (as its issuer counts them)
+    bool ok = true, stop = false;
+    int row_k = 0, page_k = 0, row_v = 0, page_v = 0;  // coordinates of this lane's box of K_j, V_{j-1}
+    auto locate = [&](const Item& it, int j) {
+      const int key = j * KT + lane * box;
+      if (lane >= boxes || key >= it.kv_end) return;
+      if (!a.start) {
+        row_k = it.row0 + key;
+        return;
+      }
+      row_k = key & ((1 << a.pages.page_shift) - 1);
+      page_k = a.pages.table[static_cast<long long>(it.b) * a.pages.table_stride + (key >> a.pages.page_shift)];
+      if (page_k < 0 || page_k >= a.pages.num_pages) {
+        report(a.status, DEV_BAD_PAGE);
+        page_k = 0;
+      }
+    };
+    // boxes of key tile j that hold keys of the item
+    auto held = [&](const Item& it, int j) { return min(boxes, (it.kv_end - j * KT + box - 1) / box); };
+    // copies of stage j; false when a wait gave up or the kernel is aborting
+    auto load_stage = [&](const Item& it, int j) -> bool {
+      const int u = u0 + j, s = u % STAGES;
+      row_v = row_k;
+      page_v = page_k;
+      if (j < it.n) locate(it, j);
+      if (u >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.kv_empty[s]), ((u / STAGES) - 1) & 1));
+      if (!ok || __any_sync(0xffffffffu, aborted(bs))) return false;
+      const uint32_t fb = smem_u32(&bs.kv_full[s]);
+      const int nk = j < it.n ? held(it, j) : 0, nv = j >= 1 ? held(it, j - 1) : 0;
+      if (lane == 0) mbar_expect_tx(fb, static_cast<uint32_t>(nk + nv) * box * 256);
+      __syncwarp();
+      const uint32_t at = static_cast<uint32_t>(lane * box) * 128;
+      if (lane < nk) {
+        const uint32_t dst = sbase + K_OFF + s * KV_TILE + at;
+        tma_load_4d(dst, &mk, fb, 0, it.g, row_k, page_k);
+        tma_load_4d(dst + KV_HALF, &mk, fb, 64, it.g, row_k, page_k);
+      }
+      if (lane < nv) {
+        const uint32_t dst = sbase + V_OFF + s * KV_TILE + at;
+        tma_load_4d(dst, &mv, fb, 0, it.g, row_v, page_v);
+        tma_load_4d(dst + KV_HALF, &mv, fb, 64, it.g, row_v, page_v);
+      }
+      __syncwarp();
+      kvn = u + 1;
+      return true;
+    };
+    for (int ii = 0; !stop && walk.next(a, it);) {
+      if (it.n == 0) continue;
+      // after the first item, the item's first stages go out before its Q
+      // tiles: their ring slots free up while the previous item's last
+      // products run, the Q tiles only after its last score products have
+      // completed
+      const int la = ii > 0 ? min(STAGES, it.n + 1) : 0;
+      for (int j = 0; j < la && !stop; ++j) stop = !load_stage(it, j);
+      if (stop) break;
+      // Q tile t is free once the last score product of the previous item
+      // that read it has completed (its s_full phase; the next product on
+      // that slot needs the new Q, so the phase cannot have moved on)
+#pragma unroll
+      for (int t = 0; t < NQ; ++t)
+        if (ok && cs[t] > 0)
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t][(cs[t] - 1) & 1]), ((cs[t] - 1) >> 1) & 1));
+      if (!ok || __any_sync(0xffffffffu, aborted(bs))) break;
+      const uint32_t qb = smem_u32(&bs.q_full);
+      if (lane == 0) {
+        const int nq = it.nt[1] ? 2 : 1;
+        mbar_expect_tx(qb, nq * 2 * q_bytes);
+        // boxes may reach into the next sequence, or past N (zeros): rows that are never stored
+        for (int t = 0; t < nq; ++t) {
+          tma_load_3d(sbase + t * Q_TILE, &mq, qb, 0, it.g * nrep, it.row0 + it.q0 + t * qp);
+          tma_load_3d(sbase + t * Q_TILE + Q_HALF, &mq, qb, 64, it.g * nrep, it.row0 + it.q0 + t * qp);
+        }
+      }
+      __syncwarp();
+      ++ii;
+      qn = ii;
+      for (int j = la; j <= it.n && !stop; ++j) stop = !load_stage(it, j);
+      if (stop) break;
+      u0 += it.n + 1;
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) cs[t] += it.nt[t];
+    }
+    if (lane == 0) {
+      if (!ok) atomicExch(&bs.abort, 1);
+      bs.q_issued = qn;
+      bs.kv_issued = kvn;
+    }
+  } else if (warp >= MMA_WARP) {
+    // issuer of Q tile t (the whole warp runs the loop; one elected lane
+    // issues): waits on every K/V stage so that its arrivals on the empty
+    // barriers stay in step with the other issuer's; a stage past this
+    // tile's causal range gets a plain arrival. cs counts this tile's score
+    // tiles over the items (S slot cs % 2, one O product group each).
+    const int t = warp - MMA_WARP;
+    const uint32_t idesc_s = umma_idesc_bf16(ROWS, KT);
+    const uint32_t idesc_o = umma_idesc_bf16(ROWS, HEAD_DIM) | (1u << 16);  // B (V) MN-major
+    const uint32_t qt = sbase + t * Q_TILE;
+    const uint32_t base = tmem + t * TILE_COLS;
+    unsigned u0 = 0, cs = 0;
+    bool ok = true;
+    for (int ii = 0; ok && walk.next(a, it);) {
+      if (it.n == 0) continue;
+      const int n_t = t ? it.nt[1] : it.nt[0];
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.q_full), ii & 1));
+      if (!ok) break;
+      ++ii;
+      for (int j = 0; ok && j <= it.n; ++j) {
+        const unsigned u = u0 + j, s = u % STAGES;
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.kv_full[s]), (u / STAGES) & 1));
+        if (!ok) break;
+        bool used = false;
+        if (j < n_t) {
+          tc_fence_after();
+          const uint32_t kt = sbase + K_OFF + s * KV_TILE;
+          const unsigned slot = (cs + j) & 1u;
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
+              const uint32_t off = (ks & 3) * 32;
+              umma_bf16(base + slot * KT, umma_desc_sw128(qt + (ks >> 2) * Q_HALF + off),
+                        umma_desc_sw128(kt + (ks >> 2) * KV_HALF + off), idesc_s, ks > 0 ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&bs.s_full[t][slot]));
+          }
+          __syncwarp();
+          used = true;
+        }
+        if (j >= 1 && j - 1 < n_t) {
+          const int i = j - 1;
+          const uint32_t vt = sbase + V_OFF + s * KV_TILE;
+          const int left = it.kv_end - i * KT;
+          if (left < KT) {
+            // clear the value rows that are not the item's (both issuers
+            // write the same zeros)
+            for (int w = lane; w < (KT - left) * 16; w += 32) {
+              const int row = left + (w >> 4);
+              st_shared_v4(vt + ((w >> 3) & 1) * KV_HALF + row * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          // P of the item's first key tile also tells that the softmax
+          // warps have read the previous item's O (their epilogue comes
+          // first), so that the first product may overwrite it
+          const unsigned c = cs + i;
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.p_full[t][c & 1]), (c >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < KT / 16; ++ks)
+              umma_bf16_ts(base + O_COL, base + (c & 1) * KT + ks * 8,
+                           umma_desc_sw128_mn(vt + ks * 16 * 128, KV_HALF), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(smem_u32(&bs.o_done[t]));
+          }
+          __syncwarp();
+          used = true;
+        }
+        // the stage is free once this issuer's products on it are done (a
+        // commit covers every product the thread issued before it)
+        if (elect_one()) {
+          if (used)
+            umma_commit(smem_u32(&bs.kv_empty[s]));
+          else
+            mbar_arrive(smem_u32(&bs.kv_empty[s]));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      u0 += it.n + 1;
+      cs += n_t;
+    }
+    if (!ok && lane == 0) atomicExch(&bs.abort, 1);
+    if (elect_one()) umma_commit(smem_u32(&bs.mma_done[t]));
+    __syncwarp();
+    mbar_wait(smem_u32(&bs.mma_done[t]), 0);
+  } else {
+    // softmax / epilogue: warpgroup t, thread r owns row r = TMEM lane r of Q tile t
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const int rp = r / nrep, hh = r - rp * nrep;
+    const bool used = rp < qp;
+    const uint32_t lane_addr = tmem + t * TILE_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float scale = a.scale_log2;
+    unsigned cs = 0;  // score tiles of this Q tile over the items (as the issuer counts them)
+    bool ok = true;
+    while (ok && walk.next(a, it)) {
+      const int n_t = t ? it.nt[1] : it.nt[0];
+      const int pos = it.q0 + t * qp + rp;  // query index within the sequence
+      const bool real = used && pos < it.T;
+      const int lim = used ? min(it.start + pos, it.kv_end - 1) : -1;  // last key this row sees
+      __nv_bfloat16* dst = a.out + (static_cast<size_t>(it.row0) + pos) * a.n_heads * HEAD_DIM +
+                           static_cast<size_t>(it.g * nrep + hh) * HEAD_DIM;
+      if (it.n == 0 && real) {
+#pragma unroll
+        for (int e = 0; e < HEAD_DIM / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+      }
+      float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
+      float l = 0.f;
+      for (int j = 0; j < n_t; ++j) {
+        const unsigned c = cs + j;
+        const unsigned s = c & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t][s]), (c >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sr[KT];
+        tmem_ld32(lane_addr + s * KT, sr);
+        tmem_ld32(lane_addr + s * KT + 32, sr + 32);
+        tmem_ld_wait();
+        const int vis = lim - j * KT;  // columns 0..vis are visible to this row
+        if (vis < KT - 1) {
+#pragma unroll
+          for (int cc = 0; cc < KT; ++cc)
+            if (cc > vis) sr[cc] = __float_as_uint(-INFINITY);
+        }
+        float mx = fmaxf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
+#pragma unroll
+        for (int cc = 2; cc < KT; cc += 2) mx = max3(mx, __uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1]));
+        float alpha = 1.f;
+        const bool grow = mx > m_ref && (m_ref == -INFINITY || (mx - m_ref) * scale > RESCALE_LOG2);
+        if (grow) {
+          alpha = m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - mx) * scale);
+          m_ref = mx;
+        }
+        const float neg = m_ref == -INFINITY ? 0.f : -m_ref * scale;
+        // exponent arguments and the row sum two columns per instruction
+        const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
+        float2 sum2 = make_float2(0.f, 0.f);
+        uint32_t pk[KT / 2];
+#pragma unroll
+        for (int cc = 0; cc < KT; cc += 2) {
+          const float2 e = fma2(make_float2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, ng2);
+          const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+          sum2 = add2(sum2, p);
+          pk[cc >> 1] = pack_bf16(p.x, p.y);
+        }
+        l = l * alpha + (sum2.x + sum2.y);
+        if (j > 0) {
+          // O must hold P_{j-1} V_{j-1} before it is rescaled (and this keeps
+          // the o_done phases in step with the score tiles)
+          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), (c - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+            for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+              uint32_t o[32];
+              tmem_ld32(lane_addr + O_COL + cc, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(lane_addr + O_COL + cc, o);
+            }
+          }
+        }
+        tmem_st32(lane_addr + s * KT, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bs.p_full[t][s]));
+      }
+      if (!ok) break;
+      if (n_t > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), (cs + n_t - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float inv = 1.f / l;
+        float chk = 0.f;  // NaN when any value of the row is not finite
+#pragma unroll 1
+        for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + O_COL + cc, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) chk = fmaf(__uint_as_float(o[e]), 0.f, chk);
+          if (real) {
+            uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+              w.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+              w.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+              w.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+              d4[e] = w;
+            }
+          }
+        }
+        unsigned again = __ballot_sync(0xffffffffu, real && chk != chk && lim < it.kv_end - 1);
+        const Item same = it;
+        for (; again; again &= again - 1) {
+          const int src = __ffs(again) - 1;
+          const int p2 = __shfl_sync(0xffffffffu, pos, src), h2 = __shfl_sync(0xffffffffu, hh, src);
+          const size_t row = static_cast<size_t>(it.row0) + p2;
+          const int head = it.g * nrep + h2;
+          __syncwarp();
+          masked_row(a, same, a.q + static_cast<long long>(row) * a.q_stride + head * HEAD_DIM, it.start + p2,
+                     a.out + (row * a.n_heads + head) * HEAD_DIM);
+        }
+      }
+      cs += n_t;
+    }
+    if (!ok && lane == 0) atomicExch(&bs.abort, 1);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (aborted(bs)) {
+    if (threadIdx.x == 0) report(a.status, DEV_WAIT_TIMEOUT);
+    if (warp == PRODUCER_WARP && lane == 0) {
+      // the last copy into each buffer may still be in flight
+      if (bs.q_issued > 0) mbar_wait(smem_u32(&bs.q_full), (bs.q_issued - 1) & 1);
+      for (int u = max(0, bs.kv_issued - STAGES); u < bs.kv_issued; ++u)
+        mbar_wait(smem_u32(&bs.kv_full[u % STAGES]), (u / STAGES) & 1);
+    }
+    __syncthreads();
+  }
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& a, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(packed_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  if (a.B <= 0 || a.B > PAGED_MAX_SEQS || a.N <= 0 || a.ctas <= 0) return cudaErrorInvalidValue;
+  // one CTA per SM (shared memory and TMEM admit no second), each walking its
+  // items; no more CTAs than the packed rows can make items
+  const int qp = ROWS / (a.n_heads / a.n_kv);
+  const long long items = (static_cast<long long>(a.N) / (NQ * qp) + a.B) * a.n_kv;
+  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned ctas = static_cast<unsigned>(items < a.ctas ? items : a.ctas);
+  packed_prefill_kernel<<<ctas, THREADS, SMEM_BYTES, s>>>(maps.q, maps.k, maps.v, a);
+  return cudaGetLastError();
+}
+
+}  // namespace gqa

@@ -1,0 +1,489 @@
+// Attention of one new token per sequence over a paged cache, split over the
+// length and joined ("Llama 3.1 8B · Grouped-query attention", mode decode:
+// o_h = softmax(scale q_h K_g^T) V_g over cache rows 0..start_pos, KV head
+// g = h / n_rep; each K/V row is loaded once for its n_rep query heads).
+//
+// n_rep flops a byte: the bound is memory, so the design is about keeping
+// every SM streaming the same number of bytes whatever the lengths.
+//   * A chunk is 16 positions of one KV head (8 KB of K and V). All chunks, in
+//     (sequence, KV head, position) order, are cut into equal contiguous
+//     ranges, one per CTA, and each CTA's range into one per warp. KV heads
+//     come before positions so that few ranges meet in one output: a long
+//     sequence is joined from ctas / n_kv partials per KV head.
+//   * Each warp streams its range through its own ring of STAGES chunks with
+//     cp.async, its page ids looked up one chunk ahead; nothing but the end
+//     of the CTA synchronises warps. Rows past the sequence are filled with
+//     zeros instead of being read (they may hold anything).
+//   * S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 (the 16 keys, then
+//     the dims, on the M side, query heads padded to 8 or 16 on the N side).
+//     The probabilities enter the product as two bf16 terms, P = hi + lo, so
+//     that the output's own rounding is the only 8-bit one; the tensor pipe
+//     has the time.
+//   * A (sequence, KV head) wholly inside a warp's range is finished in
+//     registers. The other parts are joined by the log-sum-exp rule, first in
+//     shared memory among the CTA's warps, then, where several CTAs hold
+//     parts, by the CTA that arrives last at a ticket, in CTA order: the
+//     result does not depend on the order of arrival, and no CTA waits.
+#include <math.h>
+
+#include "kernels.h"
+
+namespace gqa {
+
+namespace {
+
+constexpr int KEYS = 16;                          // positions of a chunk
+constexpr int ROW_BYTES = HEAD_DIM * 2;
+constexpr int TILE_BYTES = KEYS * ROW_BYTES;      // K or V of a chunk
+constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+constexpr int STAGES = 3;
+constexpr int MAX_WARPS = 8;
+constexpr int PART = HEAD_DIM + 2;                // floats of a partial row: o, max, sum
+
+// Row r, 16-byte piece c of a 256-byte-row tile: eight rows of one piece fall
+// into eight different 16-byte columns.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return static_cast<uint32_t>(r * ROW_BYTES + ((c ^ (r & 7)) << 4));
+}
+
+// A place in the chunk order.
+struct Cursor {
+  int b, h, j;  // sequence, KV head, chunk of it
+  int n;        // chunks of the sequence (for each KV head)
+};
+
+// pre[b]: chunks per KV head of the sequences before b.
+__device__ __forceinline__ Cursor locate(long long u, const int* pre, int B, int n_kv) {
+  const int x = static_cast<int>(u / n_kv);  // pre[b] <= x < pre[b + 1] exactly when u lies in sequence b
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  Cursor c;
+  c.b = lo;
+  c.n = pre[lo + 1] - pre[lo];
+  const int r = static_cast<int>(u - static_cast<long long>(pre[lo]) * n_kv);
+  c.h = r / c.n;
+  c.j = r - c.h * c.n;
+  return c;
+}
+__device__ __forceinline__ void advance(Cursor& c, const int* pre, int B, int n_kv) {
+  if (++c.j < c.n) return;
+  c.j = 0;
+  if (++c.h < n_kv) return;
+  c.h = 0;
+  do {
+    if (++c.b >= B) return;
+    c.n = pre[c.b + 1] - pre[c.b];
+  } while (c.n == 0);
+}
+
+__device__ __forceinline__ long long range_start(long long c, long long total, long long parts) {
+  return total * c / parts;
+}
+// The part whose range holds chunk u.
+__device__ __forceinline__ int part_of(long long u, long long total, long long parts) {
+  return static_cast<int>(((u + 1) * parts - 1) / total);
+}
+
+struct Range {
+  long long first, end;  // chunks of one (sequence, KV head)
+};
+__device__ __forceinline__ Range segment(int id, const int* pre, int n_kv) {
+  const int b = id / n_kv, h = id - b * n_kv, n = pre[b + 1] - pre[b];
+  const long long first = static_cast<long long>(pre[b]) * n_kv + static_cast<long long>(h) * n;
+  return {first, first + n};
+}
+
+// NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16).
+template <int NT>
+__global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDecodeParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_rep = p.n_heads / p.n_kv;
+  uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
+  // per warp: the partial of the part that began before its range; the one
+  // that goes on behind it is put into the ring when the warp is done
+  float* stash = reinterpret_cast<float*>(smem + W * (STAGES * STAGE_BYTES));
+  int* pre = reinterpret_cast<int*>(stash + W * n_rep * PART);
+  __shared__ int ids[2 * MAX_WARPS];   // (sequence, KV head) of each warp's two partials, or -1
+  __shared__ int warp_sum[MAX_WARPS];
+  __shared__ int last_of[2];
+
+  // chunks per sequence, prefix-summed; unused slots and bad positions have none
+  {
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int s = p.start[b];
+      const bool ok = s >= 0 && s < p.pages.capacity();
+      if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
+      const int n = ok ? s / KEYS + 1 : 0;
+      pre[b + 1] = n;
+      sum += n;
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
+    }
+    if (lane == 31) warp_sum[warp] = run;
+    if (threadIdx.x < 2 * MAX_WARPS) ids[threadIdx.x] = -1;
+    if (threadIdx.x == 0) pre[0] = 0;
+    __syncthreads();
+    run -= sum;
+    for (int w = 0; w < warp; ++w) run += warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      run += pre[b + 1];
+      pre[b + 1] = run;
+    }
+    __syncthreads();
+  }
+  // rows of sequences without keys
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (pre[b + 1] == pre[b])
+      for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
+        reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
+
+  const long long total = static_cast<long long>(pre[p.B]) * p.n_kv;
+  // no more CTAs than leave each warp a chunk
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + W - 1) / W));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long c0 = range_start(blockIdx.x, total, ctas), c1 = range_start(blockIdx.x + 1, total, ctas);
+  const long long a0 = c0 + range_start(warp, c1 - c0, W), a1 = c0 + range_start(warp + 1, c1 - c0, W);
+  const int n = static_cast<int>(a1 - a0);
+
+  const int gr = lane >> 2, t = lane & 3;
+  const int half = lane >> 4, piece = lane & 15;
+
+  if (n > 0) {
+    Cursor iss = locate(a0, pre, p.B, p.n_kv), cur = iss;
+    // element offset of row lane % 16 of the chunk at `iss`, -1 for a row past the sequence
+    auto row_offset = [&]() -> long long {
+      const int pos = iss.j * KEYS + piece;
+      if (pos > p.start[iss.b]) return -1;
+      const int page = p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)];
+      if (page < 0 || page >= p.pages.num_pages) {
+        report(p.status, DEV_BAD_PAGE);
+        return -1;
+      }
+      return page * p.pages.page_stride + (pos & ((1 << p.pages.page_shift) - 1)) * p.pages.row_stride +
+             iss.h * p.pages.head_stride;
+    };
+    int issued = 0;
+    long long next = row_offset();
+    const uint32_t ring32 = smem_u32(ring);
+    auto issue = [&]() {
+      if (issued < n) {
+        const uint32_t dst = ring32 + (issued % STAGES) * STAGE_BYTES;
+        const long long off = next;
+        ++issued;
+        if (issued < n) {
+          advance(iss, pre, p.B, p.n_kv);
+          next = row_offset();
+        }
+#pragma unroll
+        for (int i = 0; i < KEYS / 2; ++i) {
+          const int r = 2 * i + half;
+          const long long o = __shfl_sync(0xffffffffu, off, r);
+          const long long e = (o < 0 ? 0 : o) + piece * 8;
+          const uint32_t bytes = o < 0 ? 0u : 16u;
+          cp_async16(dst + tile_at(r, piece), p.pages.k + e, bytes);
+          cp_async16(dst + TILE_BYTES + tile_at(r, piece), p.pages.v + e, bytes);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    uint32_t qb[NT][8][2];  // Q^T as B fragments: dims 16s + 2t (+1) | +8, query head 8 nt + gr
+    float m_run[NT][2], l_run[NT][2], oacc[NT][8][4];  // heads 8 nt + 2t (+1); O^T tile d: dims 16d + gr (+8)
+    for (int i = 0; i < n; ++i) {
+      issue();
+      if (i == 0 || cur.j == 0) {
+        const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q + cur.b * p.q_stride + cur.h * n_rep * HEAD_DIM);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int h = nt * 8 + gr;
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            qb[nt][s][0] = h < n_rep ? __ldg(q32 + h * (HEAD_DIM / 2) + s * 8 + t) : 0u;
+            qb[nt][s][1] = h < n_rep ? __ldg(q32 + h * (HEAD_DIM / 2) + s * 8 + 4 + t) : 0u;
+          }
+          m_run[nt][0] = m_run[nt][1] = -INFINITY;
+          l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) oacc[nt][d][0] = oacc[nt][d][1] = oacc[nt][d][2] = oacc[nt][d][3] = 0.f;
+        }
+      }
+      cp_async_wait<STAGES - 1>();
+      __syncwarp();
+      const uint32_t kt = ring32 + (i % STAGES) * STAGE_BYTES, vt = kt + TILE_BYTES;
+
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        uint32_t k0, k1, k2, k3;
+        ldsm_x4(kt + tile_at(lane & 15, 2 * s + half), k0, k1, k2, k3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], k0, k1, k2, k3, qb[nt][s][0], qb[nt][s][1]);
+      }
+      // rows gr and gr + 8 of the chunk
+      const int left = p.start[cur.b] - cur.j * KEYS;
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float(&x)[4] = sc[nt];
+        x[0] = gr <= left ? x[0] * p.scale_log2 : -INFINITY;
+        x[1] = gr <= left ? x[1] * p.scale_log2 : -INFINITY;
+        x[2] = gr + 8 <= left ? x[2] * p.scale_log2 : -INFINITY;
+        x[3] = gr + 8 <= left ? x[3] * p.scale_log2 : -INFINITY;
+        float pr[4], al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = fmaxf(mx, m_run[nt][e]);
+          // scores that are all -inf leave the maximum there: no term, not a NaN
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          al[e] = ex2_approx(m_run[nt][e] - ref);
+          pr[e] = ex2_approx(x[e] - ref);
+          pr[e + 2] = ex2_approx(x[e + 2] - ref);
+          m_run[nt][e] = mx;
+          l_run[nt][e] = l_run[nt][e] * al[e] + (pr[e] + pr[e + 2]);  // this lane's rows; summed over lanes at the end
+        }
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          oacc[nt][d][0] *= al[0];
+          oacc[nt][d][1] *= al[1];
+          oacc[nt][d][2] *= al[0];
+          oacc[nt][d][3] *= al[1];
+        }
+        // P^T as B fragments, (head gr, keys 2t, 2t + 1) and 8 keys further
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // hi: the upper 16 bits; lo: the rest, kept above 0 where P is, so
+          // that an infinite value row gives an infinite sum and not a NaN
+          const float x0 = pr[2 * e], x1 = pr[2 * e + 1];
+          const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
+          hi[nt][e] = movmatrix_t(__byte_perm(u0, u1, 0x7632));
+          const float y0 = x0 - __uint_as_float(u0 & 0xffff0000u), y1 = x1 - __uint_as_float(u1 & 0xffff0000u);
+          lo[nt][e] = movmatrix_t(pack_bf16(fmaxf(y0, x0 * 0x1p-24f), fmaxf(y1, x1 * 0x1p-24f)));
+        }
+      }
+      const int vr = (lane & 7) + (half << 3);  // key row of this lane's ldmatrix address
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t v0, v1, v2, v3;
+        ldsm_x4_t(vt + tile_at(vr, 2 * d + ((lane >> 3) & 1)), v0, v1, v2, v3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(oacc[nt][d], v0, v1, v2, v3, hi[nt][0], hi[nt][1]);
+          mma16816(oacc[nt][d], v0, v1, v2, v3, lo[nt][0], lo[nt][1]);
+        }
+      }
+      __syncwarp();  // the chunk's rows are read before its slot is filled again
+
+      const Cursor here = cur;
+      advance(cur, pre, p.B, p.n_kv);
+      if (i + 1 < n && cur.j != 0) continue;
+
+      // end of this warp's part of (here.b, here.h)
+      const int id = here.b * p.n_kv + here.h;
+      const Range seg = segment(id, pre, p.n_kv);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
+      if (seg.first >= a0 && seg.end <= a1) {
+        __nv_bfloat16* out = p.out + (static_cast<long long>(here.b) * p.n_heads + here.h * n_rep) * HEAD_DIM;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float i0 = 1.f / l_run[nt][0], i1 = 1.f / l_run[nt][1];
+          const int h = nt * 8 + gr;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            // (dim gr, heads 2t, 2t + 1) -> (head gr, dims 2t, 2t + 1)
+            const uint32_t w0 = movmatrix_t(pack_bf16(oacc[nt][d][0] * i0, oacc[nt][d][1] * i1));
+            const uint32_t w1 = movmatrix_t(pack_bf16(oacc[nt][d][2] * i0, oacc[nt][d][3] * i1));
+            if (h < n_rep) {
+              uint32_t* o32 = reinterpret_cast<uint32_t*>(out + h * HEAD_DIM + 16 * d) + t;
+              o32[0] = w0;
+              o32[4] = w1;
+            }
+          }
+        }
+      } else {
+        const int slot = seg.first < a0 ? 0 : 1;
+        float* part = slot == 0 ? stash + warp * n_rep * PART : reinterpret_cast<float*>(ring);
+        if (slot == 1) {
+          // the last part of the range: every copy into the ring has landed and been read
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = nt * 8 + 2 * t + e;
+            if (h >= n_rep) continue;
+            float* row = part + h * PART;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              row[16 * d + gr] = oacc[nt][d][e];
+              row[16 * d + gr + 8] = oacc[nt][d][e + 2];
+            }
+            if (gr == 0) {
+              row[HEAD_DIM] = m_run[nt][e];
+              row[HEAD_DIM + 1] = l_run[nt][e];
+            }
+          }
+        if (lane == 0) ids[2 * warp + slot] = id;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- join this CTA's parts: entries 2w, 2w + 1 of `ids` in order; equal
+  // ids follow each other. (part, query head) pairs are dealt to the warps.
+  auto part_at = [&](int e) -> const float* {
+    return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
+                   : stash + (e >> 1) * n_rep * PART;
+  };
+  int split[2] = {-1, -1};  // ids whose parts are in other CTAs too: begun before this one, going on behind it
+  for (int e = 0, k = 0; e < 2 * W;) {
+    const int id = ids[e];
+    if (id < 0) {
+      ++e;
+      continue;
+    }
+    int f = e + 1;
+    while (f < 2 * W && (ids[f] < 0 || ids[f] == id)) ++f;
+    const Range seg = segment(id, pre, p.n_kv);
+    const bool whole = seg.first >= c0 && seg.end <= c1;
+    const int side = seg.first < c0 ? 0 : 1;
+    if (!whole) split[side] = id;
+    for (int r = 0; r < n_rep; ++r, ++k) {
+      if (k % W != warp) continue;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g = e; g < f; ++g)
+        if (ids[g] >= 0) m = fmaxf(m, part_at(g)[r * PART + HEAD_DIM]);
+      const float ref = m == -INFINITY ? 0.f : m;
+      for (int g = e; g < f; ++g) {
+        if (ids[g] < 0) continue;
+        const float* row = part_at(g) + r * PART;
+        const float w = ex2_approx(row[HEAD_DIM] - ref);
+        l += w * row[HEAD_DIM + 1];
+        const float2 x = *reinterpret_cast<const float2*>(row + 4 * lane);
+        const float2 y = *reinterpret_cast<const float2*>(row + 4 * lane + 2);
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * y.x;
+        o.w += w * y.y;
+      }
+      if (whole) {
+        const float inv = 1.f / l;
+        const int b = id / p.n_kv, h = (id - b * p.n_kv) * n_rep + r;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(b) * p.n_heads + h) * HEAD_DIM + 4 * lane) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      } else {
+        const long long at = (2LL * blockIdx.x + side) * n_rep + r;
+        __stcg(reinterpret_cast<float4*>(p.part_o + at * HEAD_DIM) + lane, o);
+        if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + at, make_float2(m, l));
+      }
+    }
+    e = f;
+  }
+  if (split[0] < 0 && split[1] < 0) return;
+
+  // ---- across CTAs: the ticket is the one of the CTA that holds the segment's first chunk
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    const int id = split[threadIdx.x];
+    int last = 0;
+    if (id >= 0) {
+      const Range seg = segment(id, pre, p.n_kv);
+      const int first = part_of(seg.first, total, ctas), end = part_of(seg.end - 1, total, ctas);
+      __threadfence();
+      last = atomicAdd(p.tickets + first, 1) == end - first;
+      if (last) p.tickets[first] = 0;
+      __threadfence();
+    }
+    last_of[threadIdx.x] = last;
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side) {
+    if (!last_of[side]) continue;
+    const int id = split[side];
+    const Range seg = segment(id, pre, p.n_kv);
+    const int first = part_of(seg.first, total, ctas), end = part_of(seg.end - 1, total, ctas);
+    // the part of its first CTA goes on behind that CTA (slot 1), the others began before theirs (slot 0)
+    for (int r = warp; r < n_rep; r += W) {
+      auto at = [&](int c) { return (2LL * c + (c == first)) * n_rep + r; };
+      float m = -INFINITY;
+      for (int c = first + lane; c <= end; c += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c)).x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float ref = m == -INFINITY ? 0.f : m;
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int c = first; c <= end; ++c) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c));
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(c) * HEAD_DIM) + lane);
+        const float w = ex2_approx(ml.x - ref);
+        l += w * ml.y;
+        o.x += w * x.x;
+        o.y += w * x.y;
+        o.z += w * x.z;
+        o.w += w * x.w;
+      }
+      const float inv = 1.f / l;
+      const int b = id / p.n_kv, h = (id - b * p.n_kv) * n_rep + r;
+      *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(b) * p.n_heads + h) * HEAD_DIM + 4 * lane) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    }
+  }
+}
+
+template <int NT>
+cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int n_rep = p.n_heads / p.n_kv;
+  // more than 4 query heads a KV head: the partials' share of shared memory leaves room for 6 rings
+  const int warps = n_rep <= 4 ? MAX_WARPS : 6;
+  const size_t smem = static_cast<size_t>(warps) * (STAGES * STAGE_BYTES + n_rep * PART * 4) + (p.B + 1) * 4;
+  paged_decode_kernel<NT><<<p.ctas, warps * 32, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s) {
+  if (p.B <= 0 || p.B > PAGED_MAX_SEQS || p.ctas <= 0) return cudaErrorInvalidValue;
+  const int n_rep = p.n_heads / p.n_kv;
+  if (n_rep < 1 || n_rep > PAGED_MAX_REP) return cudaErrorInvalidValue;
+  return n_rep <= 8 ? launch_nt<1>(p, s) : launch_nt<2>(p, s);
+}
+
+}  // namespace gqa

@@ -69,6 +69,7 @@ typedef uint16_t gqa_bf16;
 #define GQA_DEV_OK 0
 #define GQA_DEV_BAD_POSITION 1  /* a start position < 0 or >= S_max / rope rows */
 #define GQA_DEV_WAIT_TIMEOUT 2  /* a bounded barrier wait gave up */
+#define GQA_DEV_BAD_PAGE 3      /* a block table entry outside [0, num_pages) */
 
 /* Bytes of workspace a call with batch B, T new tokens per sequence and at
  * most max_keys = start_pos + T cache rows read per sequence needs. The
@@ -339,6 +340,106 @@ int gqa_decode_host(const gqa_bf16* x_host, int B, const int32_t* start_pos, int
                     size_t stage_bytes, void* workspace, size_t workspace_bytes, void* stream);
 int gqa_host_stage_wait(void* stage, void* stream);
 int gqa_host_stage_release(void* stage);
+
+/* ---------------------------------------------------------------------------
+ * Serving operators over a paged KV cache: the block's RoPE + cache append and
+ * its attention on their own, for a server that packs the tokens of many
+ * sequences into one batch and keeps their cache in pages. One step is
+ * gqa_paged_append, then gqa_paged_decode (one new token per sequence) or
+ * gqa_paged_prefill (any number of new tokens per sequence), between the
+ * caller's own projections. gqa_packed_prefill attends over keys and values
+ * packed beside the queries instead of a cache.
+ *
+ * Head size 128, n_heads a multiple of n_kv_heads with at most 16 query heads
+ * per KV head; query head h reads KV head h / (n_heads / n_kv_heads).
+ *
+ * Packed tokens: the N rows of q, k, v are the new tokens of sequence 0, then
+ * of sequence 1, and so on. cu_tokens (device int32 [B+1], non-decreasing)
+ * gives sequence b the rows cu_tokens[b] .. cu_tokens[b+1]-1; it may be empty.
+ * Rows outside [cu_tokens[0], cu_tokens[B]) and rows at or past N belong to
+ * no sequence: nothing is read from or written for them.
+ *
+ * start_pos (device int32 [B]): sequence b has start_pos[b] cached rows before
+ * the call, so its i-th new token is at position start_pos[b] + i. -1 marks an
+ * unused slot (a padded batch): its tokens append nothing and their attention
+ * rows are zero. Other values with a token at or past columns * page_size (or
+ * rope_rows), and values below -1, are reported as GQA_DEV_BAD_POSITION.
+ *
+ * Every entry enqueues on `stream` of the current device, allocates nothing
+ * and can be captured into a graph; no length is read by the host, so a
+ * captured step replays with other lengths, tables and contents. The
+ * workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled before its first
+ * use, and serves one call at a time; its status word is read with
+ * gqa_device_status. */
+
+#define GQA_PAGED_WORKSPACE_BYTES (64u << 20)
+#define GQA_PAGED_MAX_SEQS 2048   /* sequences per call */
+#define GQA_PAGED_MAX_REP 16      /* query heads per KV head */
+
+/* A paged cache. Row `r` of page `p` for KV head `g` starts at element
+ * p * page_stride + r * row_stride + g * head_stride of k and of v; position
+ * s of sequence b is row s % page_size of page block_table[b * table_stride +
+ * s / page_size]. Every pointer 16-byte aligned (block_table: 4-byte), the
+ * strides multiples of 8 elements, page_size a power of two in [16, 65536].
+ * Only the table entries of pages that hold a read or written position are
+ * looked at; one outside [0, num_pages) is reported as GQA_DEV_BAD_PAGE and
+ * what the call writes for that sequence is unspecified. */
+typedef struct gqa_pages {
+  gqa_bf16* k;
+  gqa_bf16* v;
+  int64_t page_stride, row_stride, head_stride;
+  const int32_t* block_table;
+  int num_pages, page_size, n_kv_heads;
+  int table_stride, columns;
+} gqa_pages;
+
+/* Rotates packed queries and keys by RoPE at their positions and writes keys
+ * and values into the pages (the Q|K|V epilogue of the block, for tokens that
+ * were projected elsewhere).
+ *   q, k, v  [N, heads, 128]: row n of q starts at element n * q_stride, its
+ *            heads follow each other (slices of one [N, (n_heads + 2 n_kv) *
+ *            128] projection output qualify). q and q_out may both be NULL.
+ *   cu_tokens may be NULL: one new token per sequence (N = B)
+ *   rope     [rope_rows, 64, 2] from gqa_rope_table
+ *   q_out    [N, n_heads, 128] dense, the rotated queries; may be q itself
+ *            when q is dense
+ * Rotations are computed in fp32 and rounded once to bf16; values are copied.
+ * No two new tokens may share a cache row. */
+int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                     int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B, const int32_t* start_pos,
+                     const float* rope, int rope_rows, const gqa_pages* pages, gqa_bf16* q_out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Attention of one new token per sequence over the paged cache: for every
+ * query head, softmax(scale q K^T) V over cache rows 0..start_pos[b] (row
+ * start_pos[b] is the token's own, appended before). start_pos[b] = -1: the
+ * row of out is zero.
+ *   q    [B, n_heads, 128], row b at element b * q_stride, heads dense
+ *   out  [B, n_heads, 128] dense
+ *   scale finite, > 0 (1 / sqrt(128) for the block's attention)
+ * Scores, softmax and sums in fp32; the probabilities enter the value product
+ * as two bf16 terms (16 significant bits). */
+int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                     const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Causal attention of packed new tokens over the paged cache, which already
+ * holds them: token i of sequence b reads rows 0..start_pos[b] + i. Whole
+ * prompts (start_pos 0) and chunks after a cached prefix, in one batch.
+ *   q    [N, n_heads, 128], row n at element n * q_stride, heads dense
+ *   out  [N, n_heads, 128] dense; rows of no sequence are left as they were
+ * Scores, softmax and sums in fp32; the probabilities enter the value product
+ * rounded to bf16. */
+int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
+                      const int32_t* start_pos, const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* gqa_paged_prefill for whole prompts without a cache: token i of a sequence
+ * reads the keys and values of its tokens 0..i.
+ *   k, v  [N, n_kv_heads, 128], row n at element n * k_stride (v_stride) */
+int gqa_packed_prefill(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                       int64_t v_stride, int N, int n_heads, int n_kv_heads, const int32_t* cu_tokens, int B,
+                       float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
