@@ -1,6 +1,6 @@
 """GB300 grouped-query attention block (Llama 3.1 8B) — Python binding.
 
-A thin ctypes layer over the C ABI in ``include/gqa.h`` (``lib/libgqa.so``,
+A thin layer (ctypes, mostly) over the C ABI in ``include/gqa.h`` (``lib/libgqa.so``,
 built in-tree by ``python -m grouped_query_attention_gemv_gb300.build``).
 It only checks and marshals arguments: every step of the block runs in the
 library's CUDA kernels. PyTorch supplies device memory and streams.
@@ -13,13 +13,16 @@ entries ``block_forward_host`` / ``decode_host`` (with ``make_host_stage``,
 ``rope_table``, ``workspace_bytes``, ``device_status``, ``last_launch_count``;
 and the serving operators over a paged cache ``paged_append`` /
 ``paged_decode`` / ``paged_prefill`` / ``packed_prefill`` (with
-``make_paged_workspace``).
+``make_paged_workspace``), whose argument checks are compiled
+(``csrc/binding.cpp``).
 If the library has not been built every call raises ``ImportError``; there is
 no fallback path.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 from typing import Optional
@@ -42,6 +45,7 @@ STATIC_SCRATCH_BYTES = 16 << 20
 PAGED_WORKSPACE_BYTES = 64 << 20
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "lib", "libgqa.so")
+_BINDING_PATH = os.path.join(_PKG, "lib", "gqa_binding.so")
 _HEADER = os.path.join(os.path.dirname(_PKG), "include", "gqa.h")
 
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
@@ -505,112 +509,41 @@ def block_forward_host(x_host, start_pos: int, wq, wk, wv, wo, rope, cache_k, ca
 
 # ------------------------------------------------------------ paged serving operators
 
-class _Pages(ctypes.Structure):
-    """gqa_pages of the C ABI."""
-    _fields_ = [("k", _vp), ("v", _vp), ("page_stride", _ll), ("row_stride", _ll), ("head_stride", _ll),
-                ("block_table", _vp), ("num_pages", _i), ("page_size", _i), ("n_kv_heads", _i),
-                ("table_stride", _i), ("columns", _i)]
-
-
 def make_paged_workspace(device=None) -> torch.Tensor:
     """A zero-filled workspace for the paged operators (one call at a time)."""
     return torch.zeros(PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
 
 
-def _rows(t, name, n, heads, device):
-    """Elements between the rows of packed tokens t [n, heads, 128], whose
-    heads follow each other."""
-    if not isinstance(t, torch.Tensor):
+_paged = None
+
+
+def _binding():
+    """The compiled argument checks of the paged operators (lib/gqa_binding.so,
+    built with libgqa); raises ImportError when they have not been built."""
+    global _paged
+    if _paged is None:
+        lib()
+        if not os.path.exists(_BINDING_PATH):
+            raise ImportError(f"gqa_binding.so is not built ({_BINDING_PATH}); run "
+                              "`python -m grouped_query_attention_gemv_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("gqa_binding", _BINDING_PATH)
+        _paged = loader.create_module(importlib.util.spec_from_loader("gqa_binding", loader))
+    return _paged
+
+
+def _defaults(like, name, out, workspace, stream):
+    """The output, shaped like packed rows `like`, and the workspace of a call
+    that was given none: memory of the stream that uses it."""
+    if not isinstance(like, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3 or t.shape != (n, heads, HEAD_DIM):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, HEAD_DIM)}")
-    s = t.stride()
-    if s[2] != 1 or (s[1] != HEAD_DIM and heads > 1):
-        raise ValueError(f"{name}: the 128 elements of a head and the heads of a token must follow each other")
-    return s[0] if n > 1 else heads * HEAD_DIM
-
-
-def _ints(t, name, n, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.device != device or not t.is_contiguous() or t.shape != (n,):
-        raise ValueError(f"{name} must be a contiguous [{n}] tensor on {device}")
-    return t.data_ptr()
-
-
-def _pages(k_pages, v_pages, block_table, B, device):
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (block_table, "block_table")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-    if k_pages.dtype != torch.bfloat16 or v_pages.dtype != torch.bfloat16:
-        raise TypeError("k_pages and v_pages must be torch.bfloat16")
-    shape, s = k_pages.shape, k_pages.stride()
-    if k_pages.dim() != 4 or shape[3] != HEAD_DIM or v_pages.shape != shape:
-        raise ValueError(f"k_pages and v_pages must both be [pages, page_size, n_kv, {HEAD_DIM}], got "
-                         f"{tuple(shape)} and {tuple(v_pages.shape)}")
-    if k_pages.device != device or v_pages.device != device or block_table.device != device:
-        raise ValueError(f"k_pages, v_pages and block_table must be on {device}")
-    if v_pages.stride() != s or s[3] != 1:
-        raise ValueError("k_pages and v_pages must have the same strides, the head's elements adjacent")
-    if block_table.dtype != torch.int32:
-        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
-    if block_table.dim() != 2 or block_table.shape[0] != B or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
-        raise ValueError(f"block_table must be [{B}, columns] with adjacent columns, got {tuple(block_table.shape)}")
-    columns = block_table.shape[1]
-    # the stride of an axis of one element says nothing
-    row = s[1] if shape[1] > 1 else HEAD_DIM
-    head = s[2] if shape[2] > 1 else HEAD_DIM
-    page = s[0] if shape[0] > 1 else HEAD_DIM
-    return _Pages(k_pages.data_ptr(), v_pages.data_ptr(), page, row, head, block_table.data_ptr(), shape[0], shape[1],
-                  shape[2], block_table.stride(0) if B > 1 else columns, columns)
-
-
-def _dense_out(out, n, heads, device, stream, name="out"):
-    if out is None:
-        with torch.cuda.stream(stream):   # memory of the stream that writes it
-            return torch.empty(n, heads, HEAD_DIM, dtype=torch.bfloat16, device=device)
-    if out.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {out.dtype}")
-    if out.device != device or out.shape != (n, heads, HEAD_DIM) or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {(n, heads, HEAD_DIM)} tensor on {device}")
-    return out
-
-
-def _paged_ws(workspace, device, stream):
-    if workspace is None:
-        with torch.cuda.stream(stream):   # cleared on the stream that uses it
-            workspace = make_paged_workspace(device)
-    elif workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous torch.uint8 tensor on {device}")
-    return workspace
-
-
-def _tokens(q, name="q"):
-    """Tokens, heads and device of packed rows [tokens, heads, 128]."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not q.is_cuda:
+    if not like.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if q.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, {HEAD_DIM}], got {tuple(q.shape)}")
-    return q.shape[0], q.shape[1], q.device
-
-
-def _enqueue(where, device, *args):
-    fn = getattr(lib(), where)
-    if device.index == torch.cuda.current_device():
-        r = fn(*args)
-    else:
-        with torch.cuda.device(device):
-            r = fn(*args)
-    if r:
-        raise GQAError(r, where)
+    with torch.cuda.device(like.device), torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+        if workspace is None:
+            workspace = make_paged_workspace(like.device)
+    return out, workspace
 
 
 def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens=None, q_out=None,
@@ -626,32 +559,13 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     n_kv, 128], page_size a power of two >= 16; block_table device int32 [B,
     columns]. Returns the rotated queries (q_out, which may be q), or None
     without q."""
-    n, n_kv, device = _tokens(k, "k")
-    k_stride, v_stride = _rows(k, "k", n, n_kv, device), _rows(v, "v", n, n_kv, device)
-    B = start_pos.shape[0] if isinstance(start_pos, torch.Tensor) and start_pos.dim() == 1 else -1
-    start = _ints(start_pos, "start_pos", B, device)
-    cu = None if cu_tokens is None else _ints(cu_tokens, "cu_tokens", B + 1, device)
-    if cu_tokens is None and B != n:
-        raise ValueError(f"without cu_tokens there is one token per sequence: {n} tokens, {B} sequences")
-    pages = _pages(k_pages, v_pages, block_table, B, device)
-    if pages.n_kv_heads != n_kv:
-        raise ValueError(f"k has {n_kv} heads, the pages {pages.n_kv_heads}")
-    _check(rope, "rope", torch.float32)
-    if rope.device != device or rope.dim() != 3 or rope.shape[1:] != (64, 2):
-        raise ValueError(f"rope must be [rows, 64, 2] on {device}")
-    heads, q_stride, q_ptr, o_ptr = 0, 0, None, None
-    if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        q_stride, q_ptr = _rows(q, "q", n, heads, device), q.data_ptr()
-        q_out = _dense_out(q_out, n, heads, device, stream, "q_out")
-        o_ptr = q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    workspace = _paged_ws(workspace, device, stream)
-    if n:
-        _enqueue("gqa_paged_append", device, q_ptr, q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, n, heads,
-                 cu, B, start, rope.data_ptr(), rope.shape[0], ctypes.addressof(pages), o_ptr, workspace.data_ptr(),
-                 workspace.numel(), _s(stream, device))
+    if workspace is None or (q_out is None and q is not None):
+        x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
+        q_out = None if q is None else x
+    r = (_paged or _binding()).paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens, q_out,
+                                            workspace, None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_append")
     return q_out
 
 
@@ -661,15 +575,12 @@ def paged_decode(q, start_pos, k_pages, v_pages, block_table, scale: float = HEA
     over cache rows 0..start_pos[b]; its own row is among them
     (``paged_append`` with the same start_pos comes first). start_pos[b] = -1:
     an unused slot, its output row is zero."""
-    B, heads, device = _tokens(q)
-    q_stride = _rows(q, "q", B, heads, device)
-    start = _ints(start_pos, "start_pos", B, device)
-    pages = _pages(k_pages, v_pages, block_table, B, device)
-    out = _dense_out(out, B, heads, device, stream)
-    workspace = _paged_ws(workspace, device, stream)
-    if B:
-        _enqueue("gqa_paged_decode", device, q.data_ptr(), q_stride, B, heads, start, ctypes.addressof(pages),
-                 float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _s(stream, device))
+    if out is None or workspace is None:
+        out, workspace = _defaults(q, "q", out, workspace, stream)
+    r = (_paged or _binding()).paged_decode(q, start_pos, k_pages, v_pages, block_table, scale, out, workspace,
+                                            None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_decode")
     return out
 
 
@@ -679,16 +590,12 @@ def paged_prefill(q, cu_tokens, start_pos, k_pages, v_pages, block_table, scale:
     the cache, which already holds them: token i of sequence b reads rows
     0..start_pos[b] + i. Arguments as in ``paged_append``; the rows of an
     unused slot (start_pos -1) are zero."""
-    n, heads, device = _tokens(q)
-    q_stride = _rows(q, "q", n, heads, device)
-    B = start_pos.shape[0] if isinstance(start_pos, torch.Tensor) and start_pos.dim() == 1 else -1
-    start, cu = _ints(start_pos, "start_pos", B, device), _ints(cu_tokens, "cu_tokens", B + 1, device)
-    pages = _pages(k_pages, v_pages, block_table, B, device)
-    out = _dense_out(out, n, heads, device, stream)
-    workspace = _paged_ws(workspace, device, stream)
-    if n:
-        _enqueue("gqa_paged_prefill", device, q.data_ptr(), q_stride, n, heads, cu, B, start, ctypes.addressof(pages),
-                 float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _s(stream, device))
+    if out is None or workspace is None:
+        out, workspace = _defaults(q, "q", out, workspace, stream)
+    r = (_paged or _binding()).paged_prefill(q, cu_tokens, start_pos, k_pages, v_pages, block_table, scale, out,
+                                             workspace, None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_prefill")
     return out
 
 
@@ -697,16 +604,10 @@ def packed_prefill(q, k, v, cu_tokens, scale: float = HEAD_DIM ** -0.5, out=None
     """Causal attention of whole packed prompts without a cache: token i of a
     sequence (q [N, heads, 128], k, v [N, n_kv, 128], rows cu_tokens[b] ..
     cu_tokens[b+1]-1) reads its tokens 0..i."""
-    n, heads, device = _tokens(q)
-    n_kv = _tokens(k, "k")[1]
-    q_stride = _rows(q, "q", n, heads, device)
-    k_stride, v_stride = _rows(k, "k", n, n_kv, device), _rows(v, "v", n, n_kv, device)
-    B = cu_tokens.shape[0] - 1 if isinstance(cu_tokens, torch.Tensor) and cu_tokens.dim() == 1 else -1
-    cu = _ints(cu_tokens, "cu_tokens", B + 1, device)
-    out = _dense_out(out, n, heads, device, stream)
-    workspace = _paged_ws(workspace, device, stream)
-    if n:
-        _enqueue("gqa_packed_prefill", device, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-                 n, heads, n_kv, cu, B, float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                 _s(stream, device))
+    if out is None or workspace is None:
+        out, workspace = _defaults(q, "q", out, workspace, stream)
+    r = (_paged or _binding()).packed_prefill(q, k, v, cu_tokens, scale, out, workspace,
+                                              None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_packed_prefill")
     return out

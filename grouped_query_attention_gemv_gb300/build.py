@@ -1,5 +1,6 @@
 """Build libgqa.so in-tree: one nvcc per CUDA translation unit (in parallel),
-then a shared-library link. Target: GB300, sm_103a only.
+then a shared-library link; and beside it the Python extension gqa_binding.so
+(host code only), linked to it. Target: GB300, sm_103a only.
 
     python -m grouped_query_attention_gemv_gb300.build [--force] [--verbose-ptxas]
 """
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB = os.path.join(OUT_DIR, "libgqa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(OUT_DIR, "gqa_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -33,6 +37,19 @@ def nvcc() -> str:
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def _torch_dir(sub: str) -> str:
+    import torch
+    return os.path.join(os.path.dirname(torch.__file__), sub)
+
+
+def _binding_cmd(obj: str):
+    import torch
+    inc = _torch_dir("include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", inc, "-I", cuda, "-c", BINDING_SRC, "-o", obj]
 
 
 def _deps():
@@ -64,6 +81,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    bobj = os.path.join(OBJ_DIR, "binding.o")
+    rebind = force or _stale(bobj, [BINDING_SRC, os.path.join(INCLUDE, "gqa.h"), os.path.abspath(__file__)])
+    if rebind:
+        jobs.insert(0, _binding_cmd(bobj))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -71,7 +93,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for cmd, r in ex.map(run, jobs):
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}:\n{r.stdout}\n{r.stderr}")
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}:\n{r.stdout}\n{r.stderr}")
             if verbose_ptxas or not quiet:
                 sys.stderr.write(r.stderr)
     if force or jobs or _stale(LIB, objs):
@@ -80,6 +102,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if rebind or _stale(BINDING, [bobj]):
+        tmp = BINDING + ".tmp"
+        r = subprocess.run(["g++", "-shared", "-o", tmp, bobj, "-L", OUT_DIR, "-l:libgqa.so", "-Wl,-rpath,$ORIGIN",
+                            "-L", _torch_dir("lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"],
+                           capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
     return LIB
 
 

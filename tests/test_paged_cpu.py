@@ -18,11 +18,19 @@ def lib():
     return G.lib()
 
 
+class Pages(ctypes.Structure):
+    """gqa_pages of include/gqa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_longlong),
+                ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("table_stride", ctypes.c_int), ("columns", ctypes.c_int)]
+
+
 def pages(**kw):
     a = dict(k=FAKE, v=FAKE, page_stride=16 * 8 * 128, row_stride=8 * 128, head_stride=128, block_table=FAKE,
              num_pages=4, page_size=16, n_kv_heads=8, table_stride=4, columns=4)
     a.update(kw)
-    p = G._Pages(**a)
+    p = Pages(**a)
     return ctypes.addressof(p), p   # the structure is kept by the caller
 
 
@@ -134,54 +142,88 @@ def test_binding_refuses_host_tensors():
         G.packed_prefill(None, bf, bf, i)
 
 
-CPU = torch.device("cpu")
-
-
-def test_binding_checks_rows():
+def good():
+    """Arguments of paged_append that only their device is wrong with."""
     x = torch.zeros(6, 12, 128, dtype=torch.bfloat16)
-    assert G._rows(x[:, :8], "q", 6, 8, CPU) == 12 * 128
-    assert G._rows(x[:1, :8], "q", 1, 8, CPU) == 8 * 128
-    for bad, err in ((x.float(), TypeError), (x[:, ::2], ValueError), (x.transpose(0, 1), ValueError),
-                     (x[..., :64], ValueError), ("x", TypeError)):
-        with pytest.raises(err):
-            G._rows(bad, "q", 6, 6, CPU)
+    kp = torch.zeros(5, 16, 2, 128, dtype=torch.bfloat16)
+    return dict(q=x[:, :8], k=x[:, 8:10], v=x[:, 10:], start_pos=torch.zeros(3, dtype=torch.int32),
+                rope=torch.zeros(80, 64, 2), k_pages=kp, v_pages=kp.clone(),
+                block_table=torch.zeros(3, 7, dtype=torch.int32), cu_tokens=torch.zeros(4, dtype=torch.int32),
+                q_out=torch.zeros(6, 8, 128, dtype=torch.bfloat16), workspace=torch.zeros(8, dtype=torch.uint8))
 
 
-def test_binding_checks_pages():
-    k = torch.zeros(5, 16, 2, 128, dtype=torch.bfloat16)
-    t = torch.zeros(3, 7, dtype=torch.int32)
-    p = G._pages(k, k, t[:, :4], 3, CPU)
-    assert (p.page_stride, p.row_stride, p.head_stride) == (16 * 256, 256, 128)
-    assert (p.num_pages, p.page_size, p.n_kv_heads, p.table_stride, p.columns) == (5, 16, 2, 7, 4)
-    h = torch.zeros(5, 2, 16, 128, dtype=torch.bfloat16).transpose(1, 2)
-    p = G._pages(h, h, t, 3, CPU)
-    assert (p.row_stride, p.head_stride) == (128, 16 * 128)
-    one = torch.zeros(1, 16, 1, 128, dtype=torch.bfloat16)
-    assert G._pages(one, one, t, 3, CPU).head_stride == 128
-    for bad in ((k, k[:4], t, 3), (k, h, t, 3), (k, k, t, 2), (k, k, t.t(), 7), (k[0], k[0], t, 3),
-                (k[..., :64], k[..., :64], t, 3)):
-        with pytest.raises(ValueError):
-            G._pages(*bad, CPU)
-    for bad in ((k.float(), k.float(), t, 3), (k, k, t.long(), 3), (k, k, None, 3)):
-        with pytest.raises(TypeError):
-            G._pages(*bad, CPU)
+def calls(a):
+    """The four entries on the arguments `a` (a name each takes)."""
+    pages = (a["k_pages"], a["v_pages"], a["block_table"])
+    one = dict(out=a["q_out"], workspace=a["workspace"])
+    return {
+        "append": lambda: G.paged_append(**a),
+        "decode": lambda: G.paged_decode(a["q"][:3] if isinstance(a["q"], torch.Tensor) else a["q"], a["start_pos"],
+                                         *pages, out=a["q_out"][:3], workspace=a["workspace"]),
+        "prefill": lambda: G.paged_prefill(a["q"], a["cu_tokens"], a["start_pos"], *pages, **one),
+        "packed": lambda: G.packed_prefill(a["q"], a["k"], a["v"], a["cu_tokens"], **one),
+    }
 
 
-def test_binding_checks_integers_and_outputs():
-    i = torch.zeros(4, dtype=torch.int32)
-    assert G._ints(i, "start_pos", 4, CPU) == i.data_ptr()
-    for bad, err in ((i.long(), TypeError), (i[:3], ValueError), (torch.zeros(8, dtype=torch.int32)[::2], ValueError),
-                     ([0] * 4, TypeError)):
-        with pytest.raises(err):
-            G._ints(bad, "start_pos", 4, CPU)
-    o = torch.zeros(4, 12, 128, dtype=torch.bfloat16)
-    assert G._dense_out(o, 4, 12, CPU, None) is o
-    with pytest.raises(ValueError):
-        G._dense_out(o[:, :8], 4, 8, CPU, None)
-    with pytest.raises(TypeError):
-        G._dense_out(o.float(), 4, 12, CPU, None)
-    with pytest.raises(ValueError):
-        G._paged_ws(torch.zeros(8), CPU, None)
+def test_binding_reaches_the_device_check():
+    for call in calls(good()).values():
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
+
+
+HND = torch.zeros(5, 2, 16, 128, dtype=torch.bfloat16).transpose(1, 2)
+ALL = ("append", "decode", "prefill", "packed")
+PAGED = ("append", "decode", "prefill")
+
+
+@pytest.mark.parametrize("name,change,error,match,who", [
+    ("q", lambda t: t.float(), TypeError, "q must be torch.bfloat16", ALL),
+    ("q", lambda t: "q", TypeError, "q must be a torch.Tensor", ALL),
+    ("q", lambda t: t[..., :64], ValueError, "q must be", ALL),
+    ("q", lambda t: t[:, ::2], ValueError, "one after the other", ALL),
+    ("q", lambda t: t[0], ValueError, "q must be", ("append", "packed", "prefill")),
+    ("q", lambda t: t.transpose(1, 2).contiguous().transpose(1, 2), ValueError, "one after the other", ALL),
+    ("q", lambda t: None, ValueError, "q_out needs q", ("append",)),
+    ("k", lambda t: t[:5], ValueError, "must be", ("append", "packed")),
+    ("k", lambda t: t[:, :1], ValueError, "must be", ("append",)),
+    ("v", lambda t: t[:, :1], ValueError, r"v must be \[6, 2, 128\]", ("append", "packed")),
+    ("v", lambda t: t.half(), TypeError, "v must be torch.bfloat16", ("append", "packed")),
+    ("start_pos", lambda t: t.long(), TypeError, "start_pos must be torch.int32", PAGED),
+    ("start_pos", lambda t: [0, 0, 0], TypeError, "start_pos must be a torch.Tensor", PAGED),
+    ("start_pos", lambda t: t[:2], ValueError, "must be", PAGED),
+    ("start_pos", lambda t: torch.zeros(6, dtype=torch.int32)[::2], ValueError, "start_pos must be", PAGED),
+    ("cu_tokens", lambda t: t[:3], ValueError, r"cu_tokens must be a contiguous \[4\]", ("append", "prefill")),
+    ("cu_tokens", lambda t: t[:1], ValueError, "cu_tokens must", ("append", "prefill", "packed")),
+    ("cu_tokens", lambda t: t.long(), TypeError, "cu_tokens must be torch.int32", ("append", "prefill", "packed")),
+    ("cu_tokens", lambda t: None, ValueError, "one value per token", ("append",)),
+    ("rope", lambda t: t.double(), TypeError, "rope must be torch.float32", ("append",)),
+    ("rope", lambda t: t[:, :32], ValueError, "rope must be", ("append",)),
+    ("k_pages", lambda t: t[0], ValueError, "k_pages must be", PAGED),
+    ("k_pages", lambda t: t.float(), TypeError, "k_pages must be torch.bfloat16", PAGED),
+    ("k_pages", lambda t: HND, ValueError, "strides of k_pages", PAGED),
+    ("v_pages", lambda t: t[:4], ValueError, "shape and the strides", PAGED),
+    ("block_table", lambda t: t.long(), TypeError, "block_table must be torch.int32", PAGED),
+    ("block_table", lambda t: t[:2], ValueError, r"block_table must be \[3, columns\]", PAGED),
+    ("block_table", lambda t: t.repeat(1, 2)[:, ::2], ValueError, "adjacent columns", PAGED),
+    ("block_table", lambda t: None, TypeError, "block_table must be a torch.Tensor", PAGED),
+    ("q_out", lambda t: t.float(), TypeError, "must be torch.bfloat16", ALL),
+    ("q_out", lambda t: t[:, :4], ValueError, "must be a contiguous", ALL),
+    ("q_out", lambda t: t.repeat(1, 1, 2)[..., ::2], ValueError, "must be a contiguous", ALL),
+    ("q_out", lambda t: t[:2], ValueError, "must be a contiguous", ALL),
+])
+def test_binding_refuses(name, change, error, match, who):
+    a = good()
+    a[name] = change(a[name])
+    for entry in who:
+        with pytest.raises(error, match=match):
+            calls(a)[entry]()
+
+
+def test_binding_is_required(monkeypatch, tmp_path):
+    monkeypatch.setattr(G, "_BINDING_PATH", str(tmp_path / "missing.so"))
+    monkeypatch.setattr(G, "_paged", None)
+    with pytest.raises(ImportError, match="gqa_binding"):
+        G._binding()
 
 
 # ------------------------------------------------------------------ work split of the decode attention
