@@ -133,8 +133,9 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
   if (r == GQA_OK) r = check_scale(scale);
   if (r != GQA_OK) return r;
   if (!valid_stride(q_stride, static_cast<int64_t>(n_heads) * HEAD_DIM)) return GQA_EINVAL;
-  // the chunks of 16 positions per KV head are counted in 31 bits over the batch
-  if (B * (p.pages.columns * static_cast<long long>(pages->page_size) / 16) > 0x7fffffffLL) return GQA_EINVAL;
+  // the batch's chunks of 16 positions and one KV head are counted in 31 bits
+  if (p.pages.columns * static_cast<long long>(pages->page_size) / 16 * B * pages->n_kv_heads > 0x7fffffffLL)
+    return GQA_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned4(start_pos)) return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -247,6 +247,25 @@ cudaError_t launch_rmsnorm(const __nv_bfloat16* x, const __nv_bfloat16* g, float
 constexpr int PAGED_MAX_SEQS = 2048;  // sequences per launch (prefix sums live in shared memory)
 constexpr int PAGED_MAX_REP = 16;     // query heads per KV head
 
+// Launch with programmatic stream serialization: the grid may be set up while
+// the previous kernel of the stream ends. Only for kernels that execute
+// pdl_wait() before they touch memory.
+template <class... P, class... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                          const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A paged cache as the kernels see it (gqa_pages with the page size as a shift).
 struct PagedCache {
   __nv_bfloat16* k;

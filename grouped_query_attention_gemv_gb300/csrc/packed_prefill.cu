@@ -229,6 +229,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(smem_u32(&bs.tmem_slot), TMEM_COLS);
     tmem_relinquish();
   }
+  // nothing in global memory is read or written before the previous kernel of
+  // the stream is done
+  pdl_trigger();
+  pdl_wait();
   // pairs of Q tiles per sequence, prefix-summed
   {
     const int per = (a.B + THREADS - 1) / THREADS;
@@ -631,8 +635,7 @@ cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPre
   const long long items = (static_cast<long long>(a.N) / (NQ * qp) + a.B) * a.n_kv;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned ctas = static_cast<unsigned>(items < a.ctas ? items : a.ctas);
-  packed_prefill_kernel<<<ctas, THREADS, SMEM_BYTES, s>>>(maps.q, maps.k, maps.v, a);
-  return cudaGetLastError();
+  return launch_behind(packed_prefill_kernel, ctas, THREADS, SMEM_BYTES, s, maps.q, maps.k, maps.v, a);
 }
 
 }  // namespace gqa

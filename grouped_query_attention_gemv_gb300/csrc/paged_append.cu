@@ -25,6 +25,9 @@ __device__ __forceinline__ uint32_t rotate(uint32_t x, float c, float s) {
 }
 
 __global__ void __launch_bounds__(WARPS * 32) paged_append_kernel(PagedAppendParams p, int groups) {
+  // nothing is read or written before the previous kernel of the stream is done
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31, half = lane >> 4, piece = lane & 15;
   const long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
   const int m = static_cast<int>(item / groups);
@@ -95,8 +98,7 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s) {
   const int groups = (p.n_heads + 2 * p.n_kv + ROWS - 1) / ROWS;
   const long long blocks = (static_cast<long long>(p.N) * groups + WARPS - 1) / WARPS;
   if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  paged_append_kernel<<<static_cast<unsigned>(blocks), WARPS * 32, 0, s>>>(p, groups);
-  return cudaGetLastError();
+  return launch_behind(paged_append_kernel, static_cast<unsigned>(blocks), WARPS * 32, 0, s, p, groups);
 }
 
 }  // namespace gqa

@@ -13,10 +13,15 @@
 //   * Each warp streams its range through its own ring of STAGES chunks with
 //     cp.async, its page ids looked up one chunk ahead; nothing but the end
 //     of the CTA synchronises warps. Rows past the sequence are filled with
-//     zeros instead of being read (they may hold anything).
+//     zeros instead of being read (they may hold anything). 64 to 128 KB are
+//     in flight per SM. More is worse: four groups of about ten SMs get 10 to
+//     15% less of a saturated memory than the others, the more so the deeper
+//     the queues, and the ranges are equal (3 stages: 182.6 us where 2 take
+//     174.7, 64 sequences of up to 8,192 rows). Fewer warps are too: the work
+//     on a chunk then shows (6: 178.7, 4: 190).
 //   * S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 (the 16 keys, then
 //     the dims, on the M side, query heads padded to 8 or 16 on the N side).
-//     The probabilities enter the product as two bf16 terms, P = hi + lo, so
+//     The probabilities enter the product as two bf16 terms (P = hi + lo), so
 //     that the output's own rounding is the only 8-bit one; the tensor pipe
 //     has the time.
 //   * A (sequence, KV head) wholly inside a warp's range is finished in
@@ -24,6 +29,14 @@
 //     shared memory among the CTA's warps, then, where several CTAs hold
 //     parts, by the CTA that arrives last at a ticket, in CTA order: the
 //     result does not depend on the order of arrival, and no CTA waits.
+//   * Joining across CTAs (fence, ticket, read back) takes 2 to 3 us, what a
+//     CTA streams about 16 chunks in. Where one CTA per (sequence, KV head)
+//     is no more than that behind the equal ranges, the ranges are those
+//     (16 sequences of 1,001 rows, 8 KV heads: 17.3 us against 22.9).
+// Measured (GB300, 6.8 TB/s copied): 172.3 us for 1.108 GB (64 sequences of
+// up to 8,192 rows), 87.5 for 537 MB (one of 131,072), 16.2 for 66 MB (16 of
+// 1,001), 3.5 for one sequence of 16 rows. Head-major pages ([page, KV head,
+// row]) are 2 to 4% faster than [page, row, KV head]: longer runs per CTA.
 #include <math.h>
 
 #include "kernels.h"
@@ -36,8 +49,9 @@ constexpr int KEYS = 16;                          // positions of a chunk
 constexpr int ROW_BYTES = HEAD_DIM * 2;
 constexpr int TILE_BYTES = KEYS * ROW_BYTES;      // K or V of a chunk
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-constexpr int STAGES = 3;
-constexpr int MAX_WARPS = 8;
+constexpr int STAGES = 2;
+constexpr int WARPS = 8;
+constexpr int OWN_CHUNKS = 16;                    // what joining across CTAs costs, in chunks of one CTA's stream
 constexpr int PART = HEAD_DIM + 2;                // floats of a partial row: o, max, sum
 
 // Row r, 16-byte piece c of a 256-byte-row tile: eight rows of one piece fall
@@ -53,8 +67,8 @@ struct Cursor {
 };
 
 // pre[b]: chunks per KV head of the sequences before b.
-__device__ __forceinline__ Cursor locate(long long u, const int* pre, int B, int n_kv) {
-  const int x = static_cast<int>(u / n_kv);  // pre[b] <= x < pre[b + 1] exactly when u lies in sequence b
+__device__ __forceinline__ Cursor locate(int u, const int* pre, int B, int n_kv) {
+  const int x = u / n_kv;  // pre[b] <= x < pre[b + 1] exactly when u lies in sequence b
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -63,7 +77,7 @@ __device__ __forceinline__ Cursor locate(long long u, const int* pre, int B, int
   Cursor c;
   c.b = lo;
   c.n = pre[lo + 1] - pre[lo];
-  const int r = static_cast<int>(u - static_cast<long long>(pre[lo]) * n_kv);
+  const int r = u - pre[lo] * n_kv;
   c.h = r / c.n;
   c.j = r - c.h * c.n;
   return c;
@@ -79,63 +93,84 @@ __device__ __forceinline__ void advance(Cursor& c, const int* pre, int B, int n_
   } while (c.n == 0);
 }
 
-__device__ __forceinline__ long long range_start(long long c, long long total, long long parts) {
-  return total * c / parts;
-}
-// The part whose range holds chunk u.
-__device__ __forceinline__ int part_of(long long u, long long total, long long parts) {
-  return static_cast<int>(((u + 1) * parts - 1) / total);
-}
-
-struct Range {
-  long long first, end;  // chunks of one (sequence, KV head)
+// `total` chunks over `parts` ranges, the first `more` of them one longer.
+struct Split {
+  int each, more;
+  __device__ __forceinline__ Split(int total, int parts) : each(total / parts), more(total - each * parts) {}
+  __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int holder(int u) const {  // the range that holds chunk u (each > 0)
+    const int x = more * (each + 1);
+    return u < x ? u / (each + 1) : more + (u - x) / each;
+  }
 };
-__device__ __forceinline__ Range segment(int id, const int* pre, int n_kv) {
-  const int b = id / n_kv, h = id - b * n_kv, n = pre[b + 1] - pre[b];
-  const long long first = static_cast<long long>(pre[b]) * n_kv + static_cast<long long>(h) * n;
-  return {first, first + n};
+
+// A part of a (sequence, KV head), left for joining: its chunks
+// [first, end) identify it, `row` is its first row of the output.
+struct Part {
+  int first, end, row;
+};
+
+// This lane's 4 dims of an output row.
+__device__ __forceinline__ void store_row(__nv_bfloat16* out, int row, float4 o, float inv) {
+  *(reinterpret_cast<uint2*>(out + static_cast<long long>(row) * HEAD_DIM) + (threadIdx.x & 31)) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
 // NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16).
 template <int NT>
-__global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDecodeParams p) {
+__global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int W = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int W = WARPS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_rep = p.n_heads / p.n_kv;
   uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
   // per warp: the partial of the part that began before its range; the one
   // that goes on behind it is put into the ring when the warp is done
   float* stash = reinterpret_cast<float*>(smem + W * (STAGES * STAGE_BYTES));
   int* pre = reinterpret_cast<int*>(stash + W * n_rep * PART);
-  __shared__ int ids[2 * MAX_WARPS];   // (sequence, KV head) of each warp's two partials, or -1
-  __shared__ int warp_sum[MAX_WARPS];
-  __shared__ int last_of[2];
+  int* last = pre + p.B + 1;  // last row of each sequence
+  __shared__ Part parts[2 * WARPS];  // each warp's two, first = -1: none
+  __shared__ int warp_sum[WARPS], warp_max[WARPS];
+  __shared__ int is_last[2];
 
+  // nothing is read or written before the previous kernel of the stream is done
+  pdl_trigger();
+  pdl_wait();
   // chunks per sequence, prefix-summed; unused slots and bad positions have none
+  int total, longest;
   {
     const int per = (p.B + blockDim.x - 1) / blockDim.x;
-    const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.B);
-    int sum = 0;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+    int sum = 0, most = 0;
     for (int b = b0; b < b1; ++b) {
       const int s = p.start[b];
       const bool ok = s >= 0 && s < p.pages.capacity();
       if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
       const int n = ok ? s / KEYS + 1 : 0;
       pre[b + 1] = n;
+      last[b] = s;
       sum += n;
+      most = max(most, n);
     }
     int run = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += x;
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
     if (lane == 31) warp_sum[warp] = run;
-    if (threadIdx.x < 2 * MAX_WARPS) ids[threadIdx.x] = -1;
+    if (lane == 0) warp_max[warp] = most;
+    if (threadIdx.x < 2 * WARPS) parts[threadIdx.x].first = -1;
     if (threadIdx.x == 0) pre[0] = 0;
     __syncthreads();
     run -= sum;
-    for (int w = 0; w < warp; ++w) run += warp_sum[w];
+    total = longest = 0;
+    for (int w = 0; w < W; ++w) {
+      if (w == warp) run += total;
+      total += warp_sum[w];
+      longest = max(longest, warp_max[w]);
+    }
     for (int b = b0; b < b1; ++b) {
       run += pre[b + 1];
       pre[b + 1] = run;
@@ -148,13 +183,27 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
       for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
         reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
 
-  const long long total = static_cast<long long>(pre[p.B]) * p.n_kv;
+  total *= p.n_kv;
+  if (total == 0) return;
   // no more CTAs than leave each warp a chunk
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (total + W - 1) / W));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long c0 = range_start(blockIdx.x, total, ctas), c1 = range_start(blockIdx.x + 1, total, ctas);
-  const long long a0 = c0 + range_start(warp, c1 - c0, W), a1 = c0 + range_start(warp + 1, c1 - c0, W);
-  const int n = static_cast<int>(a1 - a0);
+  const int ctas = min(static_cast<int>(gridDim.x), (total + W - 1) / W);
+  const Split split(total, ctas);
+  // One CTA per (sequence, KV head) instead of equal ranges where that costs
+  // less than joining parts across CTAs.
+  const bool own = p.B * p.n_kv <= static_cast<int>(gridDim.x) && longest <= split.each + OWN_CHUNKS;
+  int c0, c1;
+  if (own) {
+    if (static_cast<int>(blockIdx.x) >= p.B * p.n_kv) return;
+    const int b = blockIdx.x / p.n_kv, h = blockIdx.x - b * p.n_kv, n = pre[b + 1] - pre[b];
+    c0 = pre[b] * p.n_kv + h * n;
+    c1 = c0 + n;
+  } else {
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    c0 = split.start(blockIdx.x);
+    c1 = split.start(blockIdx.x + 1);
+  }
+  const int a0 = c0 + (c1 - c0) * warp / W, a1 = c0 + (c1 - c0) * (warp + 1) / W;
+  const int n = a1 - a0;
 
   const int gr = lane >> 2, t = lane & 3;
   const int half = lane >> 4, piece = lane & 15;
@@ -164,7 +213,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
     // element offset of row lane % 16 of the chunk at `iss`, -1 for a row past the sequence
     auto row_offset = [&]() -> long long {
       const int pos = iss.j * KEYS + piece;
-      if (pos > p.start[iss.b]) return -1;
+      if (pos > last[iss.b]) return -1;
       const int page = p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)];
       if (page < 0 || page >= p.pages.num_pages) {
         report(p.status, DEV_BAD_PAGE);
@@ -224,22 +273,24 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
       __syncwarp();
       const uint32_t kt = ring32 + (i % STAGES) * STAGE_BYTES, vt = kt + TILE_BYTES;
 
-      float sc[NT][4];
+      float sc[NT][4], sd[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = sd[nt][0] = sd[nt][1] = sd[nt][2] = sd[nt][3] = 0.f;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         uint32_t k0, k1, k2, k3;
         ldsm_x4(kt + tile_at(lane & 15, 2 * s + half), k0, k1, k2, k3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], k0, k1, k2, k3, qb[nt][s][0], qb[nt][s][1]);
+        for (int nt = 0; nt < NT; ++nt) mma16816((s & 1) ? sd[nt] : sc[nt], k0, k1, k2, k3, qb[nt][s][0], qb[nt][s][1]);
       }
       // rows gr and gr + 8 of the chunk
-      const int left = p.start[cur.b] - cur.j * KEYS;
+      const int left = last[cur.b] - cur.j * KEYS;
       uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float(&x)[4] = sc[nt];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += sd[nt][e];
         x[0] = gr <= left ? x[0] * p.scale_log2 : -INFINITY;
         x[1] = gr <= left ? x[1] * p.scale_log2 : -INFINITY;
         x[2] = gr + 8 <= left ? x[2] * p.scale_log2 : -INFINITY;
@@ -296,8 +347,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
       if (i + 1 < n && cur.j != 0) continue;
 
       // end of this warp's part of (here.b, here.h)
-      const int id = here.b * p.n_kv + here.h;
-      const Range seg = segment(id, pre, p.n_kv);
+      const int first = pre[here.b] * p.n_kv + here.h * here.n;
+      const Part seg{first, first + here.n, here.b * p.n_heads + here.h * n_rep};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -305,7 +356,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
       if (seg.first >= a0 && seg.end <= a1) {
-        __nv_bfloat16* out = p.out + (static_cast<long long>(here.b) * p.n_heads + here.h * n_rep) * HEAD_DIM;
+        __nv_bfloat16* out = p.out + static_cast<long long>(seg.row) * HEAD_DIM;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float i0 = 1.f / l_run[nt][0], i1 = 1.f / l_run[nt][1];
@@ -347,112 +398,139 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1) paged_decode_kernel(PagedDe
               row[HEAD_DIM + 1] = l_run[nt][e];
             }
           }
-        if (lane == 0) ids[2 * warp + slot] = id;
+        if (lane == 0) parts[2 * warp + slot] = seg;
       }
     }
   }
   __syncthreads();
 
-  // ---- join this CTA's parts: entries 2w, 2w + 1 of `ids` in order; equal
-  // ids follow each other. (part, query head) pairs are dealt to the warps.
+  // ---- join this CTA's parts: lane e < 2W looks at entry e; those of one
+  // (sequence, KV head) follow each other. (part, query head) pairs are dealt
+  // to the warps.
   auto part_at = [&](int e) -> const float* {
     return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
                    : stash + (e >> 1) * n_rep * PART;
   };
-  int split[2] = {-1, -1};  // ids whose parts are in other CTAs too: begun before this one, going on behind it
-  for (int e = 0, k = 0; e < 2 * W;) {
-    const int id = ids[e];
-    if (id < 0) {
-      ++e;
-      continue;
-    }
-    int f = e + 1;
-    while (f < 2 * W && (ids[f] < 0 || ids[f] == id)) ++f;
-    const Range seg = segment(id, pre, p.n_kv);
-    const bool whole = seg.first >= c0 && seg.end <= c1;
-    const int side = seg.first < c0 ? 0 : 1;
-    if (!whole) split[side] = id;
-    for (int r = 0; r < n_rep; ++r, ++k) {
-      if (k % W != warp) continue;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int g = e; g < f; ++g)
-        if (ids[g] >= 0) m = fmaxf(m, part_at(g)[r * PART + HEAD_DIM]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      for (int g = e; g < f; ++g) {
-        if (ids[g] < 0) continue;
-        const float* row = part_at(g) + r * PART;
-        const float w = ex2_approx(row[HEAD_DIM] - ref);
-        l += w * row[HEAD_DIM + 1];
-        const float2 x = *reinterpret_cast<const float2*>(row + 4 * lane);
-        const float2 y = *reinterpret_cast<const float2*>(row + 4 * lane + 2);
-        o.x += w * x.x;
-        o.y += w * x.y;
-        o.z += w * y.x;
-        o.w += w * y.y;
+  Part cross[2] = {{-1, 0, 0}, {-1, 0, 0}};  // with parts in other CTAs too: begun before this one, going on behind it
+  {
+    Part mine{-1, 0, 0};
+    if (lane < 2 * W) mine = parts[lane];
+    const unsigned peers = __match_any_sync(0xffffffffu, mine.first);
+    unsigned heads = __ballot_sync(0xffffffffu, mine.first >= 0 && __ffs(peers) - 1 == lane);
+    for (int k = 0; heads; heads &= heads - 1) {
+      const int e = __ffs(heads) - 1;
+      const unsigned members = __shfl_sync(0xffffffffu, peers, e);
+      const Part seg{__shfl_sync(0xffffffffu, mine.first, e), __shfl_sync(0xffffffffu, mine.end, e),
+                     __shfl_sync(0xffffffffu, mine.row, e)};
+      const int side = seg.first < c0 ? 0 : seg.end > c1 ? 1 : 2;  // 2: all of it is here
+      if (side == 0) cross[0] = seg;
+      if (side == 1) cross[1] = seg;
+      for (int r = 0; r < n_rep; ++r, ++k) {
+        if (k % W != warp) continue;
+        float m_e = -INFINITY, l_e = 0.f;
+        if (members >> lane & 1) {
+          const float2 ml = *reinterpret_cast<const float2*>(part_at(lane) + r * PART + HEAD_DIM);
+          m_e = ml.x;
+          l_e = ml.y;
+        }
+        float m = m_e;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float w_e = ex2_approx(m_e - (m == -INFINITY ? 0.f : m));
+        float l = w_e * l_e;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (unsigned g = members; g; g &= g - 1) {
+          const int f = __ffs(g) - 1;
+          const float w = __shfl_sync(0xffffffffu, w_e, f);
+          const float* row = part_at(f) + r * PART + 4 * lane;
+          const float2 x = *reinterpret_cast<const float2*>(row), y = *reinterpret_cast<const float2*>(row + 2);
+          o.x += w * x.x;
+          o.y += w * x.y;
+          o.z += w * y.x;
+          o.w += w * y.y;
+        }
+        if (side == 2) {
+          store_row(p.out, seg.row + r, o, 1.f / l);
+        } else {
+          const long long at = (2LL * blockIdx.x + side) * n_rep + r;
+          __stcg(reinterpret_cast<float4*>(p.part_o + at * HEAD_DIM) + lane, o);
+          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + at, make_float2(m, l));
+        }
       }
-      if (whole) {
-        const float inv = 1.f / l;
-        const int b = id / p.n_kv, h = (id - b * p.n_kv) * n_rep + r;
-        *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(b) * p.n_heads + h) * HEAD_DIM + 4 * lane) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      } else {
-        const long long at = (2LL * blockIdx.x + side) * n_rep + r;
-        __stcg(reinterpret_cast<float4*>(p.part_o + at * HEAD_DIM) + lane, o);
-        if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + at, make_float2(m, l));
-      }
     }
-    e = f;
   }
-  if (split[0] < 0 && split[1] < 0) return;
+  if (cross[0].first < 0 && cross[1].first < 0) return;
 
-  // ---- across CTAs: the ticket is the one of the CTA that holds the segment's first chunk
+  // ---- across CTAs: the ticket is that of the CTA with the first chunk
   __threadfence();
   __syncthreads();
   if (threadIdx.x < 2) {
-    const int id = split[threadIdx.x];
-    int last = 0;
-    if (id >= 0) {
-      const Range seg = segment(id, pre, p.n_kv);
-      const int first = part_of(seg.first, total, ctas), end = part_of(seg.end - 1, total, ctas);
+    const Part seg = threadIdx.x ? cross[1] : cross[0];
+    int mine = 0;
+    if (seg.first >= 0) {
+      const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
       __threadfence();
-      last = atomicAdd(p.tickets + first, 1) == end - first;
-      if (last) p.tickets[first] = 0;
+      mine = atomicAdd(p.tickets + a, 1) == z - a;
+      if (mine) p.tickets[a] = 0;
       __threadfence();
     }
-    last_of[threadIdx.x] = last;
+    is_last[threadIdx.x] = mine;
   }
   __syncthreads();
+  // per query head `ways` warps share the partials, then the first of them adds up
+  const int ways = max(1, W / n_rep);
   for (int side = 0; side < 2; ++side) {
-    if (!last_of[side]) continue;
-    const int id = split[side];
-    const Range seg = segment(id, pre, p.n_kv);
-    const int first = part_of(seg.first, total, ctas), end = part_of(seg.end - 1, total, ctas);
-    // the part of its first CTA goes on behind that CTA (slot 1), the others began before theirs (slot 0)
-    for (int r = warp; r < n_rep; r += W) {
-      auto at = [&](int c) { return (2LL * c + (c == first)) * n_rep + r; };
-      float m = -INFINITY;
-      for (int c = first + lane; c <= end; c += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c)).x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
+    if (!is_last[side]) continue;
+    const Part seg = cross[side];
+    const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
+    for (int r0 = 0; r0 < n_rep; r0 += W / ways) {
+      const int r = r0 + warp / ways, way = warp % ways;
+      const bool on = warp / ways < W / ways && r < n_rep;
+      float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int c = first; c <= end; ++c) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c));
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(c) * HEAD_DIM) + lane);
-        const float w = ex2_approx(ml.x - ref);
-        l += w * ml.y;
-        o.x += w * x.x;
-        o.y += w * x.y;
-        o.z += w * x.z;
-        o.w += w * x.w;
+      if (on) {
+        // the part of its first CTA goes on behind that CTA (slot 1), the others began before theirs (slot 0)
+        auto at = [&](int c) { return (2LL * c + (c == a)) * n_rep + r; };
+        for (int c = a + lane; c <= z; c += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c)).x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+        for (int c = a + way; c <= z; c += ways) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c));
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(c) * HEAD_DIM) + lane);
+          const float w = ex2_approx(ml.x - ref);
+          l += w * ml.y;
+          o.x += w * x.x;
+          o.y += w * x.y;
+          o.z += w * x.z;
+          o.w += w * x.w;
+        }
       }
-      const float inv = 1.f / l;
-      const int b = id / p.n_kv, h = (id - b * p.n_kv) * n_rep + r;
-      *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(b) * p.n_heads + h) * HEAD_DIM + 4 * lane) =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      if (ways > 1) {
+        float* mine = reinterpret_cast<float*>(smem) + warp * PART;
+        __syncthreads();
+        if (on && way) {
+          *reinterpret_cast<float2*>(mine + 4 * lane) = make_float2(o.x, o.y);
+          *reinterpret_cast<float2*>(mine + 4 * lane + 2) = make_float2(o.z, o.w);
+          if (lane == 0) mine[HEAD_DIM] = l;
+        }
+        __syncthreads();
+        if (on && !way)
+          for (int g = 1; g < ways; ++g) {
+            const float* row = mine + g * PART;
+            l += row[HEAD_DIM];
+            const float2 x = *reinterpret_cast<const float2*>(row + 4 * lane);
+            const float2 y = *reinterpret_cast<const float2*>(row + 4 * lane + 2);
+            o.x += x.x;
+            o.y += x.y;
+            o.z += y.x;
+            o.w += y.y;
+          }
+      }
+      if (on && !way) store_row(p.out, seg.row + r, o, 1.f / l);
     }
   }
 }
@@ -465,16 +543,13 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
+    e = cudaFuncSetAttribute(paged_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int n_rep = p.n_heads / p.n_kv;
-  // more than 4 query heads a KV head: the partials' share of shared memory leaves room for 6 rings
-  const int warps = n_rep <= 4 ? MAX_WARPS : 6;
-  const size_t smem = static_cast<size_t>(warps) * (STAGES * STAGE_BYTES + n_rep * PART * 4) + (p.B + 1) * 4;
-  paged_decode_kernel<NT><<<p.ctas, warps * 32, smem, s>>>(p);
-  return cudaGetLastError();
+  const size_t smem = static_cast<size_t>(WARPS) * (STAGES * STAGE_BYTES + n_rep * PART * 4) + (2 * p.B + 1) * 4;
+  return launch_behind(paged_decode_kernel<NT>, static_cast<unsigned>(p.ctas), WARPS * 32, smem, s, p);
 }
 
 }  // namespace

@@ -102,8 +102,8 @@ def test_decode_refuses(lib, kw, code):
 
 
 def test_decode_refuses_more_chunks_than_it_can_count(lib):
-    p = pages(columns=1 << 25, table_stride=1 << 25, page_size=32)
-    assert decode(lib, p, B=2048) == -1
+    p = pages(columns=1 << 21, table_stride=1 << 21)
+    assert decode(lib, p, B=128) == -1
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -228,12 +228,18 @@ def test_binding_is_required(monkeypatch, tmp_path):
 
 # ------------------------------------------------------------------ work split of the decode attention
 
-def range_start(c, total, parts):
-    return total * c // parts
+class Split:
+    """`total` chunks over `parts` ranges, the first `more` of them one longer."""
 
+    def __init__(self, total, parts):
+        self.each, self.more = divmod(total, parts)
 
-def part_of(u, total, parts):
-    return ((u + 1) * parts - 1) // total
+    def start(self, c):
+        return c * self.each + min(c, self.more)
+
+    def holder(self, u):
+        x = self.more * (self.each + 1)
+        return u // (self.each + 1) if u < x else self.more + (u - x) // self.each
 
 
 @pytest.mark.parametrize("lens", [[1], [16], [17], [1000] * 16, [131072], [0, 5, 0, 300, 1], list(range(70)), [1] * 2000])
@@ -247,6 +253,7 @@ def test_decode_ranges_cover_every_chunk_once_and_tickets_count(lens, n_kv, warp
     total = sum(chunks) * n_kv
     ctas = min(152, -(-total // warps))
     assert total >= ctas
+    split = Split(total, ctas)
     seg_ends, at = [], 0
     for n in chunks:
         for _ in range(n_kv if n else 0):
@@ -255,17 +262,17 @@ def test_decode_ranges_cover_every_chunk_once_and_tickets_count(lens, n_kv, warp
     assert at == total
     slots, tickets, covered, k = {}, {}, 0, 0
     for c in range(ctas):
-        c0, c1 = range_start(c, total, ctas), range_start(c + 1, total, ctas)
+        c0, c1 = split.start(c), split.start(c + 1)
         assert c1 > c0 == covered
         covered = c1
         w0 = c0
         for w in range(warps):
-            a0, a1 = c0 + range_start(w, c1 - c0, warps), c0 + range_start(w + 1, c1 - c0, warps)
-            assert a0 == w0 and a1 >= a0
+            a0, a1 = c0 + (c1 - c0) * w // warps, c0 + (c1 - c0) * (w + 1) // warps
+            assert a1 >= a0 == w0
             w0 = a1
         assert w0 == c1
         for u in (c0, c1 - 1):
-            assert part_of(u, total, ctas) == c
+            assert split.holder(u) == c
         while seg_ends[k][1] <= c0:
             k += 1
         j = k
@@ -275,7 +282,7 @@ def test_decode_ranges_cover_every_chunk_once_and_tickets_count(lens, n_kv, warp
                 side = 0 if first < c0 else 1
                 assert (c, side) not in slots
                 slots[c, side] = j
-                lo, hi = part_of(first, total, ctas), part_of(end - 1, total, ctas)
+                lo, hi = split.holder(first), split.holder(end - 1)
                 assert side == (1 if c == lo else 0)
                 tickets.setdefault(lo, []).append((j, hi - lo + 1))
             j += 1
