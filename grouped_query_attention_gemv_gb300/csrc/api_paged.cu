@@ -8,10 +8,16 @@ using namespace gqa;
 
 namespace {
 
-// Workspace: the status word and its 256 bytes, the decode attention's
-// tickets, its partials (two per CTA).
+// Workspace: the status word and its 256 bytes (the prefill attention's claims
+// among them), the tickets, the partials (two per CTA) of the decode or of the
+// prefill attention.
+constexpr size_t CLAIMS_OFFSET = 64;
 constexpr size_t TICKETS_OFFSET = 256;
+constexpr size_t PREFILL_ROWS = 256;  // query rows of an item
+constexpr size_t PREFILL_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * 2 * 4;
+constexpr size_t PREFILL_O_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * HEAD_DIM * 4;
 constexpr size_t PART_ML_OFFSET = TICKETS_OFFSET + 1024;
+static_assert(PART_ML_OFFSET + PREFILL_ML_BYTES + PREFILL_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 constexpr size_t PART_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * 2 * 4;
 constexpr size_t PART_O_OFFSET = (PART_ML_OFFSET + PART_ML_BYTES + 255) / 256 * 256;
 constexpr size_t PART_O_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * HEAD_DIM * 4;
@@ -181,7 +187,12 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   p.q_stride = q_stride;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = bf(out);
-  p.status = static_cast<int*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.status = reinterpret_cast<int*>(ws);
+  p.claims = reinterpret_cast<int*>(ws + CLAIMS_OFFSET);
+  p.tickets = reinterpret_cast<int*>(ws + TICKETS_OFFSET);
+  p.part_ml = reinterpret_cast<float*>(ws + PART_ML_OFFSET);
+  p.part_o = reinterpret_cast<float*>(ws + PART_ML_OFFSET + PREFILL_ML_BYTES);
   p.ctas = launch_sms();
   const int n_rep = n_heads / n_kv;
   PackedPrefillMaps maps;

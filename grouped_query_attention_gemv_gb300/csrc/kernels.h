@@ -338,6 +338,11 @@ struct PackedPrefillParams {
   long long q_stride;
   float scale_log2;
   __nv_bfloat16* out;       // [N][n_heads][128]
+  // parts of items that several CTAs share: [2 * ctas][256 rows][128], their
+  // (max in log2 units, sum), a ticket per CTA; the claims of whole items and
+  // the count of CTAs that are done. Tickets and claims zero-filled, left so.
+  float *part_o, *part_ml;
+  int *tickets, *claims;
   int* status;
   int ctas;
 };

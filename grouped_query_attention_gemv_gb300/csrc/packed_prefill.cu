@@ -46,26 +46,54 @@ constexpr int KV_TILE = 2 * KV_HALF;
 constexpr int K_OFF = NQ * Q_TILE;
 constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
 constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
-constexpr int PRE_OFF = BAR_OFF + 512;
+constexpr int MAX_SORT = 320;             // entries that are sorted, or cut into equal ranges
+constexpr int BARS_BYTES = 5120;
+constexpr int DIRECT = 2;                 // other parts of an item that are added in its epilogue at most
+constexpr int PRE_OFF = BAR_OFF + BARS_BYTES;
 constexpr int SMEM_BYTES = PRE_OFF + (PAGED_MAX_SEQS + 1) * 4 + 1024;
 constexpr int THREADS = 352;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
+constexpr int SLOTS = 2;                  // items handed from the producer to the other warps
+constexpr int JOIN_TILES = 6;             // what joining the parts of an item costs, in key tiles of one CTA
+constexpr int MIN_TILES = 6;              // key tiles of a part at least
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TILE_COLS = 256;       // TMEM columns of one Q tile
 constexpr uint32_t O_COL = 128;
 constexpr float RESCALE_LOG2 = 8.f;
+
+// What a CTA works on at a time: 2 Q tiles (NQ x qp query positions) of one
+// KV head g of sequence b, and n of the key tiles they see, from tile j0 on.
+struct Item {
+  int g, b, q0, row0, T;
+  int start, kv_end;  // cached rows before the sequence's tokens; keys behind kv_end are not the item's
+  int j0, n;          // key tiles [j0, j0 + n); n = 0: the rows are zero
+  int nt[NQ];         // of those, the tiles of each Q tile (0: none, or the tile is past T)
+  int first, last;    // the CTAs with a part of the same Q tiles (first = last: all of it is here)
+};
 
 struct Bars {
   uint64_t q_full;
   uint64_t kv_full[STAGES], kv_empty[STAGES];  // stage j of an item: K_j and V_{j-1}
   uint64_t s_full[NQ][2], p_full[NQ][2];
   uint64_t o_done[NQ], mma_done[NQ];
+  uint64_t item_full[SLOTS], item_empty[SLOTS], joint;
   uint32_t tmem_slot;
   int abort;
   int q_issued, kv_issued;
   int warp_sum[THREADS / 32];
+  int is_last;                // of an item's parts, this CTA's is the last
+  int left;                   // bits: the first / the last shared item of this CTA is left to join from memory
+  Item item[SLOTS];           // g < 0: no more
+  int cum[MAX_SORT + 1];      // key tiles before entry e, if there are at most MAX_SORT entries
+  union {
+    short order[MAX_SORT];    // entries, longest first
+    struct {
+      float row_m[NQ * ROWS], row_inv[NQ * ROWS];  // joining: a row's max and 1 / sum
+      int row_bad[NQ * ROWS];
+    };
+  };
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= BARS_BYTES, "barrier block");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool aborted(const Bars& bs) { return *reinterpret_cast<const volatile int*>(&bs.abort) != 0; }
@@ -79,25 +107,16 @@ __device__ __forceinline__ Seq seq_at(const PackedPrefillParams& a, int b) {
   return {r, r >= 0 && e > r ? e - r : 0};
 }
 
-// One work item: 2 Q tiles (NQ x qp query positions) of one KV head g of
-// sequence b, and the key tiles they see.
-struct Item {
-  int g, b, q0, row0, T;
-  int start, kv_end;  // cached rows before the sequence's tokens; keys behind kv_end are not the item's
-  int n;              // key tiles of the item (the longer of its Q tiles); 0: the rows are zero
-  int nt[NQ];         // key tiles of each Q tile (0: the tile is past T)
-};
-
-// Items in the order of the sequences, the last pair of Q tiles of each first.
-__device__ __forceinline__ Item item_at(int idx, const int* pre, int qp, const PackedPrefillParams& a) {
-  const int e = idx / a.n_kv;
+// Entry e: the pairs of Q tiles of the sequences in order, the last pair of
+// each sequence first.
+__device__ __forceinline__ Item entry_at(int e, const int* pre, int qp, const PackedPrefillParams& a) {
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pre[mid] <= e) lo = mid; else hi = mid;
   }
   Item it;
-  it.g = idx - e * a.n_kv;
+  it.g = 0;
   it.b = lo;
   const Seq s = seq_at(a, lo);
   it.row0 = s.row0;
@@ -105,7 +124,7 @@ __device__ __forceinline__ Item item_at(int idx, const int* pre, int qp, const P
   it.q0 = (pre[lo + 1] - 1 - e) * NQ * qp;
   it.start = a.start ? a.start[lo] : 0;
   const bool ok = it.start >= 0 && (!a.start || it.start + static_cast<long long>(s.T) <= a.pages.capacity());
-  it.n = 0;
+  it.j0 = it.n = it.first = it.last = 0;
 #pragma unroll
   for (int t = 0; t < NQ; ++t) {
     const int qt = it.q0 + t * qp;
@@ -116,48 +135,84 @@ __device__ __forceinline__ Item item_at(int idx, const int* pre, int qp, const P
   return it;
 }
 
-// The items of this CTA in order: round k takes item k * G + c on even rounds
-// and k * G + G - 1 - c on odd ones (G CTAs, c = blockIdx.x).
-struct ItemWalk {
-  int k, nitems, qp;
-  const int* pre;
-  __device__ __forceinline__ ItemWalk(const PackedPrefillParams& a, const int* pre, int qp)
-      : k(0), nitems(pre[a.B] * a.n_kv), qp(qp), pre(pre) {}
-  __device__ __forceinline__ bool next(const PackedPrefillParams& a, Item& it) {
-    const int G = gridDim.x, c = blockIdx.x;
-    for (; k * G < nitems; ++k) {
-      const int idx = k * G + ((k & 1) ? G - 1 - c : c);
-      if (idx >= nitems) continue;
-      it = item_at(idx, pre, qp, a);
-      ++k;
-      return true;
-    }
-    return false;
+// `total` units over `parts` ranges, the first `more` of them one longer.
+struct Split {
+  int each, more;
+  __device__ __forceinline__ Split(int total, int parts) : each(total / parts), more(total - each * parts) {}
+  __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int holder(int u) const {  // the range that holds unit u (each > 0)
+    const int x = more * (each + 1);
+    return u < x ? u / (each + 1) : more + (u - x) / each;
   }
 };
 
-// Element offset of key (value) row `key` of the item's sequence and KV head
+// Equal ranges: the key tiles in (entry, KV head, key tile) order are the
+// units, cum[e] x n_kv of them before entry e. The item with unit u, from u on
+// as far as the range that ends at `end` goes.
+__device__ __forceinline__ Item ranged_item(int u, int end, const Split& split, int E, const int* cum, const int* pre,
+                                            int qp, const PackedPrefillParams& a) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] * a.n_kv <= u) lo = mid; else hi = mid;
+  }
+  const int n = cum[lo + 1] - cum[lo], x = u - cum[lo] * a.n_kv;
+  Item it = entry_at(lo, pre, qp, a);
+  it.g = x / n;
+  it.j0 = x - it.g * n;
+  const int base = u - it.j0;  // the item's first unit
+  const int j1 = min(n, end - base);
+  it.first = split.holder(base);
+  it.last = split.holder(base + n - 1);
+  it.n = j1 - it.j0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) it.nt[t] = max(0, min(it.nt[t], j1) - it.j0);
+  return it;
+}
+
+// The items of this CTA in order, as the other warps take them from the
+// producer's slots.
+struct ItemWalk {
+  int k = 0;
+  bool ok = true;
+  __device__ __forceinline__ bool next(Bars& bs, Item& it) {
+    const int s = k % SLOTS;
+    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.item_full[s]), (k / SLOTS) & 1));
+    if (!ok) return false;
+    it = bs.item[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bs.item_empty[s]));
+    ++k;
+    return it.g >= 0;
+  }
+};
+
+// Element offset of key (value) row `key` of sequence b and KV head g
 // (a table entry out of range, reported by the producer, reads page 0).
-__device__ __forceinline__ long long key_row(const PackedPrefillParams& a, const Item& it, int key, bool value) {
+__device__ __forceinline__ long long key_row(const PackedPrefillParams& a, int b, int row0, int g, int key, bool value) {
   if (!a.start)
-    return (static_cast<long long>(it.row0) + key) * (value ? a.v_row_stride : a.pages.row_stride) +
-           it.g * a.pages.head_stride;
-  const int page = a.pages.table[static_cast<long long>(it.b) * a.pages.table_stride + (key >> a.pages.page_shift)];
+    return (static_cast<long long>(row0) + key) * (value ? a.v_row_stride : a.pages.row_stride) +
+           g * a.pages.head_stride;
+  const int page = a.pages.table[static_cast<long long>(b) * a.pages.table_stride + (key >> a.pages.page_shift)];
   return (page < 0 || page >= a.pages.num_pages ? 0 : page) * a.pages.page_stride +
-         (key & ((1 << a.pages.page_shift) - 1)) * a.pages.row_stride + it.g * a.pages.head_stride;
+         (key & ((1 << a.pages.page_shift) - 1)) * a.pages.row_stride + g * a.pages.head_stride;
 }
 
 // One output row from its visible keys 0..lim alone, by a whole warp, in
 // fp32: 32 keys at a time, a key a lane for the scores, 4 dims a lane for the
 // values. For rows that share a tile with non-finite values they do not see.
-__device__ __noinline__ void masked_row(const PackedPrefillParams& a, const Item& it, const __nv_bfloat16* q, int lim,
-                                        __nv_bfloat16* dst) {
+__device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int row0, int g, int start, int pos,
+                                        int head) {
+  const size_t row = static_cast<size_t>(row0) + pos;
+  const __nv_bfloat16* q = a.q + static_cast<long long>(row) * a.q_stride + head * HEAD_DIM;
+  __nv_bfloat16* dst = a.out + (row * a.n_heads + head) * HEAD_DIM;
+  const int lim = start + pos;
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 <= lim; j0 += 32) {
     float s = -INFINITY;
     if (j0 + lane <= lim) {
-      const uint4* k4 = reinterpret_cast<const uint4*>(a.pages.k + key_row(a, it, j0 + lane, false));
+      const uint4* k4 = reinterpret_cast<const uint4*>(a.pages.k + key_row(a, b, row0, g, j0 + lane, false));
       const uint4* q4 = reinterpret_cast<const uint4*>(q);
       float x = 0.f;
 #pragma unroll 2
@@ -184,7 +239,7 @@ __device__ __noinline__ void masked_row(const PackedPrefillParams& a, const Item
     for (int e = 0; e < 4; ++e) o[e] *= al;
     for (int j = j0; j <= min(lim, j0 + 31); ++j) {
       const float w = __shfl_sync(0xffffffffu, pr, j - j0);
-      const uint2 v = *(reinterpret_cast<const uint2*>(a.pages.v + key_row(a, it, j, true)) + lane);
+      const uint2 v = *(reinterpret_cast<const uint2*>(a.pages.v + key_row(a, b, row0, g, j, true)) + lane);
       o[0] += w * bf16_lo(v.x);
       o[1] += w * bf16_hi(v.x);
       o[2] += w * bf16_lo(v.y);
@@ -193,6 +248,112 @@ __device__ __noinline__ void masked_row(const PackedPrefillParams& a, const Item
   }
   const float inv = 1.f / l;
   *(reinterpret_cast<uint2*>(dst) + lane) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+}
+
+// Barrier of the softmax warps, the n-th of a CTA; false when it gave up.
+__device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bs.joint));
+  return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.joint), n++ & 1));
+}
+
+// Parts of an item that several CTAs share: slot 2 c + 1 for the CTA with the
+// item's first key tile (slot 2 c may hold its part of the item before), 2 c
+// otherwise. A part is the fp32 O, [32 column groups][256 rows][4], and
+// [256 rows] (max in log2 units, sum).
+__device__ __forceinline__ size_t part_slot(int c, int first) { return 2 * static_cast<size_t>(c) + (c == first); }
+__device__ __forceinline__ float2* part_ml(const PackedPrefillParams& a, size_t slot) {
+  return reinterpret_cast<float2*>(a.part_ml) + slot * NQ * ROWS;
+}
+__device__ __forceinline__ float4* part_o(const PackedPrefillParams& a, size_t slot) {
+  return reinterpret_cast<float4*>(a.part_o) + slot * NQ * ROWS * (HEAD_DIM / 4);
+}
+
+// BLOCK column groups of one row of an item from its parts in memory.
+template <int BLOCK>
+__device__ __forceinline__ bool join_block(const PackedPrefillParams& a, const Item& it, int row, int c4, float m,
+                                           float inv, __nv_bfloat16* dst) {
+  float4 o[BLOCK];
+#pragma unroll
+  for (int e = 0; e < BLOCK; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = it.first; c <= it.last; ++c) {
+    const size_t slot = part_slot(c, it.first);
+    const float w = ex2_approx(__ldcg(part_ml(a, slot) + row).x - m);
+    float4 x[BLOCK];
+#pragma unroll
+    for (int e = 0; e < BLOCK; ++e) x[e] = __ldcg(part_o(a, slot) + (c4 + e) * NQ * ROWS + row);
+#pragma unroll
+    for (int e = 0; e < BLOCK; ++e) {
+      o[e].x += w * x[e].x;
+      o[e].y += w * x[e].y;
+      o[e].z += w * x[e].z;
+      o[e].w += w * x[e].w;
+    }
+  }
+  float chk = 0.f;  // NaN when a value is not finite
+#pragma unroll
+  for (int e = 0; e < BLOCK; ++e) {
+    chk += o[e].x * 0.f + o[e].y * 0.f + o[e].z * 0.f + o[e].w * 0.f;
+    *(reinterpret_cast<uint2*>(dst) + c4 + e) =
+        make_uint2(pack_bf16(o[e].x * inv, o[e].y * inv), pack_bf16(o[e].z * inv, o[e].w * inv));
+  }
+  return chk == chk;
+}
+
+// Joins all parts of an item from memory. Run by the whole CTA at its end.
+__device__ __forceinline__ void join(const PackedPrefillParams& a, Bars& bs, const Item& it, int qp, int nrep) {
+  const int tid = threadIdx.x;
+  // the real rows of a Q tile are its first
+  int rows[NQ];
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) rows[t] = max(0, min(qp, it.T - it.q0 - t * qp)) * nrep;
+  const int total = rows[0] + rows[1];
+  if (tid < NQ * ROWS) {
+    const bool real = (tid & (ROWS - 1)) < rows[tid / ROWS];
+    float m = -INFINITY, l = 0.f;
+    if (real) {
+#pragma unroll 8
+      for (int c = it.first; c <= it.last; ++c) m = fmaxf(m, __ldcg(part_ml(a, part_slot(c, it.first)) + tid).x);
+      if (m == -INFINITY) m = 0.f;
+#pragma unroll 8
+      for (int c = it.first; c <= it.last; ++c) {
+        const float2 ml = __ldcg(part_ml(a, part_slot(c, it.first)) + tid);
+        l += ex2_approx(ml.x - m) * ml.y;
+      }
+    }
+    bs.row_m[tid] = m;
+    bs.row_inv[tid] = 1.f / l;
+    bs.row_bad[tid] = 0;
+  }
+  __syncthreads();
+  auto place = [&](int r, int& row, int& pos, int& head) {  // the r-th real row
+    const int t = r >= rows[0];
+    r -= t ? rows[0] : 0;
+    row = t * ROWS + r;
+    const int rp = r / nrep;
+    pos = it.q0 + t * qp + rp;
+    head = it.g * nrep + r - rp * nrep;
+  };
+  // (column block, row) pairs, rows fastest; narrow blocks where rows are few
+  const int width = total >= 64 ? 8 : 2;
+#pragma unroll 1
+  for (int i = tid; i < total * (HEAD_DIM / 4 / width); i += THREADS) {
+    const int blk = i / total;
+    int row, pos, head;
+    place(i - blk * total, row, pos, head);
+    __nv_bfloat16* dst = a.out + ((static_cast<size_t>(it.row0) + pos) * a.n_heads + head) * HEAD_DIM;
+    const bool fine = width == 8 ? join_block<8>(a, it, row, blk * 8, bs.row_m[row], bs.row_inv[row], dst)
+                                 : join_block<2>(a, it, row, blk * 2, bs.row_m[row], bs.row_inv[row], dst);
+    if (!fine) bs.row_bad[row] = 1;
+  }
+  __syncthreads();
+  for (int r = tid >> 5; r < total; r += THREADS / 32) {
+    int row, pos, head;
+    place(r, row, pos, head);
+    if (bs.row_bad[row] && it.start + pos < it.kv_end - 1) masked_row(a, it.b, it.row0, it.g, it.start, pos, head);
+  }
+  __syncthreads();  // the rows' figures are free again
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -220,7 +381,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&bs.o_done[t]), 1);
       mbar_init(smem_u32(&bs.mma_done[t]), 1);
     }
+    mbar_init(smem_u32(&bs.joint), 8);
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(smem_u32(&bs.item_full[s]), 1);
+      mbar_init(smem_u32(&bs.item_empty[s]), 10);  // issuers, softmax warps
+    }
     bs.abort = 0;
+    bs.left = 0;
     bs.q_issued = 0;
     bs.kv_issued = 0;
     fence_barrier_init();
@@ -264,15 +431,114 @@ __global__ void __launch_bounds__(THREADS, 1)
       pre[b + 1] = run;
     }
   }
+  __syncthreads();
+  // ---- the plan. E entries x n_kv KV heads are the items. Few entries: their
+  // key tiles are prefix-summed and sorted by length.
+  const int E = pre[a.B], G = gridDim.x;
+  const long long nitems = static_cast<long long>(E) * a.n_kv;
+  bool equal = false;  // equal ranges of key tiles instead of whole items
+  int units = 0, parts = 1;
+  if (E <= MAX_SORT) {
+    const int e = threadIdx.x;
+    const int n = e < E ? entry_at(e, pre, qp, a).n : 0;
+    if (e < E) bs.cum[e + 1] = n;
+    if (e == 0) bs.cum[0] = 0;
+    __syncthreads();
+    int before = 0, rank = 0;
+    if (e < E)
+      for (int f = 0; f < E; ++f) {
+        const int m = bs.cum[f + 1];
+        before += f <= e ? m : 0;
+        rank += m > n || (m == n && f < e);
+      }
+    __syncthreads();
+    if (e < E) {
+      bs.order[rank] = static_cast<short>(e);
+      bs.cum[e + 1] = before;
+    }
+    __syncthreads();
+    units = bs.cum[E] * a.n_kv;
+    // the load of CTA `threadIdx.x` if whole items went round in turn, longest first
+    long long load = 0;
+    if (static_cast<int>(threadIdx.x) < G)
+      for (int k = 0; k * G < nitems; ++k) {
+        const int i = k * G + ((k & 1) ? G - 1 - static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x));
+        if (i < nitems) {
+          const int o = bs.order[i / a.n_kv];
+          load += bs.cum[o + 1] - bs.cum[o];
+        }
+      }
+    const bool mine = load > units / G + JOIN_TILES + 1;
+    equal = __syncthreads_or(mine) && units >= 2 * MIN_TILES;
+    if (equal) parts = min(G, units / MIN_TILES);
+  }
+  const bool claim = !equal && nitems > G;  // items are claimed as CTAs get to them
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bs.tmem_slot;
   const uint32_t sbase = smem_u32(smem);
-  ItemWalk walk(a, pre, qp);
+  ItemWalk walk;
   Item it;
 
   if (warp == PRODUCER_WARP) {
+    // ---- which item comes next. Asked for when the last copies of the one
+    // before have been issued: whole items go to the CTAs that are free first.
+    const Split split(units, parts);
+    const bool ranged = equal && static_cast<int>(blockIdx.x) < parts;
+    int ru = ranged ? split.start(blockIdx.x) : 0;
+    const int rend = ranged ? split.start(blockIdx.x + 1) : 0;
+    int ze = 0, zg = -1;          // equal ranges: the next entry without keys
+    long long wi = blockIdx.x;    // whole items: the next one
+    bool asked = false;
+    auto next_item = [&](Item& it) {
+      if (!equal) {
+        if (asked) {
+          if (!claim) return false;
+          int c = 0;
+          if (lane == 0) c = atomicAdd(a.claims, 1);
+          wi = static_cast<long long>(G) + __shfl_sync(0xffffffffu, c, 0);
+        }
+        asked = true;
+        if (wi >= nitems) return false;
+        const int e = static_cast<int>(wi / a.n_kv);
+        it = entry_at(E <= MAX_SORT ? bs.order[e] : e, pre, qp, a);
+        it.g = static_cast<int>(wi - static_cast<long long>(e) * a.n_kv);
+        return true;
+      }
+      // units in (entry, KV head, key tile) order; this CTA's range of them
+      if (ru < rend) {
+        it = ranged_item(ru, rend, split, E, bs.cum, pre, qp, a);
+        ru += it.n;
+        return true;
+      }
+      // entries without keys (unused slots), whose rows are zero
+      for (;;) {
+        if (zg >= 0 && zg < a.n_kv) {
+          it = entry_at(ze, pre, qp, a);
+          it.g = zg;
+          zg += G;
+          return true;
+        }
+        if (zg >= 0) ++ze;
+        while (ze < E && bs.cum[ze + 1] != bs.cum[ze]) ++ze;
+        if (ze >= E) return false;
+        zg = (static_cast<int>(blockIdx.x) + ze) % G;
+      }
+    };
+    int puts = 0;
+    auto put = [&](const Item& x) {
+      const int s = puts % SLOTS;
+      if (puts >= SLOTS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.item_empty[s]), (puts / SLOTS - 1) & 1)))
+        return false;
+      if (lane == 0) {
+        bs.item[s] = x;
+        mbar_arrive(smem_u32(&bs.item_full[s]));
+      }
+      __syncwarp();
+      ++puts;
+      return true;
+    };
     if (lane == 0) {
       tma_prefetch_desc(&mq);
       tma_prefetch_desc(&mk);
@@ -290,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true, stop = false;
     int row_k = 0, page_k = 0, row_v = 0, page_v = 0;  // coordinates of this lane's box of K_j, V_{j-1}
     auto locate = [&](const Item& it, int j) {
-      const int key = j * KT + lane * box;
+      const int key = (it.j0 + j) * KT + lane * box;
       if (lane >= boxes || key >= it.kv_end) return;
       if (!a.start) {
         row_k = it.row0 + key;
@@ -304,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     };
     // boxes of key tile j that hold keys of the item
-    auto held = [&](const Item& it, int j) { return min(boxes, (it.kv_end - j * KT + box - 1) / box); };
+    auto held = [&](const Item& it, int j) { return min(boxes, (it.kv_end - (it.j0 + j) * KT + box - 1) / box); };
     // copies of stage j; false when a wait gave up or the kernel is aborting
     auto load_stage = [&](const Item& it, int j) -> bool {
       const int u = u0 + j, s = u % STAGES;
@@ -332,7 +598,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       kvn = u + 1;
       return true;
     };
-    for (int ii = 0; !stop && walk.next(a, it);) {
+    for (int ii = 0; !stop && next_item(it);) {
+      if (!put(it)) {
+        ok = false;
+        break;
+      }
       if (it.n == 0) continue;
       // after the first item, the item's first stages go out before its Q
       // tiles: their ring slots free up while the previous item's last
@@ -368,12 +638,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int t = 0; t < NQ; ++t) cs[t] += it.nt[t];
     }
+    if (ok && !stop) {
+      it.g = -1;
+      ok = put(it);
+    }
     if (lane == 0) {
       if (!ok) atomicExch(&bs.abort, 1);
       bs.q_issued = qn;
       bs.kv_issued = kvn;
     }
-  } else if (warp >= MMA_WARP) {
+  } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
     // issuer of Q tile t (the whole warp runs the loop; one elected lane
     // issues): waits on every K/V stage so that its arrivals on the empty
     // barriers stay in step with the other issuer's; a stage past this
@@ -386,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t base = tmem + t * TILE_COLS;
     unsigned u0 = 0, cs = 0;
     bool ok = true;
-    for (int ii = 0; ok && walk.next(a, it);) {
+    for (int ii = 0; ok && walk.next(bs, it);) {
       if (it.n == 0) continue;
       const int n_t = t ? it.nt[1] : it.nt[0];
       ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.q_full), ii & 1));
@@ -416,7 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (j >= 1 && j - 1 < n_t) {
           const int i = j - 1;
           const uint32_t vt = sbase + V_OFF + s * KV_TILE;
-          const int left = it.kv_end - i * KT;
+          const int left = it.kv_end - (it.j0 + i) * KT;
           if (left < KT) {
             // clear the value rows that are not the item's (both issuers
             // write the same zeros)
@@ -458,7 +732,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       u0 += it.n + 1;
       cs += n_t;
     }
-    if (!ok && lane == 0) atomicExch(&bs.abort, 1);
+    if ((!ok || !walk.ok) && lane == 0) atomicExch(&bs.abort, 1);
     if (elect_one()) umma_commit(smem_u32(&bs.mma_done[t]));
     __syncwarp();
     mbar_wait(smem_u32(&bs.mma_done[t]), 0);
@@ -469,10 +743,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int rp = r / nrep, hh = r - rp * nrep;
     const bool used = rp < qp;
     const uint32_t lane_addr = tmem + t * TILE_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t o_at = lane_addr + O_COL;
     const float scale = a.scale_log2;
     unsigned cs = 0;  // score tiles of this Q tile over the items (as the issuer counts them)
+    unsigned syncs = 0;
     bool ok = true;
-    while (ok && walk.next(a, it)) {
+    while (ok && walk.next(bs, it)) {
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int pos = it.q0 + t * qp + rp;  // query index within the sequence
       const bool real = used && pos < it.T;
@@ -497,7 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld32(lane_addr + s * KT, sr);
         tmem_ld32(lane_addr + s * KT + 32, sr + 32);
         tmem_ld_wait();
-        const int vis = lim - j * KT;  // columns 0..vis are visible to this row
+        const int vis = lim - (it.j0 + j) * KT;  // columns 0..vis are visible to this row
         if (vis < KT - 1) {
 #pragma unroll
           for (int cc = 0; cc < KT; ++cc)
@@ -537,11 +813,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int cc = 0; cc < HEAD_DIM; cc += 32) {
               uint32_t o[32];
-              tmem_ld32(lane_addr + O_COL + cc, o);
+              tmem_ld32(o_at + cc, o);
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(lane_addr + O_COL + cc, o);
+              tmem_st32(o_at + cc, o);
             }
           }
         }
@@ -558,13 +834,108 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
+      }
+      bool whole = true;
+      float m_own = 0.f, w_own = 1.f;  // of a shared item: the joint max in log2 units, the factor of this CTA's O
+      if (it.first != it.last) {
+        // the parts of the other CTAs may all be there already (the usual
+        // case for the CTA with the item's first keys, which come last in its
+        // range): then this one is added to them here, else it is left in memory
+        const int c = blockIdx.x, side = c == it.first;
+        if (threadIdx.x == 0)
+          bs.is_last = it.last - it.first <= DIRECT && ld_acquire(a.tickets + it.first) == it.last - it.first;
+        if (!softmax_sync(bs, syncs)) {
+          ok = false;
+          break;
+        }
+        whole = bs.is_last;
+        const float m2 = l > 0.f || l != l ? m_ref * scale : -INFINITY;
+        if (whole) {
+          m_own = m2;
+          if (real)
+            for (int d = it.first; d <= it.last; ++d)
+              if (d != c) m_own = fmaxf(m_own, __ldcg(part_ml(a, part_slot(d, it.first)) + t * ROWS + r).x);
+          if (m_own == -INFINITY) m_own = 0.f;
+          w_own = ex2_approx(m2 - m_own);
+          l *= w_own;
+          if (real)
+            for (int d = it.first; d <= it.last; ++d)
+              if (d != c) {
+                const float2 ml = __ldcg(part_ml(a, part_slot(d, it.first)) + t * ROWS + r);
+                l += ex2_approx(ml.x - m_own) * ml.y;
+              }
+        } else {
+          const size_t slot = part_slot(c, it.first);
+          if (real) __stcg(part_ml(a, slot) + t * ROWS + r, make_float2(m2, l));
+#pragma unroll 1
+          for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+            uint32_t o[32];
+            if (n_t > 0) {
+              tmem_ld32(o_at + cc, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+            if (real) {
+              float4* o4 = part_o(a, slot) + (cc / 4) * NQ * ROWS + t * ROWS + r;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(o4 + e * NQ * ROWS, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+            }
+          }
+          __threadfence();
+        }
+        if (!softmax_sync(bs, syncs)) {
+          ok = false;
+          break;
+        }
+        if (threadIdx.x == 0) {
+          if (whole) {
+            a.tickets[it.first] = 0;
+          } else {
+            __threadfence();
+            if (atomicAdd(a.tickets + it.first, 1) == it.last - it.first) {
+              a.tickets[it.first] = 0;
+              bs.left |= 1 << side;  // all parts are in memory, this one came last
+            }
+          }
+        }
+      }
+      if (whole && (n_t > 0 || it.first != it.last)) {
         const float inv = 1.f / l;
         float chk = 0.f;  // NaN when any value of the row is not finite
 #pragma unroll 1
         for (int cc = 0; cc < HEAD_DIM; cc += 32) {
           uint32_t o[32];
-          tmem_ld32(lane_addr + O_COL + cc, o);
-          tmem_ld_wait();
+          if (n_t > 0) {
+            tmem_ld32(o_at + cc, o);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (it.first != it.last && real) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w_own);
+            for (int d = it.first; d <= it.last; ++d) {
+              if (d == static_cast<int>(blockIdx.x)) continue;
+              const size_t slot = part_slot(d, it.first);
+              const float w = ex2_approx(__ldcg(part_ml(a, slot) + t * ROWS + r).x - m_own);
+              const float4* o4 = part_o(a, slot) + (cc / 4) * NQ * ROWS + t * ROWS + r;
+              float4 x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __ldcg(o4 + e * NQ * ROWS);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + w * x[e].x);
+                o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + w * x[e].y);
+                o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + w * x[e].z);
+                o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + w * x[e].w);
+              }
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 32; ++e) chk = fmaf(__uint_as_float(o[e]), 0.f, chk);
           if (real) {
@@ -581,20 +952,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         unsigned again = __ballot_sync(0xffffffffu, real && chk != chk && lim < it.kv_end - 1);
-        const Item same = it;
         for (; again; again &= again - 1) {
           const int src = __ffs(again) - 1;
-          const int p2 = __shfl_sync(0xffffffffu, pos, src), h2 = __shfl_sync(0xffffffffu, hh, src);
-          const size_t row = static_cast<size_t>(it.row0) + p2;
-          const int head = it.g * nrep + h2;
-          __syncwarp();
-          masked_row(a, same, a.q + static_cast<long long>(row) * a.q_stride + head * HEAD_DIM, it.start + p2,
-                     a.out + (row * a.n_heads + head) * HEAD_DIM);
+          masked_row(a, it.b, it.row0, it.g, it.start, __shfl_sync(0xffffffffu, pos, src),
+                     it.g * nrep + __shfl_sync(0xffffffffu, hh, src));
         }
       }
       cs += n_t;
     }
-    if (!ok && lane == 0) atomicExch(&bs.abort, 1);
+    if ((!ok || !walk.ok) && lane == 0) atomicExch(&bs.abort, 1);
   }
 
   tc_fence_before();
@@ -613,6 +979,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
+  // the item that this CTA's range ends, and the one it begins, where their
+  // parts are all in memory
+  const int left = bs.left;
+  if (left) {
+    __threadfence();
+    const Split split(units, parts);
+    const int u0 = split.start(blockIdx.x), u1 = split.start(blockIdx.x + 1);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side)
+      if (left >> side & 1) {
+        Item it = ranged_item(side ? u1 - 1 : u0, u1, split, E, bs.cum, pre, qp, a);
+        join(a, bs, it, qp, nrep);
+      }
+  }
+  // the last CTA out clears the claims for the next call
+  if (threadIdx.x == 0 && claim) {
+    __threadfence();
+    if (atomicAdd(a.claims + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      a.claims[0] = 0;
+      a.claims[1] = 0;
+    }
+  }
 }
 
 }  // namespace
@@ -629,12 +1017,8 @@ cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPre
     attr_set[dev] = true;
   }
   if (a.B <= 0 || a.B > PAGED_MAX_SEQS || a.N <= 0 || a.ctas <= 0) return cudaErrorInvalidValue;
-  // one CTA per SM (shared memory and TMEM admit no second), each walking its
-  // items; no more CTAs than the packed rows can make items
-  const int qp = ROWS / (a.n_heads / a.n_kv);
-  const long long items = (static_cast<long long>(a.N) / (NQ * qp) + a.B) * a.n_kv;
-  if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned ctas = static_cast<unsigned>(items < a.ctas ? items : a.ctas);
+  // one CTA per SM (shared memory and TMEM admit no second), each walking its items
+  const unsigned ctas = static_cast<unsigned>(a.ctas);
   return launch_behind(packed_prefill_kernel, ctas, THREADS, SMEM_BYTES, s, maps.q, maps.k, maps.v, a);
 }
 
