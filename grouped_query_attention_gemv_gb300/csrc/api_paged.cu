@@ -16,12 +16,12 @@ constexpr size_t TICKETS_OFFSET = 256;
 constexpr size_t PREFILL_ROWS = 256;  // query rows of an item
 constexpr size_t PREFILL_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * 2 * 4;
 constexpr size_t PREFILL_O_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * HEAD_DIM * 4;
-constexpr size_t PART_ML_OFFSET = TICKETS_OFFSET + 1024;
+constexpr size_t PART_ML_OFFSET = TICKETS_OFFSET + 2048;
 static_assert(PART_ML_OFFSET + PREFILL_ML_BYTES + PREFILL_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 constexpr size_t PART_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * 2 * 4;
 constexpr size_t PART_O_OFFSET = (PART_ML_OFFSET + PART_ML_BYTES + 255) / 256 * 256;
 constexpr size_t PART_O_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * HEAD_DIM * 4;
-static_assert(REF_SMS * 4 <= 1024, "tickets");
+static_assert(REF_SMS * 2 * 4 <= PART_ML_OFFSET - TICKETS_OFFSET, "tickets");
 static_assert(PART_O_OFFSET + PART_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 static_assert(GQA_PAGED_MAX_SEQS == PAGED_MAX_SEQS && GQA_PAGED_MAX_REP == PAGED_MAX_REP, "limits");
 
@@ -220,6 +220,10 @@ int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, c
   const int r = check_pages(pages, &p.pages);
   if (r != GQA_OK) return r;
   if (!aligned4(start_pos)) return GQA_EALIGN;
+  // the key tiles of the (at most 320) items that are cut into ranges are counted in 31 bits over the KV heads
+  if ((static_cast<long long>(pages->columns) * pages->page_size / PACKED_TILE + 1) * 320 * pages->n_kv_heads >
+      0x7fffffffLL)
+    return GQA_EINVAL;
   p.start = start_pos;
   return prefill_call(q, q_stride, N, n_heads, pages->n_kv_heads, cu_tokens, B, scale, out, workspace,
                       workspace_bytes, stream, p, pages->page_size, pages->num_pages,
@@ -242,7 +246,7 @@ int gqa_packed_prefill(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, i
   p.pages.page_stride = k_stride;
   p.v_row_stride = v_stride;
   return prefill_call(q, q_stride, N, n_heads, n_kv_heads, cu_tokens, B, scale, out, workspace, workspace_bytes,
-                      stream, p, N, 1, PREFILL_TILE);
+                      stream, p, N, 1, PACKED_TILE);
 }
 
 }  // extern "C"

@@ -339,8 +339,9 @@ struct PackedPrefillParams {
   float scale_log2;
   __nv_bfloat16* out;       // [N][n_heads][128]
   // parts of items that several CTAs share: [2 * ctas][256 rows][128], their
-  // (max in log2 units, sum), a ticket per CTA; the claims of whole items and
-  // the count of CTAs that are done. Tickets and claims zero-filled, left so.
+  // (max in log2 units, sum), two counts per CTA (parts that arrived, parts
+  // written); the claims of whole items and the count of CTAs that are done.
+  // Counts zero-filled, left so.
   float *part_o, *part_ml;
   int *tickets, *claims;
   int* status;
@@ -352,7 +353,8 @@ struct PackedPrefillParams {
 struct PackedPrefillMaps {
   CUtensorMap q, k, v;
 };
-__host__ __device__ constexpr int prefill_box_rows(int page_size) { return page_size < PREFILL_TILE ? page_size : PREFILL_TILE; }
+constexpr int PACKED_TILE = 128;  // keys of a tile
+__host__ __device__ constexpr int prefill_box_rows(int page_size) { return page_size < PACKED_TILE ? page_size : PACKED_TILE; }
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& p, cudaStream_t s);
 
 cudaError_t launch_rope_table(float* rope, int rows, double theta, int scaled, double factor, double lo,

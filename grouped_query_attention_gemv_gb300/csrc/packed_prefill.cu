@@ -37,8 +37,9 @@ namespace {
 
 constexpr int ROWS = 128;                 // rows of a Q tile = MMA M
 constexpr int NQ = 2;                     // Q tiles per CTA
-constexpr int KT = PREFILL_TILE;          // keys per tile
-constexpr int STAGES = 4;                 // K tiles and V tiles in flight
+constexpr int KT = PACKED_TILE;           // keys per tile
+constexpr int HALF = KT / 2;
+constexpr int STAGES = 2;                 // K tiles and V tiles in shared memory
 constexpr int Q_HALF = ROWS * 128;        // 128 rows x 64 dims
 constexpr int Q_TILE = 2 * Q_HALF;
 constexpr int KV_HALF = KT * 128;         // 64 keys x 64 dims
@@ -54,11 +55,11 @@ constexpr int SMEM_BYTES = PRE_OFF + (PAGED_MAX_SEQS + 1) * 4 + 1024;
 constexpr int THREADS = 352;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                  // items handed from the producer to the other warps
-constexpr int JOIN_TILES = 6;             // what joining the parts of an item costs, in key tiles of one CTA
-constexpr int MIN_TILES = 6;              // key tiles of a part at least
+constexpr int JOIN_TILES = 3;             // what joining the parts of an item costs, in key tiles of one CTA
+constexpr int MIN_TILES = 3;              // key tiles of a part at least
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TILE_COLS = 256;       // TMEM columns of one Q tile
-constexpr uint32_t O_COL = 128;
+// TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
+constexpr uint32_t S_COLS = 128, O_COL = 256, O_COLS = 128;
 constexpr float RESCALE_LOG2 = 8.f;
 
 // What a CTA works on at a time: 2 Q tiles (NQ x qp query positions) of one
@@ -72,16 +73,18 @@ struct Item {
 };
 
 struct Bars {
-  uint64_t q_full;
-  uint64_t kv_full[STAGES], kv_empty[STAGES];  // stage j of an item: K_j and V_{j-1}
-  uint64_t s_full[NQ][2], p_full[NQ][2];
+  uint64_t q_full[NQ];
+  uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
+  uint64_t s_full[NQ], p_full[NQ][2];  // p_full: the first and the second half of the keys
+  uint64_t turn[NQ];                   // the issuer of Q tile t has issued a step
   uint64_t o_done[NQ], mma_done[NQ];
   uint64_t item_full[SLOTS], item_empty[SLOTS], joint;
   uint32_t tmem_slot;
   int abort;
-  int q_issued, kv_issued;
+  int q_issued[NQ], k_issued, v_issued;
   int warp_sum[THREADS / 32];
   int is_last;                // of an item's parts, this CTA's is the last
+  int parts_there;            // the others are written
   int left;                   // bits: the first / the last shared item of this CTA is left to join from memory
   Item item[SLOTS];           // g < 0: no more
   int cum[MAX_SORT + 1];      // key tiles before entry e, if there are at most MAX_SORT entries
@@ -276,19 +279,29 @@ __device__ __forceinline__ bool join_block(const PackedPrefillParams& a, const I
   float4 o[BLOCK];
 #pragma unroll
   for (int e = 0; e < BLOCK; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = it.first; c <= it.last; ++c) {
-    const size_t slot = part_slot(c, it.first);
-    const float w = ex2_approx(__ldcg(part_ml(a, slot) + row).x - m);
-    float4 x[BLOCK];
+  constexpr int AHEAD = 4;  // parts in flight
+  for (int c0 = it.first; c0 <= it.last; c0 += AHEAD) {
+    float w[AHEAD];
+    float4 x[AHEAD][BLOCK];
 #pragma unroll
-    for (int e = 0; e < BLOCK; ++e) x[e] = __ldcg(part_o(a, slot) + (c4 + e) * NQ * ROWS + row);
+    for (int k = 0; k < AHEAD; ++k) {
+      if (c0 + k > it.last) continue;
+      const size_t slot = part_slot(c0 + k, it.first);
+      w[k] = __ldcg(part_ml(a, slot) + row).x;
 #pragma unroll
-    for (int e = 0; e < BLOCK; ++e) {
-      o[e].x += w * x[e].x;
-      o[e].y += w * x[e].y;
-      o[e].z += w * x[e].z;
-      o[e].w += w * x[e].w;
+      for (int e = 0; e < BLOCK; ++e) x[k][e] = __ldcg(part_o(a, slot) + (c4 + e) * NQ * ROWS + row);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (c0 + k > it.last) continue;
+      const float f = ex2_approx(w[k] - m);
+#pragma unroll
+      for (int e = 0; e < BLOCK; ++e) {
+        o[e].x += f * x[k][e].x;
+        o[e].y += f * x[k][e].y;
+        o[e].z += f * x[k][e].z;
+        o[e].w += f * x[k][e].w;
+      }
     }
   }
   float chk = 0.f;  // NaN when a value is not finite
@@ -335,16 +348,15 @@ __device__ __forceinline__ void join(const PackedPrefillParams& a, Bars& bs, con
     pos = it.q0 + t * qp + rp;
     head = it.g * nrep + r - rp * nrep;
   };
-  // (column block, row) pairs, rows fastest; narrow blocks where rows are few
-  const int width = total >= 64 ? 8 : 2;
+  // (column block, row) pairs, rows fastest
+  constexpr int WIDTH = 2;
 #pragma unroll 1
-  for (int i = tid; i < total * (HEAD_DIM / 4 / width); i += THREADS) {
+  for (int i = tid; i < total * (HEAD_DIM / 4 / WIDTH); i += THREADS) {
     const int blk = i / total;
     int row, pos, head;
     place(i - blk * total, row, pos, head);
     __nv_bfloat16* dst = a.out + ((static_cast<size_t>(it.row0) + pos) * a.n_heads + head) * HEAD_DIM;
-    const bool fine = width == 8 ? join_block<8>(a, it, row, blk * 8, bs.row_m[row], bs.row_inv[row], dst)
-                                 : join_block<2>(a, it, row, blk * 2, bs.row_m[row], bs.row_inv[row], dst);
+    const bool fine = join_block<WIDTH>(a, it, row, blk * WIDTH, bs.row_m[row], bs.row_inv[row], dst);
     if (!fine) bs.row_bad[row] = 1;
   }
   __syncthreads();
@@ -368,16 +380,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int qp = ROWS / nrep;  // query positions per Q tile
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&bs.q_full), 1);
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&bs.kv_full[s]), 1);
-      mbar_init(smem_u32(&bs.kv_empty[s]), NQ);  // one arrival per MMA issuer
+      mbar_init(smem_u32(&bs.k_full[s]), 1);
+      mbar_init(smem_u32(&bs.k_empty[s]), NQ);  // one arrival per MMA issuer
+      mbar_init(smem_u32(&bs.v_full[s]), 1);
+      mbar_init(smem_u32(&bs.v_empty[s]), NQ);
     }
     for (int t = 0; t < NQ; ++t) {
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(smem_u32(&bs.s_full[t][s]), 1);
-        mbar_init(smem_u32(&bs.p_full[t][s]), 4);
-      }
+      mbar_init(smem_u32(&bs.q_full[t]), 1);
+      mbar_init(smem_u32(&bs.s_full[t]), 1);
+      mbar_init(smem_u32(&bs.turn[t]), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&bs.p_full[t][h]), 4);
       mbar_init(smem_u32(&bs.o_done[t]), 1);
       mbar_init(smem_u32(&bs.mma_done[t]), 1);
     }
@@ -388,8 +401,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     bs.abort = 0;
     bs.left = 0;
-    bs.q_issued = 0;
-    bs.kv_issued = 0;
+    bs.q_issued[0] = bs.q_issued[1] = 0;
+    bs.k_issued = bs.v_issued = 0;
     fence_barrier_init();
   }
   if (warp == MMA_WARP) {
@@ -436,12 +449,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   // key tiles are prefix-summed and sorted by length.
   const int E = pre[a.B], G = gridDim.x;
   const long long nitems = static_cast<long long>(E) * a.n_kv;
-  bool equal = false;  // equal ranges of key tiles instead of whole items
+  bool equal = false;   // equal ranges of key tiles instead of whole items
+  bool sorted = false;  // whole items in the order of bs.order
   int units = 0, parts = 1;
-  if (E <= MAX_SORT) {
+  const int own_n = E <= MAX_SORT && static_cast<int>(threadIdx.x) < E ? entry_at(threadIdx.x, pre, qp, a).n : 0;
+  // nothing to plan where every CTA has one short item at most
+  if (E <= MAX_SORT && (__syncthreads_or(own_n > JOIN_TILES + 1) || nitems > G)) {
     const int e = threadIdx.x;
-    const int n = e < E ? entry_at(e, pre, qp, a).n : 0;
-    if (e < E) bs.cum[e + 1] = n;
+    if (e < E) bs.cum[e + 1] = own_n;
     if (e == 0) bs.cum[0] = 0;
     __syncthreads();
     int before = 0, rank = 0;
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int f = 0; f < E; ++f) {
         const int m = bs.cum[f + 1];
         before += f <= e ? m : 0;
-        rank += m > n || (m == n && f < e);
+        rank += m > own_n || (m == own_n && f < e);
       }
     __syncthreads();
     if (e < E) {
@@ -457,9 +472,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       bs.cum[e + 1] = before;
     }
     __syncthreads();
+    sorted = true;
     units = bs.cum[E] * a.n_kv;
     // the load of CTA `threadIdx.x` if whole items went round in turn, longest first
-    long long load = 0;
+    int load = 0;
     if (static_cast<int>(threadIdx.x) < G)
       for (int k = 0; k * G < nitems; ++k) {
         const int i = k * G + ((k & 1) ? G - 1 - static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x));
@@ -502,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         asked = true;
         if (wi >= nitems) return false;
         const int e = static_cast<int>(wi / a.n_kv);
-        it = entry_at(E <= MAX_SORT ? bs.order[e] : e, pre, qp, a);
+        it = entry_at(sorted ? bs.order[e] : e, pre, qp, a);
         it.g = static_cast<int>(wi - static_cast<long long>(e) * a.n_kv);
         return true;
       }
@@ -544,97 +560,85 @@ __global__ void __launch_bounds__(THREADS, 1)
       tma_prefetch_desc(&mk);
       tma_prefetch_desc(&mv);
     }
-    // stage j of an item holds K_j (j < n) and V_{j-1} (j >= 1), the tiles
-    // its two issuers' iteration j reads: one full and one empty barrier a
-    // stage. u counts stages over the CTA's items, ring slot u % STAGES.
-    // Lane x < boxes handles box x of every tile.
+    // Lane x < boxes handles box x of every tile. u counts tiles over the
+    // CTA's items, ring slot u % STAGES.
     const int box = a.start ? prefill_box_rows(1 << a.pages.page_shift) : KT;
     const int boxes = KT / box;
     const uint32_t q_bytes = static_cast<uint32_t>(qp * nrep) * 128;
-    int u0 = 0, kvn = 0, qn = 0;
+    int u = 0, kn = 0, vn = 0, qn[NQ] = {};
     int cs[NQ] = {};  // score tiles of each Q tile so far (as its issuer counts them)
     bool ok = true, stop = false;
-    int row_k = 0, page_k = 0, row_v = 0, page_v = 0;  // coordinates of this lane's box of K_j, V_{j-1}
-    auto locate = [&](const Item& it, int j) {
-      const int key = (it.j0 + j) * KT + lane * box;
-      if (lane >= boxes || key >= it.kv_end) return;
-      if (!a.start) {
-        row_k = it.row0 + key;
-        return;
-      }
-      row_k = key & ((1 << a.pages.page_shift) - 1);
-      page_k = a.pages.table[static_cast<long long>(it.b) * a.pages.table_stride + (key >> a.pages.page_shift)];
-      if (page_k < 0 || page_k >= a.pages.num_pages) {
-        report(a.status, DEV_BAD_PAGE);
-        page_k = 0;
-      }
+    auto go_on = [&](uint64_t& bar, int parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity));
+      return ok && !__any_sync(0xffffffffu, aborted(bs));
     };
-    // boxes of key tile j that hold keys of the item
-    auto held = [&](const Item& it, int j) { return min(boxes, (it.kv_end - (it.j0 + j) * KT + box - 1) / box); };
-    // copies of stage j; false when a wait gave up or the kernel is aborting
-    auto load_stage = [&](const Item& it, int j) -> bool {
-      const int u = u0 + j, s = u % STAGES;
-      row_v = row_k;
-      page_v = page_k;
-      if (j < it.n) locate(it, j);
-      if (u >= STAGES) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.kv_empty[s]), ((u / STAGES) - 1) & 1));
-      if (!ok || __any_sync(0xffffffffu, aborted(bs))) return false;
-      const uint32_t fb = smem_u32(&bs.kv_full[s]);
-      const int nk = j < it.n ? held(it, j) : 0, nv = j >= 1 ? held(it, j - 1) : 0;
-      if (lane == 0) mbar_expect_tx(fb, static_cast<uint32_t>(nk + nv) * box * 256);
+    auto copy = [&](const CUtensorMap* map, uint64_t& full, uint32_t dst, int held, int g, int row, int page) {
+      const uint32_t fb = smem_u32(&full);
+      if (lane == 0) mbar_expect_tx(fb, static_cast<uint32_t>(held * box) * 256);
       __syncwarp();
-      const uint32_t at = static_cast<uint32_t>(lane * box) * 128;
-      if (lane < nk) {
-        const uint32_t dst = sbase + K_OFF + s * KV_TILE + at;
-        tma_load_4d(dst, &mk, fb, 0, it.g, row_k, page_k);
-        tma_load_4d(dst + KV_HALF, &mk, fb, 64, it.g, row_k, page_k);
-      }
-      if (lane < nv) {
-        const uint32_t dst = sbase + V_OFF + s * KV_TILE + at;
-        tma_load_4d(dst, &mv, fb, 0, it.g, row_v, page_v);
-        tma_load_4d(dst + KV_HALF, &mv, fb, 64, it.g, row_v, page_v);
+      if (lane < held) {
+        const uint32_t at = dst + static_cast<uint32_t>(lane * box) * 128;
+        tma_load_4d(at, map, fb, 0, g, row, page);
+        tma_load_4d(at + KV_HALF, map, fb, 64, g, row, page);
       }
       __syncwarp();
-      kvn = u + 1;
-      return true;
     };
-    for (int ii = 0; !stop && next_item(it);) {
+    while (!stop && next_item(it)) {
       if (!put(it)) {
         ok = false;
         break;
       }
-      if (it.n == 0) continue;
-      // after the first item, the item's first stages go out before its Q
-      // tiles: their ring slots free up while the previous item's last
-      // products run, the Q tiles only after its last score products have
-      // completed
-      const int la = ii > 0 ? min(STAGES, it.n + 1) : 0;
-      for (int j = 0; j < la && !stop; ++j) stop = !load_stage(it, j);
-      if (stop) break;
-      // Q tile t is free once the last score product of the previous item
-      // that read it has completed (its s_full phase; the next product on
-      // that slot needs the new Q, so the phase cannot have moved on)
-#pragma unroll
-      for (int t = 0; t < NQ; ++t)
-        if (ok && cs[t] > 0)
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t][(cs[t] - 1) & 1]), ((cs[t] - 1) >> 1) & 1));
-      if (!ok || __any_sync(0xffffffffu, aborted(bs))) break;
-      const uint32_t qb = smem_u32(&bs.q_full);
-      if (lane == 0) {
-        const int nq = it.nt[1] ? 2 : 1;
-        mbar_expect_tx(qb, nq * 2 * q_bytes);
-        // boxes may reach into the next sequence, or past N (zeros): rows that are never stored
-        for (int t = 0; t < nq; ++t) {
-          tma_load_3d(sbase + t * Q_TILE, &mq, qb, 0, it.g * nrep, it.row0 + it.q0 + t * qp);
-          tma_load_3d(sbase + t * Q_TILE + Q_HALF, &mq, qb, 64, it.g * nrep, it.row0 + it.q0 + t * qp);
+      for (int j = 0; j < it.n && !stop; ++j, ++u) {
+        const int s = u % STAGES;
+        // boxes of the tile that hold keys of the item; this lane's
+        const int held = min(boxes, (it.kv_end - (it.j0 + j) * KT + box - 1) / box);
+        const int key = (it.j0 + j) * KT + lane * box;
+        int row = it.row0 + key, page = 0;
+        if (a.start) {
+          row = key & ((1 << a.pages.page_shift) - 1);
+          if (lane < held)
+            page = a.pages.table[static_cast<long long>(it.b) * a.pages.table_stride + (key >> a.pages.page_shift)];
         }
+        if (u >= STAGES && !go_on(bs.k_empty[s], (u / STAGES - 1) & 1)) {
+          stop = true;
+          break;
+        }
+        if (page < 0 || (a.start && page >= a.pages.num_pages)) {
+          report(a.status, DEV_BAD_PAGE);
+          page = 0;
+        }
+        copy(&mk, bs.k_full[s], sbase + K_OFF + s * KV_TILE, held, it.g, row, page);
+        kn = u + 1;
+        if (j == 0) {
+          // Q tile t is free once the last score product of the previous item
+          // that read it has completed (the next one on its S needs the new
+          // Q, so that phase is the latest)
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) {
+            if (stop || !it.nt[t]) continue;
+            if (cs[t] > 0 && !go_on(bs.s_full[t], (cs[t] - 1) & 1)) {
+              stop = true;
+              continue;
+            }
+            if (lane == 0) {
+              const uint32_t qb = smem_u32(&bs.q_full[t]);
+              mbar_expect_tx(qb, 2 * q_bytes);
+              // boxes may reach into the next sequence, or past N (zeros): rows that are never stored
+              tma_load_3d(sbase + t * Q_TILE, &mq, qb, 0, it.g * nrep, it.row0 + it.q0 + t * qp);
+              tma_load_3d(sbase + t * Q_TILE + Q_HALF, &mq, qb, 64, it.g * nrep, it.row0 + it.q0 + t * qp);
+            }
+            __syncwarp();
+            ++qn[t];
+          }
+          if (stop) break;
+        }
+        if (u >= STAGES && !go_on(bs.v_empty[s], (u / STAGES - 1) & 1)) {
+          stop = true;
+          break;
+        }
+        copy(&mv, bs.v_full[s], sbase + V_OFF + s * KV_TILE, held, it.g, row, page);
+        vn = u + 1;
       }
-      __syncwarp();
-      ++ii;
-      qn = ii;
-      for (int j = la; j <= it.n && !stop; ++j) stop = !load_stage(it, j);
-      if (stop) break;
-      u0 += it.n + 1;
 #pragma unroll
       for (int t = 0; t < NQ; ++t) cs[t] += it.nt[t];
     }
@@ -644,93 +648,126 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (lane == 0) {
       if (!ok) atomicExch(&bs.abort, 1);
-      bs.q_issued = qn;
-      bs.kv_issued = kvn;
+      bs.q_issued[0] = qn[0];
+      bs.q_issued[1] = qn[1];
+      bs.k_issued = kn;
+      bs.v_issued = vn;
     }
   } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
     // issuer of Q tile t (the whole warp runs the loop; one elected lane
-    // issues): waits on every K/V stage so that its arrivals on the empty
-    // barriers stay in step with the other issuer's; a stage past this
-    // tile's causal range gets a plain arrival. cs counts this tile's score
-    // tiles over the items (S slot cs % 2, one O product group each).
+    // issues). Step j: P_{j-1} V_{j-1}, then S_j into the columns P_{j-1} lay
+    // in (products of one thread complete in order). The two issuers take
+    // turns step by step: both tiles' products side by side would end
+    // together, and both softmaxes run side by side after them; in turns, one
+    // tile's softmax runs beside the other's products. They wait on every K
+    // and V tile of the item, so that their arrivals on the empty barriers
+    // stay in step; a tile past the causal range gets a plain arrival. cs
+    // counts this Q tile's score tiles over the items, qi its items, step the
+    // steps of all items.
     const int t = warp - MMA_WARP;
-    const uint32_t idesc_s = umma_idesc_bf16(ROWS, KT);
+    const uint32_t idesc_s = umma_idesc_bf16(ROWS, KT), idesc_sh = umma_idesc_bf16(ROWS, HALF);
     const uint32_t idesc_o = umma_idesc_bf16(ROWS, HEAD_DIM) | (1u << 16);  // B (V) MN-major
     const uint32_t qt = sbase + t * Q_TILE;
-    const uint32_t base = tmem + t * TILE_COLS;
-    unsigned u0 = 0, cs = 0;
+    const uint32_t s_at = tmem + t * S_COLS, o_at = tmem + O_COL + t * O_COLS;
+    unsigned u0 = 0, cs = 0, qi = 0, step = 0;
     bool ok = true;
-    for (int ii = 0; ok && walk.next(bs, it);) {
+    auto wait = [&](uint64_t& bar, unsigned parity) {
+      return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity));
+    };
+    // the stage is free once this issuer's products on it are done (a commit
+    // covers every product the thread issued before it)
+    auto release = [&](uint64_t& bar, bool used) {
+      if (elect_one()) {
+        if (used) umma_commit(smem_u32(&bar));
+        else mbar_arrive(smem_u32(&bar));
+      }
+      __syncwarp();
+    };
+    while (ok && walk.next(bs, it)) {
       if (it.n == 0) continue;
       const int n_t = t ? it.nt[1] : it.nt[0];
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.q_full), ii & 1));
-      if (!ok) break;
-      ++ii;
-      for (int j = 0; ok && j <= it.n; ++j) {
-        const unsigned u = u0 + j, s = u % STAGES;
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.kv_full[s]), (u / STAGES) & 1));
-        if (!ok) break;
-        bool used = false;
+      const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
+      for (int j = 0; j <= it.n; ++j, ++step) {
+        if (j >= 1) {
+          const int i = j - 1, tile = it.j0 + i;
+          const unsigned u = u0 + i, s = u % STAGES;
+          if (!wait(bs.v_full[s], (u / STAGES) & 1)) break;
+          const uint32_t vt = sbase + V_OFF + s * KV_TILE;
+          const bool second = end_t - tile * KT > HALF;
+          if (i < n_t) {
+            const int left = it.kv_end - tile * KT, read = second ? KT : HALF;
+            if (left < read) {
+              // clear the value rows that are not the item's (both issuers
+              // write the same zeros)
+              for (int w = lane; w < (read - left) * 16; w += 32) {
+                const int row = left + (w >> 4);
+                st_shared_v4(vt + ((w >> 3) & 1) * KV_HALF + row * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            // P of the item's first key tile also tells that the softmax
+            // warps have read the previous item's O (their epilogue comes
+            // first), so that the first product may overwrite it
+            if (!wait(bs.p_full[t][0], (cs + i) & 1)) break;
+          }
+          if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) break;
+          if (i < n_t) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !wait(bs.p_full[t][1], (cs + i) & 1)) break;
+              tc_fence_after();
+              if (h == 1 && !second) break;  // no visible keys in the second half
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < HALF / 16; ++ks)
+                  umma_bf16_ts(o_at, s_at + h * (HALF / 2) + ks * 8,
+                               umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF), idesc_o,
+                               (i > 0 || h > 0 || ks > 0) ? 1u : 0u);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+        } else if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) {
+          break;
+        }
         if (j < n_t) {
+          const unsigned u = u0 + j, s = u % STAGES;
+          if (j == 0 && !wait(bs.q_full[t], qi & 1)) break;
+          if (!wait(bs.k_full[s], (u / STAGES) & 1)) break;
           tc_fence_after();
           const uint32_t kt = sbase + K_OFF + s * KV_TILE;
-          const unsigned slot = (cs + j) & 1u;
+          const uint32_t idesc = end_t - (it.j0 + j) * KT > HALF ? idesc_s : idesc_sh;
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
               const uint32_t off = (ks & 3) * 32;
-              umma_bf16(base + slot * KT, umma_desc_sw128(qt + (ks >> 2) * Q_HALF + off),
-                        umma_desc_sw128(kt + (ks >> 2) * KV_HALF + off), idesc_s, ks > 0 ? 1u : 0u);
+              umma_bf16(s_at, umma_desc_sw128(qt + (ks >> 2) * Q_HALF + off),
+                        umma_desc_sw128(kt + (ks >> 2) * KV_HALF + off), idesc, ks > 0 ? 1u : 0u);
             }
-            umma_commit(smem_u32(&bs.s_full[t][slot]));
+            umma_commit(smem_u32(&bs.s_full[t]));
           }
           __syncwarp();
-          used = true;
         }
-        if (j >= 1 && j - 1 < n_t) {
-          const int i = j - 1;
-          const uint32_t vt = sbase + V_OFF + s * KV_TILE;
-          const int left = it.kv_end - (it.j0 + i) * KT;
-          if (left < KT) {
-            // clear the value rows that are not the item's (both issuers
-            // write the same zeros)
-            for (int w = lane; w < (KT - left) * 16; w += 32) {
-              const int row = left + (w >> 4);
-              st_shared_v4(vt + ((w >> 3) & 1) * KV_HALF + row * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
-            }
-            fence_proxy_async_smem();
+        if (lane == 0) mbar_arrive(smem_u32(&bs.turn[t]));
+        if (j >= 1) {
+          if (j == n_t) {
+            if (elect_one()) umma_commit(smem_u32(&bs.o_done[t]));
             __syncwarp();
           }
-          // P of the item's first key tile also tells that the softmax
-          // warps have read the previous item's O (their epilogue comes
-          // first), so that the first product may overwrite it
-          const unsigned c = cs + i;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.p_full[t][c & 1]), (c >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks)
-              umma_bf16_ts(base + O_COL, base + (c & 1) * KT + ks * 8,
-                           umma_desc_sw128_mn(vt + ks * 16 * 128, KV_HALF), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
-            umma_commit(smem_u32(&bs.o_done[t]));
-          }
-          __syncwarp();
-          used = true;
+          release(bs.v_empty[(u0 + j - 1) % STAGES], j <= n_t);
         }
-        // the stage is free once this issuer's products on it are done (a
-        // commit covers every product the thread issued before it)
-        if (elect_one()) {
-          if (used)
-            umma_commit(smem_u32(&bs.kv_empty[s]));
-          else
-            mbar_arrive(smem_u32(&bs.kv_empty[s]));
+        if (j < it.n) {
+          const unsigned u = u0 + j, s = u % STAGES;
+          if (j >= n_t && !wait(bs.k_full[s], (u / STAGES) & 1)) break;
+          release(bs.k_empty[s], j < n_t);
         }
-        __syncwarp();
       }
       if (!ok) break;
-      u0 += it.n + 1;
+      u0 += it.n;
       cs += n_t;
+      qi += n_t > 0;
     }
     if ((!ok || !walk.ok) && lane == 0) atomicExch(&bs.abort, 1);
     if (elect_one()) umma_commit(smem_u32(&bs.mma_done[t]));
@@ -742,16 +779,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r = (warp & 3) * 32 + lane;
     const int rp = r / nrep, hh = r - rp * nrep;
     const bool used = rp < qp;
-    const uint32_t lane_addr = tmem + t * TILE_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_at = lane_addr + O_COL;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + t * S_COLS + lanes, o_at = tmem + O_COL + t * O_COLS + lanes;
     const float scale = a.scale_log2;
     unsigned cs = 0;  // score tiles of this Q tile over the items (as the issuer counts them)
-    unsigned syncs = 0;
+    unsigned syncs = 0, items = 0;  // items with keys of this Q tile
     bool ok = true;
     while (ok && walk.next(bs, it)) {
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int pos = it.q0 + t * qp + rp;  // query index within the sequence
       const bool real = used && pos < it.T;
+      const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
       const int lim = used ? min(it.start + pos, it.kv_end - 1) : -1;  // last key this row sees
       __nv_bfloat16* dst = a.out + (static_cast<size_t>(it.row0) + pos) * a.n_heads * HEAD_DIM +
                            static_cast<size_t>(it.g * nrep + hh) * HEAD_DIM;
@@ -762,109 +800,122 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
       float l = 0.f;
       for (int j = 0; j < n_t; ++j) {
-        const unsigned c = cs + j;
-        const unsigned s = c & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t][s]), (c >> 1) & 1))) {
+        // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t]), (cs + j) & 1))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t sr[KT];
-        tmem_ld32(lane_addr + s * KT, sr);
-        tmem_ld32(lane_addr + s * KT + 32, sr + 32);
-        tmem_ld_wait();
-        const int vis = lim - (it.j0 + j) * KT;  // columns 0..vis are visible to this row
-        if (vis < KT - 1) {
+        const int tile = it.j0 + j;
+        const bool second = end_t - tile * KT > HALF;
+        const int vis = lim - tile * KT;  // columns 0..vis are visible to this row
+        // columns of half h, keys past the row's position at -inf; the second
+        // half is read for the max first and again for its P (registers)
+        uint32_t sr[HALF];
+        auto load = [&](int h) {
+          tmem_ld32(s_at + h * HALF, sr);
+          tmem_ld32(s_at + h * HALF + 32, sr + 32);
+          tmem_ld_wait();
+          if (vis < h * HALF + HALF - 1) {
 #pragma unroll
-          for (int cc = 0; cc < KT; ++cc)
-            if (cc > vis) sr[cc] = __float_as_uint(-INFINITY);
+            for (int cc = 0; cc < HALF; ++cc)
+              if (h * HALF + cc > vis) sr[cc] = __float_as_uint(-INFINITY);
+          }
+        };
+        float mx = -INFINITY, m1 = mx, m2 = mx, m3 = mx;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          if (h == 1 && !second) continue;
+          load(h);
+#pragma unroll
+          for (int cc = 0; cc < HALF; cc += 8) {
+            mx = max3(mx, __uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1]));
+            m1 = max3(m1, __uint_as_float(sr[cc + 2]), __uint_as_float(sr[cc + 3]));
+            m2 = max3(m2, __uint_as_float(sr[cc + 4]), __uint_as_float(sr[cc + 5]));
+            m3 = max3(m3, __uint_as_float(sr[cc + 6]), __uint_as_float(sr[cc + 7]));
+          }
         }
-        float mx = fmaxf(__uint_as_float(sr[0]), __uint_as_float(sr[1]));
-#pragma unroll
-        for (int cc = 2; cc < KT; cc += 2) mx = max3(mx, __uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1]));
+        mx = fmaxf(max3(mx, m1, m2), m3);
         float alpha = 1.f;
         const bool grow = mx > m_ref && (m_ref == -INFINITY || (mx - m_ref) * scale > RESCALE_LOG2);
         if (grow) {
           alpha = m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - mx) * scale);
           m_ref = mx;
         }
+        if (j > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + cc, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(o_at + cc, o);
+          }
+        }
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref * scale;
         // exponent arguments and the row sum two columns per instruction
         const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
-        float2 sum2 = make_float2(0.f, 0.f);
-        uint32_t pk[KT / 2];
+        float2 sum2 = make_float2(0.f, 0.f), sum3 = sum2;
 #pragma unroll
-        for (int cc = 0; cc < KT; cc += 2) {
-          const float2 e = fma2(make_float2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, ng2);
-          const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-          sum2 = add2(sum2, p);
-          pk[cc >> 1] = pack_bf16(p.x, p.y);
-        }
-        l = l * alpha + (sum2.x + sum2.y);
-        if (j > 0) {
-          // O must hold P_{j-1} V_{j-1} before it is rescaled (and this keeps
-          // the o_done phases in step with the score tiles)
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), (c - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll 1
-            for (int cc = 0; cc < HEAD_DIM; cc += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + cc, o);
-              tmem_ld_wait();
+        for (int h = 0; h < 2; ++h) {
+          if (h == 0 || second) {
+            if (h == 1) load(1);
+            uint32_t pk[HALF / 2];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st32(o_at + cc, o);
+            for (int cc = 0; cc < HALF; cc += 4) {
+              const float2 e = fma2(make_float2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, ng2);
+              const float2 f =
+                  fma2(make_float2(__uint_as_float(sr[cc + 2]), __uint_as_float(sr[cc + 3])), sc2, ng2);
+              const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              const float2 q = make_float2(ex2_approx(f.x), ex2_approx(f.y));
+              sum2 = add2(sum2, p);
+              sum3 = add2(sum3, q);
+              pk[cc >> 1] = pack_bf16(p.x, p.y);
+              pk[(cc >> 1) + 1] = pack_bf16(q.x, q.y);
             }
+            tmem_st32(s_at + h * (HALF / 2), pk);
+            tmem_st_wait();
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bs.p_full[t][h]));
         }
-        tmem_st32(lane_addr + s * KT, pk);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bs.p_full[t][s]));
+        sum2 = add2(sum2, sum3);
+        l = l * alpha + (sum2.x + sum2.y);
       }
       if (!ok) break;
       if (n_t > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), (cs + n_t - 1) & 1))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), items & 1))) {
           ok = false;
           break;
         }
+        ++items;
         tc_fence_after();
       }
       bool whole = true;
-      float m_own = 0.f, w_own = 1.f;  // of a shared item: the joint max in log2 units, the factor of this CTA's O
+      // of a shared item that is joined here: the factor of this CTA's O, the
+      // other parts' slots and factors
+      float w_own = 1.f, w_part[DIRECT] = {};
+      size_t at_part[DIRECT] = {};
+      int nparts = 0;
       if (it.first != it.last) {
-        // the parts of the other CTAs may all be there already (the usual
-        // case for the CTA with the item's first keys, which come last in its
-        // range): then this one is added to them here, else it is left in memory
-        const int c = blockIdx.x, side = c == it.first;
-        if (threadIdx.x == 0)
-          bs.is_last = it.last - it.first <= DIRECT && ld_acquire(a.tickets + it.first) == it.last - it.first;
+        // The CTA that arrives last at the item's ticket joins its parts (the
+        // others have arrived, so they are running and about to write
+        // theirs). A few parts are added to this CTA's in its epilogue; of
+        // many, this one is left in memory as well and all are joined by the
+        // whole CTA at its end.
+        const int c = blockIdx.x, others = it.last - it.first;
+        int* arrived = a.tickets + 2 * it.first;
+        if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
         if (!softmax_sync(bs, syncs)) {
           ok = false;
           break;
         }
-        whole = bs.is_last;
+        const bool last = bs.is_last;
+        whole = last && others <= DIRECT;
         const float m2 = l > 0.f || l != l ? m_ref * scale : -INFINITY;
-        if (whole) {
-          m_own = m2;
-          if (real)
-            for (int d = it.first; d <= it.last; ++d)
-              if (d != c) m_own = fmaxf(m_own, __ldcg(part_ml(a, part_slot(d, it.first)) + t * ROWS + r).x);
-          if (m_own == -INFINITY) m_own = 0.f;
-          w_own = ex2_approx(m2 - m_own);
-          l *= w_own;
-          if (real)
-            for (int d = it.first; d <= it.last; ++d)
-              if (d != c) {
-                const float2 ml = __ldcg(part_ml(a, part_slot(d, it.first)) + t * ROWS + r);
-                l += ex2_approx(ml.x - m_own) * ml.y;
-              }
-        } else {
+        if (!whole) {
           const size_t slot = part_slot(c, it.first);
           if (real) __stcg(part_ml(a, slot) + t * ROWS + r, make_float2(m2, l));
 #pragma unroll 1
@@ -885,21 +936,37 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
             }
           }
-          __threadfence();
         }
-        if (!softmax_sync(bs, syncs)) {
+        if (last && threadIdx.x == 0) {
+          // the others' parts are written
+          bs.parts_there = wait_counter(arrived + 1, others);
+          arrived[0] = 0;
+          arrived[1] = 0;
+          if (!whole) bs.left |= 1 << (c == it.first);
+        }
+        if (!softmax_sync(bs, syncs) || (last && !bs.parts_there)) {
           ok = false;
           break;
         }
-        if (threadIdx.x == 0) {
-          if (whole) {
-            a.tickets[it.first] = 0;
-          } else {
-            __threadfence();
-            if (atomicAdd(a.tickets + it.first, 1) == it.last - it.first) {
-              a.tickets[it.first] = 0;
-              bs.left |= 1 << side;  // all parts are in memory, this one came last
-            }
+        if (!last && threadIdx.x == 0) signal_counter(arrived + 1, 1);  // all warps' parts: the barrier is before it
+        if (whole) {
+          static_assert(DIRECT == 2, "the two parts below");
+          nparts = others;
+          float2 ml[DIRECT];
+#pragma unroll
+          for (int d = 0; d < DIRECT; ++d) {
+            const int o = it.first + d + (it.first + d >= c);  // the d-th other CTA
+            at_part[d] = part_slot(o, it.first);
+            ml[d] = d < others && real ? __ldcg(part_ml(a, at_part[d]) + t * ROWS + r) : make_float2(-INFINITY, 0.f);
+          }
+          float m = max3(m2, ml[0].x, ml[1].x);
+          if (m == -INFINITY) m = 0.f;
+          w_own = ex2_approx(m2 - m);
+          l *= w_own;
+#pragma unroll
+          for (int d = 0; d < DIRECT; ++d) {
+            w_part[d] = ex2_approx(ml[d].x - m);
+            l += w_part[d] * ml[d].y;
           }
         }
       }
@@ -916,14 +983,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          if (it.first != it.last && real) {
+          if (nparts > 0 && real) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w_own);
-            for (int d = it.first; d <= it.last; ++d) {
-              if (d == static_cast<int>(blockIdx.x)) continue;
-              const size_t slot = part_slot(d, it.first);
-              const float w = ex2_approx(__ldcg(part_ml(a, slot) + t * ROWS + r).x - m_own);
-              const float4* o4 = part_o(a, slot) + (cc / 4) * NQ * ROWS + t * ROWS + r;
+#pragma unroll 1
+            for (int d = 0; d < nparts; ++d) {
+              const float w = d ? w_part[1] : w_part[0];
+              const float4* o4 = part_o(a, d ? at_part[1] : at_part[0]) + (cc / 4) * NQ * ROWS + t * ROWS + r;
               float4 x[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) x[e] = __ldcg(o4 + e * NQ * ROWS);
@@ -969,9 +1035,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) report(a.status, DEV_WAIT_TIMEOUT);
     if (warp == PRODUCER_WARP && lane == 0) {
       // the last copy into each buffer may still be in flight
-      if (bs.q_issued > 0) mbar_wait(smem_u32(&bs.q_full), (bs.q_issued - 1) & 1);
-      for (int u = max(0, bs.kv_issued - STAGES); u < bs.kv_issued; ++u)
-        mbar_wait(smem_u32(&bs.kv_full[u % STAGES]), (u / STAGES) & 1);
+      for (int t = 0; t < NQ; ++t)
+        if (bs.q_issued[t] > 0) mbar_wait(smem_u32(&bs.q_full[t]), (bs.q_issued[t] - 1) & 1);
+      for (int u = max(0, bs.k_issued - STAGES); u < bs.k_issued; ++u)
+        mbar_wait(smem_u32(&bs.k_full[u % STAGES]), (u / STAGES) & 1);
+      for (int u = max(0, bs.v_issued - STAGES); u < bs.v_issued; ++u)
+        mbar_wait(smem_u32(&bs.v_full[u % STAGES]), (u / STAGES) & 1);
     }
     __syncthreads();
   }

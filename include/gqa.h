@@ -370,7 +370,8 @@ int gqa_host_stage_release(void* stage);
  * captured step replays with other lengths, tables and contents. The
  * workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled before its first
  * use, and serves one call at a time; its status word is read with
- * gqa_device_status. */
+ * gqa_device_status. After GQA_DEV_WAIT_TIMEOUT zero-fill it again
+ * (gqa_workspace_init). */
 
 #define GQA_PAGED_WORKSPACE_BYTES (64u << 20)
 #define GQA_PAGED_MAX_SEQS 2048   /* sequences per call */
@@ -417,6 +418,8 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
  *   q    [B, n_heads, 128], row b at element b * q_stride, heads dense
  *   out  [B, n_heads, 128] dense
  *   scale finite, > 0 (1 / sqrt(128) for the block's attention)
+ * columns * page_size / 16 * B * n_kv_heads must stay below 2^31, else
+ * GQA_EINVAL.
  * Scores, softmax and sums in fp32; the probabilities enter the value product
  * as two bf16 terms (16 significant bits). */
 int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
@@ -429,7 +432,8 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
  *   q    [N, n_heads, 128], row n at element n * q_stride, heads dense
  *   out  [N, n_heads, 128] dense; rows of no sequence are left as they were
  * Scores, softmax and sums in fp32; the probabilities enter the value product
- * rounded to bf16. */
+ * rounded to bf16. columns * page_size * n_kv_heads must stay below
+ * 858,993,459 (107 million positions for 8 KV heads), else GQA_EINVAL. */
 int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
                       const int32_t* start_pos, const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace,
                       size_t workspace_bytes, void* stream);
