@@ -3,30 +3,62 @@
 // beside the queries ("Llama 3.1 8B · Grouped-query attention": query t sees
 // keys 0..start_pos + t, softmax in fp32, output heads merged h * 128 + d).
 //
-// The tile scheme is that of the dense prefill attention (attn_prefill.cu):
-// a work item is two 128-row Q tiles of one KV head and one sequence, each
-// 128 / n_rep positions x n_rep query heads (row r: position r / n_rep, head
-// r % n_rep; n_rep need not divide 128, the last rows then stay unused), and
-// every 64-key K/V tile is staged once for both. What differs:
-//   * sequences start anywhere in the packed rows and end anywhere in a tile:
-//     items come from a prefix sum over the sequences' tile counts that every
-//     CTA makes for itself, and Q boxes may reach into the next sequence
-//     (rows that are never stored);
-//   * a K/V tile is 64 / min(page, 64) TMA boxes, one lane of the producer
-//     warp each, so that the table look-ups of a tile are one load wide;
-//   * key rows behind the item's last position may hold anything (the next
-//     sequence, a page's unwritten rows): scores there are masked, and the
-//     issuers clear those value rows in shared memory before the product,
-//     because 0 x NaN is NaN. A NaN among the values of an item's own later
-//     positions, which only its earlier rows mask, cannot be cleared for
-//     some rows of a tile and not for others: a row whose result holds a NaN
-//     is computed again by a warp from its visible keys alone.
-//   warp 8        TMA producer
+// Bound by the tensor cores from a few hundred keys on (4 x 128 flops per
+// visible (query, key) pair and head).
+//
+// Tiles. A work item is two 128-row Q tiles of one KV head and one sequence,
+// each 128 / n_rep positions x n_rep query heads (row r: position r / n_rep,
+// head r % n_rep; n_rep need not divide 128, the last rows then stay unused),
+// and every 128-key K/V tile is staged once for both. S = Q K^T (M=128, N=128)
+// goes to TMEM, P = 2^(S scale - max) over its first half as bf16, and
+// O += P V takes P from TMEM and V as an MN-major operand. 512 TMEM columns:
+// S and O of both Q tiles; S is not doubled. Tiles of 64 keys, which leave
+// room for that (the dense prefill's scheme), measured 8% slower over long
+// prompts: a product of N = 64 waits for its operands in shared memory (49
+// cycles measured where the arithmetic takes 32; N = 128: 64 and 64). The last
+// key tile of a Q tile is half as wide where its second half is all masked.
+//
+// Turns. The two Q tiles' issuers alternate step by step (P V of one key tile,
+// S of the next), so that one tile's softmax (~1,400 cycles from S to all of
+// P) runs beside the other's products (~1,430 a step). Left alone they fall
+// into step, both softmaxes and then all products: 3,900 cycles a key tile
+// against 3,150. One issuer for both took 3,700.
+//
+// Ragged sequences. Entries (pairs of Q tiles of a sequence) x KV heads are
+// the items. Up to 320 entries are sorted longest first, and the CTAs claim
+// whole items as they get free (the next one when the last copies of one have
+// been issued). Where whole items dealt out longest first would leave the
+// fullest CTA more than a join behind the mean (few or long items: a chunk
+// after a long prefix), the key tiles of all items are cut into one equal
+// range per CTA instead, at least MIN_TILES each: 103.6 against 111.5 us for
+// 1,024 tokens after 7,168 (128 items on 152 SMs). Parts of an item are joined
+// in CTA order by the CTA that arrives last at its count: it waits only for
+// CTAs that have arrived, which are running and about to write.
+//
+// Masked and foreign values. Q boxes may reach into the next sequence (rows
+// that are never stored), K and V boxes into the next sequence's rows, a
+// page's unwritten rows, or past the end (zeros): scores there are masked, and
+// the issuers clear those value rows in shared memory before the product,
+// because 0 x NaN is NaN. A NaN among the values of an item's own later
+// positions, which only its earlier rows mask, cannot be cleared for some rows
+// of a tile and not for others: a row whose result is not finite, with such
+// values behind it, is computed again by a warp from its visible keys alone.
+//
+//   warp 8        plans the items, TMA producer: a K/V tile is 128 / min(page,
+//                 128) boxes, one lane each, so that the table look-ups of a
+//                 tile are one load wide
 //   warps 9, 10   MMA issuers, one per Q tile
 //   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
-// Every barrier wait is bounded; a wait that gives up records
-// DEV_WAIT_TIMEOUT, lets issued copies and products finish (bounded) and frees
-// TMEM before the CTA exits.
+// P is rounded to bf16 (the product takes no wider operand); sums are fp32 of
+// the unrounded values. O is rescaled only when a row's max grows by more than
+// 2^8 over the max its P values were taken against.
+// Every wait is bounded; one that gives up records DEV_WAIT_TIMEOUT, lets
+// issued copies and products finish (bounded) and frees TMEM before the CTA
+// exits.
+// Measured: 426 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,356
+// TFLOP/s of 1,962 measured), 101 us for 1,024 tokens after 7,168, 35.6 for
+// 2,048 tokens, 6.9 for 17. What bounds the long ones is the alternation: per
+// key tile the tensor pipe works 2 x 1,024 of 3,150 cycles.
 #include <math.h>
 
 #include "kernels.h"
@@ -51,7 +83,9 @@ constexpr int MAX_SORT = 320;             // entries that are sorted, or cut int
 constexpr int BARS_BYTES = 5120;
 constexpr int DIRECT = 2;                 // other parts of an item that are added in its epilogue at most
 constexpr int PRE_OFF = BAR_OFF + BARS_BYTES;
-constexpr int SMEM_BYTES = PRE_OFF + (PAGED_MAX_SEQS + 1) * 4 + 1024;
+constexpr int OUT_OFF = (PRE_OFF + (PAGED_MAX_SEQS + 1) * 4 + 127) / 128 * 128;
+constexpr int OUT_WARP = 32 * 64;         // staging of 32 output rows x 32 columns, per softmax warp
+constexpr int SMEM_BYTES = OUT_OFF + 8 * OUT_WARP + 1024;
 constexpr int THREADS = 352;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                  // items handed from the producer to the other warps
@@ -203,14 +237,28 @@ __device__ __forceinline__ long long key_row(const PackedPrefillParams& a, int b
 
 // One output row from its visible keys 0..lim alone, by a whole warp, in
 // fp32: 32 keys at a time, a key a lane for the scores, 4 dims a lane for the
-// values. For rows that share a tile with non-finite values they do not see.
+// values. For rows whose result is not finite and that share tiles with later
+// keys of their item (up to kv_end): nothing is done where those values are
+// all finite, because the row's own keys then made it so.
 __device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int row0, int g, int start, int pos,
-                                        int head) {
+                                        int head, int kv_end) {
   const size_t row = static_cast<size_t>(row0) + pos;
   const __nv_bfloat16* q = a.q + static_cast<long long>(row) * a.q_stride + head * HEAD_DIM;
   __nv_bfloat16* dst = a.out + (row * a.n_heads + head) * HEAD_DIM;
   const int lim = start + pos;
   const int lane = threadIdx.x & 31;
+  bool dirty = false;
+  for (int j = lim + 1; j < kv_end && !dirty; j += 4) {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (j + k >= kv_end) continue;
+      const uint2 v = *(reinterpret_cast<const uint2*>(a.pages.v + key_row(a, b, row0, g, j + k, true)) + lane);
+      x += bf16_lo(v.x) * 0.f + bf16_hi(v.x) * 0.f + bf16_lo(v.y) * 0.f + bf16_hi(v.y) * 0.f;
+    }
+    dirty = __any_sync(0xffffffffu, x != x);
+  }
+  if (!dirty) return;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 <= lim; j0 += 32) {
     float s = -INFINITY;
@@ -363,7 +411,7 @@ __device__ __forceinline__ void join(const PackedPrefillParams& a, Bars& bs, con
   for (int r = tid >> 5; r < total; r += THREADS / 32) {
     int row, pos, head;
     place(r, row, pos, head);
-    if (bs.row_bad[row] && it.start + pos < it.kv_end - 1) masked_row(a, it.b, it.row0, it.g, it.start, pos, head);
+    if (bs.row_bad[row] && it.start + pos < it.kv_end - 1) masked_row(a, it.b, it.row0, it.g, it.start, pos, head, it.kv_end);
   }
   __syncthreads();  // the rows' figures are free again
 }
@@ -791,11 +839,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool real = used && pos < it.T;
       const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
       const int lim = used ? min(it.start + pos, it.kv_end - 1) : -1;  // last key this row sees
-      __nv_bfloat16* dst = a.out + (static_cast<size_t>(it.row0) + pos) * a.n_heads * HEAD_DIM +
-                           static_cast<size_t>(it.g * nrep + hh) * HEAD_DIM;
+      // the item's first output row, and this thread's elements behind it (-1: no row)
+      __nv_bfloat16* out = a.out + (static_cast<size_t>(it.row0) + it.q0) * a.n_heads * HEAD_DIM;
+      const int dst_off = real ? ((pos - it.q0) * a.n_heads + it.g * nrep + hh) * HEAD_DIM : -1;
       if (it.n == 0 && real) {
-#pragma unroll
-        for (int e = 0; e < HEAD_DIM / 8; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int e = 0; e < HEAD_DIM / 8; ++e) reinterpret_cast<uint4*>(out + dst_off)[e] = make_uint4(0, 0, 0, 0);
       }
       float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
       float l = 0.f;
@@ -821,6 +870,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int cc = 0; cc < HALF; ++cc)
               if (h * HALF + cc > vis) sr[cc] = __float_as_uint(-INFINITY);
           }
+          __syncwarp();  // the TMEM accesses want the warp converged
         };
         float mx = -INFINITY, m1 = mx, m2 = mx, m3 = mx;
 #pragma unroll
@@ -880,6 +930,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bs.p_full[t][h]));
+          __syncwarp();
         }
         sum2 = add2(sum2, sum3);
         l = l * alpha + (sum2.x + sum2.y);
@@ -918,6 +969,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!whole) {
           const size_t slot = part_slot(c, it.first);
           if (real) __stcg(part_ml(a, slot) + t * ROWS + r, make_float2(m2, l));
+          __syncwarp();
 #pragma unroll 1
           for (int cc = 0; cc < HEAD_DIM; cc += 32) {
             uint32_t o[32];
@@ -935,6 +987,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __stcg(o4 + e * NQ * ROWS, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
             }
+            __syncwarp();
           }
         }
         if (last && threadIdx.x == 0) {
@@ -971,7 +1024,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (whole && (n_t > 0 || it.first != it.last)) {
+        __syncwarp();
         const float inv = 1.f / l;
+        uint8_t* turn_at = smem + OUT_OFF + warp * OUT_WARP;
         float chk = 0.f;  // NaN when any value of the row is not finite
 #pragma unroll 1
         for (int cc = 0; cc < HEAD_DIM; cc += 32) {
@@ -1004,24 +1059,34 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) chk = fmaf(__uint_as_float(o[e]), 0.f, chk);
-          if (real) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
+          // Rows are turned round in shared memory, so that four lanes store
+          // 64 bytes of a row (a lane storing its own row's 16 bytes at a
+          // time touches 32 lines an instruction: 1.8 us an item).
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
-              w.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
-              w.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
-              w.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
-              d4[e] = w;
-            }
+          for (int e = 0; e < 4; ++e) {
+            uint4 w;
+            w.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+            w.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+            w.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+            w.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+            *reinterpret_cast<uint4*>(turn_at + lane * 64 + ((e ^ (lane >> 1 & 3)) << 4)) = w;
           }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 8 * e + (lane >> 2), piece = lane & 3;
+            const uint4 w = *reinterpret_cast<const uint4*>(turn_at + row * 64 + ((piece ^ (row >> 1 & 3)) << 4));
+            const int off = __shfl_sync(0xffffffffu, dst_off, row);
+            if (off >= 0)
+              reinterpret_cast<uint4*>(out + off + cc)[piece] = w;
+          }
+          __syncwarp();
         }
         unsigned again = __ballot_sync(0xffffffffu, real && chk != chk && lim < it.kv_end - 1);
         for (; again; again &= again - 1) {
           const int src = __ffs(again) - 1;
           masked_row(a, it.b, it.row0, it.g, it.start, __shfl_sync(0xffffffffu, pos, src),
-                     it.g * nrep + __shfl_sync(0xffffffffu, hh, src));
+                     it.g * nrep + __shfl_sync(0xffffffffu, hh, src), it.kv_end);
         }
       }
       cs += n_t;

@@ -124,6 +124,11 @@ def test_prefill_refuses_its_own_arguments(lib):
     assert packed(lib, k=FAKE + 8) == -2
 
 
+def test_prefill_refuses_more_key_tiles_than_it_can_count(lib):
+    p = pages(columns=1 << 23, table_stride=1 << 23)    # 2^27 positions, 8 KV heads
+    assert prefill(lib, p) == -1
+
+
 def test_no_tokens_is_no_launch(lib):
     assert append(lib, N=0) == 0 and lib.gqa_last_launch_count() == 0
     assert prefill(lib, N=0) == 0 and packed(lib, N=0) == 0 and lib.gqa_last_launch_count() == 0
@@ -289,6 +294,48 @@ def test_decode_ranges_cover_every_chunk_once_and_tickets_count(lens, n_kv, warp
     assert covered == total
     for arrivals in tickets.values():
         assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][1]
+
+
+@pytest.mark.parametrize("tiles", [[64] * 4, [57, 58, 59, 60, 61, 62, 63, 64], [157, 1, 0, 3], [469], [1, 1, 20]])
+@pytest.mark.parametrize("n_kv", [1, 2, 8])
+def test_prefill_ranges_cover_every_key_tile_once(tiles, n_kv):
+    """Equal ranges of key tiles: every tile of every item in one part; the
+    parts of an item come from the CTAs its first and last unit lie in, one
+    each, at most two shared items per CTA, begun before it and going on behind."""
+    cum = [0]
+    for n in tiles:
+        cum.append(cum[-1] + n)
+    units = cum[-1] * n_kv
+    parts = min(152, units // 3)
+    if parts < 2:
+        return
+    split = Split(units, parts)
+    seen, slots = {}, set()
+    for c in range(parts):
+        u, end = split.start(c), split.start(c + 1)
+        assert end > u
+        while u < end:
+            e = max(i for i in range(len(tiles)) if cum[i] * n_kv <= u)
+            n = cum[e + 1] - cum[e]
+            assert n > 0
+            g, j0 = divmod(u - cum[e] * n_kv, n)
+            base = u - j0
+            j1 = min(n, end - base)
+            first, last = split.holder(base), split.holder(base + n - 1)
+            assert first <= c <= last and (j0 == 0) == (c == first)
+            if first != last:
+                slot = 2 * c + (c == first)
+                assert slot not in slots
+                slots.add(slot)
+            seen.setdefault((e, g), []).append((j0, j1, c, first, last))
+            u = base + j1
+    for (e, g), got in seen.items():
+        at = 0
+        for j0, j1, c, first, last in got:
+            assert j0 == at and j1 > j0
+            at = j1
+        assert at == tiles[e] and [x[2] for x in got] == list(range(got[0][3], got[0][4] + 1))
+    assert len(seen) == n_kv * sum(n > 0 for n in tiles)
 
 
 def sequence_of(cu, B, m):

@@ -364,6 +364,34 @@ def test_packed_prefill_rows_do_not_see_later_keys(gen, ws):
     assert torch.isnan(out[150:]).all()
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("new,prefix,at", [(100, 6000, 6050), (100, 6000, 3000), (64, 500, 563), (1, 9000, 9000)])
+def test_paged_prefill_shared_items_do_not_see_later_values(gen, ws, value, new, prefix, at):
+    # few items after a long prefix: their keys are split over CTAs and joined
+    k_pages, v_pages, table, rows = fill_cache(gen, [prefix + new, 40], 64, 2)
+    p, r = P.slots(table, 64, 0, at, 1)
+    v_pages[p, r, 1, 3] = value
+    q = P.normal(gen, new + 2, 8, P.D)
+    out = G.paged_prefill(q, offsets([new, 2]), ints([prefix, 38]), k_pages, v_pages, table, workspace=ws)
+    assert G.device_status(ws) == 0
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[max(0, at - prefix):new, 4:, 3] = True
+    assert (torch.isnan(out[hit]) if math.isnan(value) else out[hit] == value).all()
+    for sl, (k, v), first in ((slice(0, new), rows[0], prefix), (slice(new, new + 2), rows[1], 38)):
+        ref, mean, size = P.attend64(q[sl], k, v, first)
+        tol = P.bound(ref, mean, size, k.shape[0], P.P_ONE_TERM)
+        keep = ~hit[sl]
+        P.check(out[sl][keep], ref[keep], tol[keep], f"rows {sl}")
+
+
+def test_paged_prefill_shared_items_and_unused_slots(gen, ws):
+    run_paged_prefill(gen, ws, 8, 2, 64, [5, 33, 1, 0, 70, 2], [4000, -1, 12000, 100, -1, 0])
+
+
+def test_paged_prefill_one_item_over_every_cta(gen, ws):
+    run_paged_prefill(gen, ws, 16, 1, 128, [8], [60000])
+
+
 # ------------------------------------------------------------------ errors on the device
 
 def test_bad_positions_are_reported_and_skipped(gen, ws):
