@@ -31,7 +31,7 @@
 // fullest CTA more than a join behind the mean (few or long items: a chunk
 // after a long prefix), the key tiles of all items are cut into one equal
 // range per CTA instead, at least MIN_TILES each: 103.6 against 111.5 us for
-// 1,024 tokens after 7,168 (128 items on 152 SMs). Parts of an item are joined
+// 1,024 tokens after 7,168 (128 items on 152 SMs; both before later steps). Parts of an item are joined
 // in CTA order by the CTA that arrives last at its count: it waits only for
 // CTAs that have arrived, which are running and about to write.
 //
@@ -55,10 +55,10 @@
 // Every wait is bounded; one that gives up records DEV_WAIT_TIMEOUT, lets
 // issued copies and products finish (bounded) and frees TMEM before the CTA
 // exits.
-// Measured: 426 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,356
-// TFLOP/s of 1,962 measured), 101 us for 1,024 tokens after 7,168, 35.6 for
-// 2,048 tokens, 6.9 for 17. What bounds the long ones is the alternation: per
-// key tile the tensor pipe works 2 x 1,024 of 3,150 cycles.
+// Measured: 399 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,448
+// TFLOP/s of 1,962 measured), 98 us for 1,024 tokens after 7,168, 35.1 for
+// 2,048 tokens, 7.0 for 17. What bounds the long ones is the alternation: per
+// key tile the tensor pipe works 2 x 1,024 of 2,900 cycles.
 #include <math.h>
 
 #include "kernels.h"
@@ -736,6 +736,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
       for (int j = 0; j <= it.n; ++j, ++step) {
+        // everything S_j needs but its turn, so that it follows P_{j-1} V_{j-1} at once
+        const unsigned uk = u0 + j, sk = uk % STAGES;
+        if (j < it.n && !wait(bs.k_full[sk], (uk / STAGES) & 1)) break;
+        if (j == 0 && n_t > 0 && !wait(bs.q_full[t], qi & 1)) break;
+        const uint32_t kt = sbase + K_OFF + sk * KV_TILE;
+        const uint32_t idesc = end_t - (it.j0 + j) * KT > HALF ? idesc_s : idesc_sh;
         if (j >= 1) {
           const int i = j - 1, tile = it.j0 + i;
           const unsigned u = u0 + i, s = u % STAGES;
@@ -781,12 +787,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         if (j < n_t) {
-          const unsigned u = u0 + j, s = u % STAGES;
-          if (j == 0 && !wait(bs.q_full[t], qi & 1)) break;
-          if (!wait(bs.k_full[s], (u / STAGES) & 1)) break;
           tc_fence_after();
-          const uint32_t kt = sbase + K_OFF + s * KV_TILE;
-          const uint32_t idesc = end_t - (it.j0 + j) * KT > HALF ? idesc_s : idesc_sh;
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
@@ -807,9 +808,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           release(bs.v_empty[(u0 + j - 1) % STAGES], j <= n_t);
         }
         if (j < it.n) {
-          const unsigned u = u0 + j, s = u % STAGES;
-          if (j >= n_t && !wait(bs.k_full[s], (u / STAGES) & 1)) break;
-          release(bs.k_empty[s], j < n_t);
+          release(bs.k_empty[sk], j < n_t);
         }
       }
       if (!ok) break;
@@ -848,6 +847,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
       float l = 0.f;
+      float m_limit = -INFINITY, neg = 0.f;  // max that P is still taken against m_ref with; -m_ref in log2 units
       for (int j = 0; j < n_t; ++j) {
         // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t]), (cs + j) & 1))) {
@@ -886,24 +886,30 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         mx = fmaxf(max3(mx, m1, m2), m3);
-        float alpha = 1.f;
-        const bool grow = mx > m_ref && (m_ref == -INFINITY || (mx - m_ref) * scale > RESCALE_LOG2);
-        if (grow) {
-          alpha = m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - mx) * scale);
-          m_ref = mx;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, grow)) {
-#pragma unroll 1
-          for (int cc = 0; cc < HEAD_DIM; cc += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_at + cc, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(o_at + cc, o);
+        // the max outgrew the reference (always at a row's first keys)
+        if (__any_sync(0xffffffffu, mx > m_limit)) {
+          float alpha = 1.f;
+          if (mx > m_limit) {
+            alpha = m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - mx) * scale);
+            m_ref = mx;
+            m_limit = mx + RESCALE_LOG2 / scale;
+            neg = -mx * scale;
+            l *= alpha;
           }
+          if (j > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+              uint32_t o[32];
+              __syncwarp();
+              tmem_ld32(o_at + cc, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(o_at + cc, o);
+            }
+          }
+          __syncwarp();
         }
-        const float neg = m_ref == -INFINITY ? 0.f : -m_ref * scale;
         // exponent arguments and the row sum two columns per instruction
         const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
         float2 sum2 = make_float2(0.f, 0.f), sum3 = sum2;
@@ -933,7 +939,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         sum2 = add2(sum2, sum3);
-        l = l * alpha + (sum2.x + sum2.y);
+        l += sum2.x + sum2.y;
       }
       if (!ok) break;
       if (n_t > 0) {
