@@ -29,13 +29,19 @@
 //     shared memory among the CTA's warps, then, where several CTAs hold
 //     parts, by the CTA that arrives last at a ticket, in CTA order: the
 //     result does not depend on the order of arrival, and no CTA waits.
-//   * Joining across CTAs (fence, ticket, read back) takes 2 to 3 us, what a
-//     CTA streams about 16 chunks in. Where one CTA per (sequence, KV head)
-//     is no more than that behind the equal ranges, the ranges are those
-//     (16 sequences of 1,001 rows, 8 KV heads: 17.3 us against 22.9).
-// Measured (GB300, 6.8 TB/s copied): 172.3 us for 1.108 GB (64 sequences of
-// up to 8,192 rows), 87.5 for 537 MB (one of 131,072), 16.2 for 66 MB (16 of
-// 1,001), 3.5 for one sequence of 16 rows. Head-major pages ([page, KV head,
+//   * Joining across CTAs (fence, ticket, read back) takes about 4 us. Where
+//     one CTA per (sequence, KV head) is no more than that behind the equal
+//     ranges, the ranges are those. Both measured, own / equal: 16 sequences
+//     of 2,001 rows and 8 KV heads 25.7 / 30.4 us, of 8,192 rows 83.4 / 87.5,
+//     12 of 4,001 37.2 / 39.4, 8 of 2,001 20.1 / 20.6, 4 of 1,001 11.7 / 10.2,
+//     one of 2,001 18.2 / 9.6. The longest sequence's time alone on a CTA, or
+//     the batch's at the memory's rate, tells them apart.
+//   * Code that runs once a CTA, and the join that runs in a few CTAs, wait
+//     for instructions more than for data: their loops are not unrolled.
+// Measured (GB300, 6.8 TB/s copied): 171.8 us for 1.108 GB (64 sequences of
+// up to 8,192 rows), 87.0 for 537 MB (one of 131,072), 48.5 for 263 MB (16 of
+// 1,001, 32 KV heads), 16.2 for 66 MB (8 KV heads), 3.4 for one sequence of
+// 16 rows. Head-major pages ([page, KV head,
 // row]) are 2 to 4% faster than [page, row, KV head]: longer runs per CTA.
 #include <math.h>
 
@@ -51,7 +57,11 @@ constexpr int TILE_BYTES = KEYS * ROW_BYTES;      // K or V of a chunk
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int STAGES = 2;
 constexpr int WARPS = 8;
-constexpr int OWN_CHUNKS = 16;                    // what joining across CTAs costs, in chunks of one CTA's stream
+// In 1/800 us, what a chunk takes at the whole memory's rate: a chunk of a CTA
+// by itself (it streams 9 or 10 a us, 64 to 128 KB in flight), and joining
+// across CTAs (about 4 us).
+constexpr float ALONE = 85.f, JOIN_COST = 3200.f;
+constexpr int BATCH = 8;                          // partials a warp has in flight when it joins
 constexpr int PART = HEAD_DIM + 2;                // floats of a partial row: o, max, sum
 
 // Row r, 16-byte piece c of a 256-byte-row tile: eight rows of one piece fall
@@ -132,6 +142,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   __shared__ Part parts[2 * WARPS];  // each warp's two, first = -1: none
   __shared__ int warp_sum[WARPS], warp_max[WARPS];
   __shared__ int is_last[2];
+  __shared__ Part joint[2];  // of the shared segments: first and last CTA, first output row
 
   // nothing is read or written before the previous kernel of the stream is done
   pdl_trigger();
@@ -142,6 +153,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     const int per = (p.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
     int sum = 0, most = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int s = p.start[b];
       const bool ok = s >= 0 && s < p.pages.capacity();
@@ -171,6 +183,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
       total += warp_sum[w];
       longest = max(longest, warp_max[w]);
     }
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       run += pre[b + 1];
       pre[b + 1] = run;
@@ -178,8 +191,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     __syncthreads();
   }
   // rows of sequences without keys
+#pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
     if (pre[b + 1] == pre[b])
+#pragma unroll 1
       for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
         reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
 
@@ -190,7 +205,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   const Split split(total, ctas);
   // One CTA per (sequence, KV head) instead of equal ranges where that costs
   // less than joining parts across CTAs.
-  const bool own = p.B * p.n_kv <= static_cast<int>(gridDim.x) && longest <= split.each + OWN_CHUNKS;
+  const float memory = static_cast<float>(total);
+  const bool own = p.B * p.n_kv <= static_cast<int>(gridDim.x) &&
+                   fmaxf(static_cast<float>(longest) * ALONE, memory) <=
+                       fmaxf(static_cast<float>(split.each) * ALONE, memory) + JOIN_COST;
   int c0, c1;
   if (own) {
     if (static_cast<int>(blockIdx.x) >= p.B * p.n_kv) return;
@@ -417,6 +435,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     if (lane < 2 * W) mine = parts[lane];
     const unsigned peers = __match_any_sync(0xffffffffu, mine.first);
     unsigned heads = __ballot_sync(0xffffffffu, mine.first >= 0 && __ffs(peers) - 1 == lane);
+#pragma unroll 1
     for (int k = 0; heads; heads &= heads - 1) {
       const int e = __ffs(heads) - 1;
       const unsigned members = __shfl_sync(0xffffffffu, peers, e);
@@ -425,6 +444,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
       const int side = seg.first < c0 ? 0 : seg.end > c1 ? 1 : 2;  // 2: all of it is here
       if (side == 0) cross[0] = seg;
       if (side == 1) cross[1] = seg;
+#pragma unroll 1
       for (int r = 0; r < n_rep; ++r, ++k) {
         if (k % W != warp) continue;
         float m_e = -INFINITY, l_e = 0.f;
@@ -441,6 +461,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (unsigned g = members; g; g &= g - 1) {
           const int f = __ffs(g) - 1;
           const float w = __shfl_sync(0xffffffffu, w_e, f);
@@ -468,23 +489,27 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   __syncthreads();
   if (threadIdx.x < 2) {
     const Part seg = threadIdx.x ? cross[1] : cross[0];
-    int mine = 0;
+    int last = 0;
     if (seg.first >= 0) {
       const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
       __threadfence();
-      mine = atomicAdd(p.tickets + a, 1) == z - a;
-      if (mine) p.tickets[a] = 0;
+      last = atomicAdd(p.tickets + a, 1) == z - a;
+      if (last) p.tickets[a] = 0;
       __threadfence();
+      joint[threadIdx.x] = {a, z, seg.row};
     }
-    is_last[threadIdx.x] = mine;
+    is_last[threadIdx.x] = last;
   }
   __syncthreads();
-  // per query head `ways` warps share the partials, then the first of them adds up
+  // Per query head `ways` warps share the partials, then the first of them
+  // adds up. Few CTAs come here and their instruction caches are cold: the
+  // loops are kept short (16 partials unrolled took as long as one at a time).
   const int ways = max(1, W / n_rep);
+#pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     if (!is_last[side]) continue;
-    const Part seg = cross[side];
-    const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
+    const int a = joint[side].first, z = joint[side].end;
+#pragma unroll 1
     for (int r0 = 0; r0 < n_rep; r0 += W / ways) {
       const int r = r0 + warp / ways, way = warp % ways;
       const bool on = warp / ways < W / ways && r < n_rep;
@@ -492,21 +517,37 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (on) {
         // the part of its first CTA goes on behind that CTA (slot 1), the others began before theirs (slot 0)
-        auto at = [&](int c) { return (2LL * c + (c == a)) * n_rep + r; };
-        for (int c = a + lane; c <= z; c += 32) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c)).x);
+        auto at = [&](int c) { return (2 * c + (c == a)) * n_rep + r; };
+        const float2* mls = reinterpret_cast<const float2*>(p.part_ml);
+        const float4* os = reinterpret_cast<const float4*>(p.part_o) + lane;
+#pragma unroll 1
+        for (int c = a + lane; c <= z; c += 32) m = fmaxf(m, __ldcg(mls + at(c)).x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-        for (int c = a + way; c <= z; c += ways) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(c));
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part_o + at(c) * HEAD_DIM) + lane);
-          const float w = ex2_approx(ml.x - ref);
-          l += w * ml.y;
-          o.x += w * x.x;
-          o.y += w * x.y;
-          o.z += w * x.z;
-          o.w += w * x.w;
+#pragma unroll 1
+        for (int c0 = a + way; c0 <= z; c0 += BATCH * ways) {
+          float2 ml[BATCH];
+          float4 x[BATCH];
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const int c = c0 + k * ways;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c <= z) {
+              ml[k] = __ldcg(mls + at(c));
+              x[k] = __ldcg(os + at(c) * (HEAD_DIM / 4));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) {
+            const float w = ex2_approx(ml[k].x - ref);
+            l += w * ml[k].y;
+            o.x += w * x[k].x;
+            o.y += w * x[k].y;
+            o.z += w * x[k].z;
+            o.w += w * x[k].w;
+          }
         }
       }
       if (ways > 1) {
@@ -519,6 +560,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         }
         __syncthreads();
         if (on && !way)
+#pragma unroll 1
           for (int g = 1; g < ways; ++g) {
             const float* row = mine + g * PART;
             l += row[HEAD_DIM];
@@ -530,7 +572,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
             o.w += y.y;
           }
       }
-      if (on && !way) store_row(p.out, seg.row + r, o, 1.f / l);
+      if (on && !way) store_row(p.out, joint[side].row + r, o, 1.f / l);
     }
   }
 }
