@@ -1,5 +1,6 @@
 // C ABI of the paged serving operators (declared in include/gqa.h): argument
-// validation on the host, workspace layout, tensor maps and one launch each.
+// validation on the host, workspace layout, tensor maps and one launch each (the
+// prefill attention's join is a second).
 #include <math.h>
 
 #include "api_internal.h"
@@ -9,19 +10,21 @@ using namespace gqa;
 namespace {
 
 // Workspace: the status word and its 256 bytes (the prefill attention's claims
-// among them), the tickets, the partials (two per CTA) of the decode or of the
-// prefill attention.
+// among them), the tickets, the items that the prefill attention's second
+// kernel joins, the partials (two per CTA) of the decode or prefill attention.
 constexpr size_t CLAIMS_OFFSET = 64;
 constexpr size_t TICKETS_OFFSET = 256;
 constexpr size_t PREFILL_ROWS = 256;  // query rows of an item
 constexpr size_t PREFILL_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * 2 * 4;
 constexpr size_t PREFILL_O_BYTES = static_cast<size_t>(2) * REF_SMS * PREFILL_ROWS * HEAD_DIM * 4;
-constexpr size_t PART_ML_OFFSET = TICKETS_OFFSET + 2048;
+constexpr size_t JOINS_OFFSET = TICKETS_OFFSET + 2048;
+constexpr size_t JOINS_BYTES = 16384;
+constexpr size_t PART_ML_OFFSET = JOINS_OFFSET + JOINS_BYTES;
 static_assert(PART_ML_OFFSET + PREFILL_ML_BYTES + PREFILL_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 constexpr size_t PART_ML_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * 2 * 4;
 constexpr size_t PART_O_OFFSET = (PART_ML_OFFSET + PART_ML_BYTES + 255) / 256 * 256;
 constexpr size_t PART_O_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * HEAD_DIM * 4;
-static_assert(REF_SMS * 2 * 4 <= PART_ML_OFFSET - TICKETS_OFFSET, "tickets");
+static_assert(REF_SMS * 2 * 4 <= JOINS_OFFSET - TICKETS_OFFSET, "tickets");
 static_assert(PART_O_OFFSET + PART_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 static_assert(GQA_PAGED_MAX_SEQS == PAGED_MAX_SEQS && GQA_PAGED_MAX_REP == PAGED_MAX_REP, "limits");
 
@@ -168,7 +171,7 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
 
 static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, int n_kv, const int32_t* cu_tokens,
                         int B, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream,
-                        PackedPrefillParams& p, int kv_rows, int kv_pages, int box_rows) {
+                        PackedPrefillParams& p, int kv_rows, int kv_pages, int box_rows, long long most_keys) {
   if (!q || !cu_tokens || !out || N < 0 || N > MAX_TOKENS || B <= 0 || B > PAGED_MAX_SEQS) return GQA_EINVAL;
   int r = check_heads(n_heads, n_kv);
   if (r == GQA_OK) r = check_scale(scale);
@@ -195,6 +198,8 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   p.part_o = reinterpret_cast<float*>(ws + PART_ML_OFFSET + PREFILL_ML_BYTES);
   p.ctas = launch_sms();
   const int n_rep = n_heads / n_kv;
+  if (packed_prefill_may_join(N, n_rep, most_keys)) p.joins = ws + JOINS_OFFSET;
+  if (packed_prefill_join_bytes(p.ctas) > JOINS_BYTES) return fail_cuda(cudaErrorInvalidConfiguration);
   PackedPrefillMaps maps;
   const cuuint64_t dims[3] = {HEAD_DIM, static_cast<cuuint64_t>(n_heads), static_cast<cuuint64_t>(N)};
   const cuuint64_t strides[2] = {HEAD_DIM * 2, static_cast<cuuint64_t>(q_stride) * 2};
@@ -209,6 +214,10 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   prof_mark(0, s);
   r = launched(launch_packed_prefill(maps, p, s));
   prof_mark(1, s);
+  if (r == GQA_OK && p.joins) {
+    r = launched(launch_packed_prefill_join(p, s));
+    prof_mark(2, s);
+  }
   return r;
 }
 
@@ -227,7 +236,8 @@ int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, c
   p.start = start_pos;
   return prefill_call(q, q_stride, N, n_heads, pages->n_kv_heads, cu_tokens, B, scale, out, workspace,
                       workspace_bytes, stream, p, pages->page_size, pages->num_pages,
-                      prefill_box_rows(pages->page_size));
+                      prefill_box_rows(pages->page_size),
+                      static_cast<long long>(pages->columns) * pages->page_size);
 }
 
 int gqa_packed_prefill(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
@@ -246,7 +256,7 @@ int gqa_packed_prefill(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, i
   p.pages.page_stride = k_stride;
   p.v_row_stride = v_stride;
   return prefill_call(q, q_stride, N, n_heads, n_kv_heads, cu_tokens, B, scale, out, workspace, workspace_bytes,
-                      stream, p, N, 1, PACKED_TILE);
+                      stream, p, N, 1, PACKED_TILE, N);
 }
 
 }  // extern "C"

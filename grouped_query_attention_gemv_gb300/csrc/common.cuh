@@ -205,18 +205,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return true;
 }
 
-// mbar_wait for a warp that is far ahead of the others: it sleeps between its
-// looks, so that they cost the working warps of its scheduler nothing.
-__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (global_ns() - t0 > WAIT_LIMIT_NS) return false;
-    __nanosleep(500);
-  }
-  return true;
-}
-
 // mbar_wait that also gives up (false) as soon as *abort, a shared-memory
 // flag a producer raises when it stops issuing, becomes non-zero: consumers
 // then leave a phase whose loads will not come without waiting out the limit.

@@ -251,10 +251,10 @@ constexpr int PAGED_MAX_REP = 16;     // query heads per KV head
 // the previous kernel of the stream ends. Only for kernels that execute
 // pdl_wait() before they touch memory.
 template <class... P, class... A>
-cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
                           const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -338,11 +338,13 @@ struct PackedPrefillParams {
   long long q_stride;
   float scale_log2;
   __nv_bfloat16* out;       // [N][n_heads][128]
-  // parts of items that several CTAs share: [2 * ctas][256 rows][128], their
-  // (max in log2 units, sum), two counts per CTA (parts that arrived, parts
-  // written); the claims of whole items and the count of CTAs that are done.
-  // Counts zero-filled, left so.
+  // Parts of items that several CTAs share: [2 * ctas][32 column groups][256
+  // rows at most][4], their (max in log2 units, sum); the items that the second
+  // kernel joins (packed_prefill_join_bytes; null: there are none); two counts
+  // per CTA (parts that arrived, parts written); the claims of whole items and
+  // the count of CTAs that are done. Counts zero-filled, left so.
   float *part_o, *part_ml;
+  void* joins;
   int *tickets, *claims;
   int* status;
   int ctas;
@@ -356,6 +358,10 @@ struct PackedPrefillMaps {
 constexpr int PACKED_TILE = 128;  // keys of a tile
 __host__ __device__ constexpr int prefill_box_rows(int page_size) { return page_size < PACKED_TILE ? page_size : PACKED_TILE; }
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& p, cudaStream_t s);
+// With p.joins set, the join follows.
+cudaError_t launch_packed_prefill_join(const PackedPrefillParams& p, cudaStream_t s);
+bool packed_prefill_may_join(int N, int n_rep, long long most_keys);
+size_t packed_prefill_join_bytes(int ctas);
 
 cudaError_t launch_rope_table(float* rope, int rows, double theta, int scaled, double factor, double lo,
                               double hi, double ctx, cudaStream_t s);

@@ -27,13 +27,20 @@
 // Ragged sequences. Entries (pairs of Q tiles of a sequence) x KV heads are
 // the items. Up to 320 entries are sorted longest first, and the CTAs claim
 // whole items as they get free (the next one when the last copies of one have
-// been issued). Where whole items dealt out longest first would leave the
-// fullest CTA more than a join behind the mean (few or long items: a chunk
-// after a long prefix), the key tiles of all items are cut into one equal
-// range per CTA instead, at least MIN_TILES each: 103.6 against 111.5 us for
-// 1,024 tokens after 7,168 (128 items on 152 SMs; both before later steps). Parts of an item are joined
-// in CTA order by the CTA that arrives last at its count: it waits only for
-// CTAs that have arrived, which are running and about to write.
+// been issued). Whole items dealt out longest first may leave the fullest CTA
+// far behind the mean (few or long items: a chunk after a long prefix). The key
+// tiles of all items can be cut into one equal range per CTA instead, two ways,
+// and the cheapest of the three by the costs below is taken:
+//   - Ranges of half the longest item at least. An item then has three parts
+//     at most, and the CTA that arrives last at its count adds the others to
+//     its own in its epilogue: it waits only for CTAs that have arrived, which
+//     are running and about to write. 1,024 tokens after 7,168 (128 items on
+//     152 SMs): 100 us, 112 with all parts left to a second kernel.
+//   - Shorter ranges, whose items' parts a second kernel joins, in CTA order:
+//     25 us for 40 tokens after 8,000 (8 heads, 2 KV heads), where a join by
+//     the last CTA took 47; 33 for 256 after 4,000 (32 and 8 heads) against 52.
+//     Empty, that kernel takes 2 us, so it is not launched where no sequence
+//     can have more than 2,048 keys.
 //
 // Masked and foreign values. Q boxes may reach into the next sequence (rows
 // that are never stored), K and V boxes into the next sequence's rows, a
@@ -55,8 +62,8 @@
 // Every wait is bounded; one that gives up records DEV_WAIT_TIMEOUT, lets
 // issued copies and products finish (bounded) and frees TMEM before the CTA
 // exits.
-// Measured: 399 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,448
-// TFLOP/s of 1,962 measured), 98 us for 1,024 tokens after 7,168, 35.1 for
+// Measured: 400 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,445
+// TFLOP/s of 1,962 measured), 100 for 1,024 tokens after 7,168, 35.3 for
 // 2,048 tokens, 7.0 for 17. What bounds the long ones is the alternation: per
 // key tile the tensor pipe works 2 x 1,024 of 2,900 cycles.
 #include <math.h>
@@ -89,7 +96,12 @@ constexpr int SMEM_BYTES = OUT_OFF + 8 * OUT_WARP + 1024;
 constexpr int THREADS = 352;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                  // items handed from the producer to the other warps
-constexpr int JOIN_TILES = 3;             // what joining the parts of an item costs, in key tiles of one CTA
+// What sharing items costs, in key tiles of one CTA (about 1.6 us), measured on
+// full items of 256 rows and scaled: with up to 1 + DIRECT parts 18 us (the
+// last CTA writes none and reads two); with more 14 us for writing two parts
+// and the second kernel, and 9 us per 40 MB of parts that it reads.
+constexpr float DIRECT_ROW = 10.f / (NQ * ROWS), JOIN_TILES = 9.f, JOIN_ROW = 1.4e-4f;
+constexpr int MAX_PARTS = 64;             // of an item
 constexpr int MIN_TILES = 3;              // key tiles of a part at least
 constexpr uint32_t TMEM_COLS = 512;
 // TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
@@ -117,18 +129,12 @@ struct Bars {
   int abort;
   int q_issued[NQ], k_issued, v_issued;
   int warp_sum[THREADS / 32];
+  int rows;                   // most query rows of an item
   int is_last;                // of an item's parts, this CTA's is the last
   int parts_there;            // the others are written
-  int left;                   // bits: the first / the last shared item of this CTA is left to join from memory
   Item item[SLOTS];           // g < 0: no more
   int cum[MAX_SORT + 1];      // key tiles before entry e, if there are at most MAX_SORT entries
-  union {
-    short order[MAX_SORT];    // entries, longest first
-    struct {
-      float row_m[NQ * ROWS], row_inv[NQ * ROWS];  // joining: a row's max and 1 / sum
-      int row_bad[NQ * ROWS];
-    };
-  };
+  short order[MAX_SORT];      // entries, longest first
 };
 static_assert(sizeof(Bars) <= BARS_BYTES, "barrier block");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -310,8 +316,8 @@ __device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n) {
 
 // Parts of an item that several CTAs share: slot 2 c + 1 for the CTA with the
 // item's first key tile (slot 2 c may hold its part of the item before), 2 c
-// otherwise. A part is the fp32 O, [32 column groups][256 rows][4], and
-// [256 rows] (max in log2 units, sum).
+// otherwise. A part is the fp32 O, [32 column groups][span rows][4] without
+// gaps, and [256 rows] (max in log2 units, sum).
 __device__ __forceinline__ size_t part_slot(int c, int first) { return 2 * static_cast<size_t>(c) + (c == first); }
 __device__ __forceinline__ float2* part_ml(const PackedPrefillParams& a, size_t slot) {
   return reinterpret_cast<float2*>(a.part_ml) + slot * NQ * ROWS;
@@ -320,100 +326,97 @@ __device__ __forceinline__ float4* part_o(const PackedPrefillParams& a, size_t s
   return reinterpret_cast<float4*>(a.part_o) + slot * NQ * ROWS * (HEAD_DIM / 4);
 }
 
-// BLOCK column groups of one row of an item from its parts in memory.
-template <int BLOCK>
-__device__ __forceinline__ bool join_block(const PackedPrefillParams& a, const Item& it, int row, int c4, float m,
-                                           float inv, __nv_bfloat16* dst) {
-  float4 o[BLOCK];
-#pragma unroll
-  for (int e = 0; e < BLOCK; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int AHEAD = 4;  // parts in flight
-  for (int c0 = it.first; c0 <= it.last; c0 += AHEAD) {
-    float w[AHEAD];
-    float4 x[AHEAD][BLOCK];
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      if (c0 + k > it.last) continue;
-      const size_t slot = part_slot(c0 + k, it.first);
-      w[k] = __ldcg(part_ml(a, slot) + row).x;
-#pragma unroll
-      for (int e = 0; e < BLOCK; ++e) x[k][e] = __ldcg(part_o(a, slot) + (c4 + e) * NQ * ROWS + row);
-    }
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      if (c0 + k > it.last) continue;
-      const float f = ex2_approx(w[k] - m);
-#pragma unroll
-      for (int e = 0; e < BLOCK; ++e) {
-        o[e].x += f * x[k][e].x;
-        o[e].y += f * x[k][e].y;
-        o[e].z += f * x[k][e].z;
-        o[e].w += f * x[k][e].w;
-      }
-    }
-  }
-  float chk = 0.f;  // NaN when a value is not finite
-#pragma unroll
-  for (int e = 0; e < BLOCK; ++e) {
-    chk += o[e].x * 0.f + o[e].y * 0.f + o[e].z * 0.f + o[e].w * 0.f;
-    *(reinterpret_cast<uint2*>(dst) + c4 + e) =
-        make_uint2(pack_bf16(o[e].x * inv, o[e].y * inv), pack_bf16(o[e].z * inv, o[e].w * inv));
-  }
-  return chk == chk;
-}
+// The real rows of an item's Q tiles, each tile's first ones, and the rows
+// 0 .. span - 1 that hold them all (tile 1 from row 128 on).
+struct Rows {
+  int rows0, rows1, span;
+  __device__ __forceinline__ Rows(const Item& it, int qp, int nrep)
+      : rows0(min(qp, it.T - it.q0) * nrep), rows1(max(0, min(qp, it.T - it.q0 - qp)) * nrep),
+        span(rows1 ? ROWS + rows1 : rows0) {}
+};
 
-// Joins all parts of an item from memory. Run by the whole CTA at its end.
-__device__ __forceinline__ void join(const PackedPrefillParams& a, Bars& bs, const Item& it, int qp, int nrep) {
-  const int tid = threadIdx.x;
-  // the real rows of a Q tile are its first
-  int rows[NQ];
-#pragma unroll
-  for (int t = 0; t < NQ; ++t) rows[t] = max(0, min(qp, it.T - it.q0 - t * qp)) * nrep;
-  const int total = rows[0] + rows[1];
-  if (tid < NQ * ROWS) {
-    const bool real = (tid & (ROWS - 1)) < rows[tid / ROWS];
+// ---- the second kernel: joins the parts of items that more than 1 + DIRECT
+// CTAs share, block x the item
+// that CTA x of the first kernel began, if it is shared, block y a slice of its
+// rows. One part per (CTA, item), in CTA order: the result does not depend on
+// who was first.
+constexpr int JOIN_THREADS = 256, JOIN_SLICE = 32, JOIN_SLICES = NQ * ROWS / JOIN_SLICE;
+__global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const __grid_constant__ PackedPrefillParams a) {
+  __shared__ float weight[MAX_PARTS][JOIN_SLICE];
+  __shared__ int off[JOIN_SLICE], bad[JOIN_SLICE];
+  pdl_trigger();
+  pdl_wait();
+  const Item it = reinterpret_cast<const Item*>(a.joins)[blockIdx.x];
+  const int np = it.last - it.first + 1;
+  if (np <= 1 + DIRECT) return;
+  const int nrep = a.n_heads / a.n_kv, qp = ROWS / nrep, tid = threadIdx.x, lane = tid & 31;
+  const Rows n(it, qp, nrep);
+  const int r0 = blockIdx.y * JOIN_SLICE;
+  if (r0 >= n.span) return;
+  {
+    // eight lanes a row: its max over the parts, the parts' factors, the sum
+    const int r = tid >> 3, row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep;
+    const bool real = row < n.span && rr < (t ? n.rows1 : n.rows0);
     float m = -INFINITY, l = 0.f;
-    if (real) {
-#pragma unroll 8
-      for (int c = it.first; c <= it.last; ++c) m = fmaxf(m, __ldcg(part_ml(a, part_slot(c, it.first)) + tid).x);
-      if (m == -INFINITY) m = 0.f;
-#pragma unroll 8
-      for (int c = it.first; c <= it.last; ++c) {
-        const float2 ml = __ldcg(part_ml(a, part_slot(c, it.first)) + tid);
-        l += ex2_approx(ml.x - m) * ml.y;
+    if (real)
+      for (int c = tid & 7; c < np; c += 8) m = fmaxf(m, __ldcg(part_ml(a, part_slot(it.first + c, it.first)) + row).x);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (m == -INFINITY) m = 0.f;
+    if (real)
+      for (int c = tid & 7; c < np; c += 8) {
+        const float2 ml = __ldcg(part_ml(a, part_slot(it.first + c, it.first)) + row);
+        const float w = ex2_approx(ml.x - m);
+        l += w * ml.y;
+        weight[c][r] = w;
       }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const float inv = 1.f / l;
+    if (real)
+      for (int c = tid & 7; c < np; c += 8) weight[c][r] *= inv;
+    if ((tid & 7) == 0) {
+      off[r] = real ? ((t * qp + rp) * a.n_heads + it.g * nrep + rr - rp * nrep) * HEAD_DIM : -1;
+      bad[r] = 0;
     }
-    bs.row_m[tid] = m;
-    bs.row_inv[tid] = 1.f / l;
-    bs.row_bad[tid] = 0;
   }
   __syncthreads();
-  auto place = [&](int r, int& row, int& pos, int& head) {  // the r-th real row
-    const int t = r >= rows[0];
-    r -= t ? rows[0] : 0;
-    row = t * ROWS + r;
-    const int rp = r / nrep;
-    pos = it.q0 + t * qp + rp;
-    head = it.g * nrep + r - rp * nrep;
-  };
-  // (column block, row) pairs, rows fastest
-  constexpr int WIDTH = 2;
-#pragma unroll 1
-  for (int i = tid; i < total * (HEAD_DIM / 4 / WIDTH); i += THREADS) {
-    const int blk = i / total;
-    int row, pos, head;
-    place(i - blk * total, row, pos, head);
-    __nv_bfloat16* dst = a.out + ((static_cast<size_t>(it.row0) + pos) * a.n_heads + head) * HEAD_DIM;
-    const bool fine = join_block<WIDTH>(a, it, row, blk * WIDTH, bs.row_m[row], bs.row_inv[row], dst);
-    if (!fine) bs.row_bad[row] = 1;
+  // a warp: 8 rows x 4 column groups, so that whole sectors are read and stored
+  __nv_bfloat16* out = a.out + (static_cast<size_t>(it.row0) + it.q0) * a.n_heads * HEAD_DIM;
+  const int g = (tid >> 5) * 4 + (lane >> 3);
+  constexpr int EACH = JOIN_SLICE / 8;
+  float4 o[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int c = 0; c < np; ++c) {
+    const float4* x4 = part_o(a, part_slot(it.first + c, it.first)) + g * n.span + r0 + (lane & 7);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int r = 8 * i + (lane & 7);
+      if (off[r] < 0) continue;
+      const float4 x = __ldcg(x4 + 8 * i);
+      const float w = weight[c][r];
+      o[i].x += w * x.x;
+      o[i].y += w * x.y;
+      o[i].z += w * x.z;
+      o[i].w += w * x.w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int r = 8 * i + (lane & 7);
+    if (off[r] < 0) continue;
+    const float chk = o[i].x * 0.f + o[i].y * 0.f + o[i].z * 0.f + o[i].w * 0.f;
+    if (chk != chk) bad[r] = 1;
+    *(reinterpret_cast<uint2*>(out + off[r]) + g) = make_uint2(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i].z, o[i].w));
   }
   __syncthreads();
-  for (int r = tid >> 5; r < total; r += THREADS / 32) {
-    int row, pos, head;
-    place(r, row, pos, head);
-    if (bs.row_bad[row] && it.start + pos < it.kv_end - 1) masked_row(a, it.b, it.row0, it.g, it.start, pos, head, it.kv_end);
+  for (int r = tid >> 5; r < JOIN_SLICE; r += JOIN_THREADS / 32) {
+    const int row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep, pos = it.q0 + t * qp + rp;
+    if (bad[r] && it.start + pos < it.kv_end - 1)
+      masked_row(a, it.b, it.row0, it.g, it.start, pos, it.g * nrep + rr - rp * nrep, it.kv_end);
   }
-  __syncthreads();  // the rows' figures are free again
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&bs.item_empty[s]), 10);  // issuers, softmax warps
     }
     bs.abort = 0;
-    bs.left = 0;
+    bs.rows = 0;
     bs.q_issued[0] = bs.q_issued[1] = 0;
     bs.k_issued = bs.v_issued = 0;
     fence_barrier_init();
@@ -500,9 +503,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   bool equal = false;   // equal ranges of key tiles instead of whole items
   bool sorted = false;  // whole items in the order of bs.order
   int units = 0, parts = 1;
-  const int own_n = E <= MAX_SORT && static_cast<int>(threadIdx.x) < E ? entry_at(threadIdx.x, pre, qp, a).n : 0;
+  int own_n = 0;
+  if (E <= MAX_SORT && static_cast<int>(threadIdx.x) < E) {
+    const Item own = entry_at(threadIdx.x, pre, qp, a);
+    own_n = own.n;
+    atomicMax(&bs.rows, min(own.T - own.q0, NQ * qp) * nrep);
+  }
   // nothing to plan where every CTA has one short item at most
-  if (E <= MAX_SORT && (__syncthreads_or(own_n > JOIN_TILES + 1) || nitems > G)) {
+  if (E <= MAX_SORT && (__syncthreads_or(own_n > 2 * MIN_TILES) || nitems > G)) {
     const int e = threadIdx.x;
     if (e < E) bs.cum[e + 1] = own_n;
     if (e == 0) bs.cum[0] = 0;
@@ -522,9 +530,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     sorted = true;
     units = bs.cum[E] * a.n_kv;
-    // the load of CTA `threadIdx.x` if whole items went round in turn, longest first
+    // The load of CTA `threadIdx.x` if whole items went round in turn, longest
+    // first, against equal ranges (no shorter than pays for the joins) and the
+    // joins they bring.
     int load = 0;
     if (static_cast<int>(threadIdx.x) < G)
+#pragma unroll 1
       for (int k = 0; k * G < nitems; ++k) {
         const int i = k * G + ((k & 1) ? G - 1 - static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x));
         if (i < nitems) {
@@ -532,9 +543,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           load += bs.cum[o + 1] - bs.cum[o];
         }
       }
-    const bool mine = load > units / G + JOIN_TILES + 1;
-    equal = __syncthreads_or(mine) && units >= 2 * MIN_TILES;
-    if (equal) parts = min(G, units / MIN_TILES);
+    const int o = bs.order[0], longest = bs.cum[o + 1] - bs.cum[o];
+    const int mean = max((units + G - 1) / G, MIN_TILES);
+    // ranges of half an item: each in three at most
+    const int few = max(mean, (longest + 1) / 2);
+    const float few_cost = few + DIRECT_ROW * bs.rows;
+    // whole tiles: no item then lies in more than MAX_PARTS ranges
+    const int many = max(mean, (longest + MAX_PARTS - 3) / (MAX_PARTS - 2));
+    const float many_cost = a.joins ? many + JOIN_TILES + JOIN_ROW * (units / many) * bs.rows : INFINITY;
+    equal = __syncthreads_or(static_cast<float>(load) > fminf(few_cost, many_cost));
+    if (equal) parts = min(G, max(1, units / (few_cost <= many_cost ? few : many)));
   }
   const bool claim = !equal && nitems > G;  // items are claimed as CTAs get to them
   tc_fence_before();
@@ -957,21 +975,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       size_t at_part[DIRECT] = {};
       int nparts = 0;
       if (it.first != it.last) {
-        // The CTA that arrives last at the item's ticket joins its parts (the
-        // others have arrived, so they are running and about to write
-        // theirs). A few parts are added to this CTA's in its epilogue; of
-        // many, this one is left in memory as well and all are joined by the
-        // whole CTA at its end.
+        // Of few parts, the CTA that arrives last at the item's ticket adds the
+        // others (they have arrived, so they are running and about to write
+        // theirs) to its own. More are left to the second kernel.
         const int c = blockIdx.x, others = it.last - it.first;
         int* arrived = a.tickets + 2 * it.first;
-        if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
-        if (!softmax_sync(bs, syncs)) {
-          ok = false;
-          break;
+        if (others <= DIRECT) {
+          if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
+          if (!softmax_sync(bs, syncs)) {
+            ok = false;
+            break;
+          }
+          whole = bs.is_last;
+        } else {
+          whole = false;
         }
-        const bool last = bs.is_last;
-        whole = last && others <= DIRECT;
         const float m2 = l > 0.f || l != l ? m_ref * scale : -INFINITY;
+        const int span = Rows(it, qp, nrep).span;
         if (!whole) {
           const size_t slot = part_slot(c, it.first);
           if (real) __stcg(part_ml(a, slot) + t * ROWS + r, make_float2(m2, l));
@@ -987,27 +1007,28 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int e = 0; e < 32; ++e) o[e] = 0u;
             }
             if (real) {
-              float4* o4 = part_o(a, slot) + (cc / 4) * NQ * ROWS + t * ROWS + r;
+              float4* o4 = part_o(a, slot) + (cc / 4) * span + t * ROWS + r;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                __stcg(o4 + e * NQ * ROWS, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                       __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                __stcg(o4 + e * span, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                  __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
             }
             __syncwarp();
           }
         }
-        if (last && threadIdx.x == 0) {
-          // the others' parts are written
-          bs.parts_there = wait_counter(arrived + 1, others);
-          arrived[0] = 0;
-          arrived[1] = 0;
-          if (!whole) bs.left |= 1 << (c == it.first);
+        if (others <= DIRECT) {
+          if (whole && threadIdx.x == 0) {
+            // the others' parts are written
+            bs.parts_there = wait_counter(arrived + 1, others);
+            arrived[0] = 0;
+            arrived[1] = 0;
+          }
+          if (!softmax_sync(bs, syncs) || (whole && !bs.parts_there)) {
+            ok = false;
+            break;
+          }
+          if (!whole && threadIdx.x == 0) signal_counter(arrived + 1, 1);  // all warps' parts: the barrier is before it
         }
-        if (!softmax_sync(bs, syncs) || (last && !bs.parts_there)) {
-          ok = false;
-          break;
-        }
-        if (!last && threadIdx.x == 0) signal_counter(arrived + 1, 1);  // all warps' parts: the barrier is before it
         if (whole) {
           static_assert(DIRECT == 2, "the two parts below");
           nparts = others;
@@ -1045,15 +1066,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
           if (nparts > 0 && real) {
+            const int span = Rows(it, qp, nrep).span;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w_own);
 #pragma unroll 1
             for (int d = 0; d < nparts; ++d) {
               const float w = d ? w_part[1] : w_part[0];
-              const float4* o4 = part_o(a, d ? at_part[1] : at_part[0]) + (cc / 4) * NQ * ROWS + t * ROWS + r;
+              const float4* o4 = part_o(a, d ? at_part[1] : at_part[0]) + (cc / 4) * span + t * ROWS + r;
               float4 x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __ldcg(o4 + e * NQ * ROWS);
+              for (int e = 0; e < 8; ++e) x[e] = __ldcg(o4 + e * span);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + w * x[e].x);
@@ -1119,19 +1141,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
   }
-  // the item that this CTA's range ends, and the one it begins, where their
-  // parts are all in memory
-  const int left = bs.left;
-  if (left) {
-    __threadfence();
-    const Split split(units, parts);
-    const int u0 = split.start(blockIdx.x), u1 = split.start(blockIdx.x + 1);
-#pragma unroll 1
-    for (int side = 0; side < 2; ++side)
-      if (left >> side & 1) {
-        Item it = ranged_item(side ? u1 - 1 : u0, u1, split, E, bs.cum, pre, qp, a);
-        join(a, bs, it, qp, nrep);
-      }
+  // what the second kernel has to join: the item that this CTA's range begins
+  // and does not end
+  if (a.joins && threadIdx.x == 0) {
+    Item it = {};
+    if (equal && static_cast<int>(blockIdx.x) < parts) {
+      const Split split(units, parts);
+      const int end = split.start(blockIdx.x + 1);
+      it = ranged_item(end - 1, end, split, E, bs.cum, pre, qp, a);
+      if (it.first != static_cast<int>(blockIdx.x)) it.last = it.first;
+    }
+    reinterpret_cast<Item*>(a.joins)[blockIdx.x] = it;
   }
   // the last CTA out clears the claims for the next call
   if (threadIdx.x == 0 && claim) {
@@ -1144,6 +1164,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 }  // namespace
+
+// Whether items can come to have parts for the second kernel: no more entries
+// than are sorted, and keys enough to repay it (an empty one takes 2 us).
+bool packed_prefill_may_join(int N, int n_rep, long long most_keys) {
+  return N / (NQ * (ROWS / n_rep)) <= MAX_SORT && most_keys > 2048;
+}
+size_t packed_prefill_join_bytes(int ctas) { return ctas * sizeof(Item); }
+
+cudaError_t launch_packed_prefill_join(const PackedPrefillParams& a, cudaStream_t s) {
+  return launch_behind(packed_prefill_join_kernel, dim3(a.ctas, JOIN_SLICES), JOIN_THREADS, 0, s, a);
+}
 
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& a, cudaStream_t s) {
   static bool attr_set[64] = {};

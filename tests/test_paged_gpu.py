@@ -392,6 +392,28 @@ def test_paged_prefill_one_item_over_every_cta(gen, ws):
     run_paged_prefill(gen, ws, 16, 1, 128, [8], [60000])
 
 
+@pytest.mark.parametrize("heads,n_kv,lens,starts", [
+    (8, 2, [300], [9000]), (28, 4, [100], [5000]), (28, 4, [1, 90], [7000, 2500]), (16, 16, [130], [4000]),
+    (32, 8, [600, 40], [5000, 3000]), (32, 8, [1000], [1500]), (4, 1, [2500], [0]), (16, 1, [40], [30000])])
+def test_paged_prefill_items_shared_by_few_and_many(gen, ws, heads, n_kv, lens, starts):
+    run_paged_prefill(gen, ws, heads, n_kv, 64, lens, starts, behind=2)
+
+
+def test_paged_prefill_joins_only_its_own_items(gen, ws):
+    # the second call has none to join: what the first left stays unread
+    k_pages, v_pages, table, ((k, v),) = fill_cache(gen, [9000], 64, 2)
+    q = P.normal(gen, 100, 8, P.D)
+    out = torch.full_like(q, 9.0)
+    G.paged_prefill(q, offsets([100]), ints([8900]), k_pages, v_pages, table, out=out, workspace=ws)
+    assert G.last_launch_count() == 2
+    check_prefill(out, q, [(k, v)], [100], [8900])
+    out.fill_(9.0)
+    G.paged_prefill(q, offsets([3]), ints([0]), k_pages, v_pages, table, out=out, workspace=ws)
+    assert G.device_status(ws) == 0
+    check_prefill(out, q, [(k[:3], v[:3])], [3], [0])
+    assert (out[3:] == 9.0).all()
+
+
 # ------------------------------------------------------------------ errors on the device
 
 def test_bad_positions_are_reported_and_skipped(gen, ws):
