@@ -69,6 +69,27 @@ int check_workspace(const void* ws, size_t bytes) {
   return bytes < GQA_PAGED_WORKSPACE_BYTES ? GQA_EWORKSPACE : GQA_OK;
 }
 
+// Whether an output of n_out elements shares memory with n_in elements (counted
+// in 128 bits: strides times counts of a faulty call may pass 64).
+bool overlaps(const gqa_bf16* out, __int128 n_out, const gqa_bf16* in, __int128 n_in) {
+  const __int128 o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+  return n_out > 0 && n_in > 0 && o < i + 2 * n_in && i < o + 2 * n_out;
+}
+// ... with n packed rows of `row` elements
+bool overlaps(const gqa_bf16* out, __int128 n_out, const gqa_bf16* in, int n, int64_t stride, int64_t row) {
+  return n > 0 && overlaps(out, n_out, in, static_cast<__int128>(n - 1) * stride + row);
+}
+// ... with rows of keys or values in pages
+bool overlaps(const gqa_bf16* out, __int128 n_out, const PagedCache& c, int pages, int rows, int n_kv,
+              long long v_row_stride) {
+  const __int128 others = static_cast<__int128>(pages - 1) * c.page_stride +
+                          static_cast<__int128>(n_kv - 1) * c.head_stride + HEAD_DIM;
+  return overlaps(out, n_out, reinterpret_cast<const gqa_bf16*>(c.k),
+                  others + static_cast<__int128>(rows - 1) * c.row_stride) ||
+         overlaps(out, n_out, reinterpret_cast<const gqa_bf16*>(c.v),
+                  others + static_cast<__int128>(rows - 1) * v_row_stride);
+}
+
 int check_scale(float scale) { return scale > 0.f && scale < 1e30f ? GQA_OK : GQA_EINVAL; }
 
 const __nv_bfloat16* bf(const gqa_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
@@ -108,6 +129,10 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
       !aligned4(start_pos) || (cu_tokens && !aligned4(cu_tokens)))
     return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
+  if (q && ((q != q_out && overlaps(q_out, N * q_row, q, N, q_stride, q_row)) ||
+            overlaps(q_out, N * q_row, k, N, k_stride, kv_row) || overlaps(q_out, N * q_row, v, N, v_stride, kv_row) ||
+            overlaps(q_out, N * q_row, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride)))
+    return GQA_EINVAL;
   begin_call();
   if (N == 0) return GQA_OK;
   p.q = bf(q);
@@ -147,6 +172,10 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
     return GQA_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned4(start_pos)) return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
+  const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
+  if (overlaps(out, B * row, q, B, q_stride, row) ||
+      overlaps(out, B * row, p.pages, pages->num_pages, pages->page_size, pages->n_kv_heads, p.pages.row_stride))
+    return GQA_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = bf(q);
   p.q_stride = q_stride;
@@ -179,6 +208,11 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   if (!valid_stride(q_stride, static_cast<int64_t>(n_heads) * HEAD_DIM)) return GQA_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned4(cu_tokens)) return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
+  const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
+  const PagedCache& c = p.pages;
+  const long long v_row = p.v_row_stride ? p.v_row_stride : c.row_stride;
+  if (overlaps(out, N * row, q, N, q_stride, row) || overlaps(out, N * row, c, kv_pages, kv_rows, n_kv, v_row))
+    return GQA_EINVAL;
   begin_call();
   if (N == 0) return GQA_OK;
   p.N = N;
@@ -204,8 +238,6 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   const cuuint64_t dims[3] = {HEAD_DIM, static_cast<cuuint64_t>(n_heads), static_cast<cuuint64_t>(N)};
   const cuuint64_t strides[2] = {HEAD_DIM * 2, static_cast<cuuint64_t>(q_stride) * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(n_rep), static_cast<cuuint32_t>(128 / n_rep)};
-  const PagedCache& c = p.pages;
-  const long long v_row = p.v_row_stride ? p.v_row_stride : c.row_stride;
   if (!encode_bf16(&maps.q, 3, q, dims, strides, box) ||
       !map_kv(&maps.k, c.k, n_kv, kv_rows, kv_pages, c.head_stride, c.row_stride, c.page_stride, box_rows) ||
       !map_kv(&maps.v, c.v, n_kv, kv_rows, kv_pages, c.head_stride, v_row, c.page_stride, box_rows))

@@ -1,7 +1,7 @@
 // Argument checks and marshalling of the paged serving operators, compiled: a
 // decode step makes a few of these calls a layer, each on a kernel of a few
 // microseconds, and the same checks written in Python cost 6 to 10 us a call
-// (measured on the GPU machine's Arm cores), more than the kernels of a small
+// (measured on Grace's Arm cores), more than the kernels of a small
 // batch. Nothing is computed here. Each function takes its tensors by
 // position, raises TypeError or ValueError, and returns the status of the C
 // entry.

@@ -365,12 +365,16 @@ int gqa_host_stage_release(void* stage);
  * rows are zero. Other values with a token at or past columns * page_size (or
  * rope_rows), and values below -1, are reported as GQA_DEV_BAD_POSITION.
  *
+ * Outputs share no memory with inputs or pages, but for q_out = q below (else
+ * GQA_EINVAL).
+ *
  * Every entry enqueues on `stream` of the current device, allocates nothing
  * and can be captured into a graph; no length is read by the host, so a
  * captured step replays with other lengths, tables and contents. The
  * workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled before its first
  * use, and serves one call at a time; its status word is read with
- * gqa_device_status. After GQA_DEV_WAIT_TIMEOUT zero-fill it again
+ * gqa_device_status. One launch each; two for the prefill attention where a
+ * sequence may have more than 2,048 keys. After GQA_DEV_WAIT_TIMEOUT zero-fill it again
  * (gqa_workspace_init). */
 
 #define GQA_PAGED_WORKSPACE_BYTES (64u << 20)

@@ -1,6 +1,7 @@
 """The paged operators' refusals (argument checks of the binding and of the C
 ABI; nothing is launched) and the arithmetic of their work split, on the CPU."""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -127,6 +128,24 @@ def test_prefill_refuses_its_own_arguments(lib):
 def test_prefill_refuses_more_key_tiles_than_it_can_count(lib):
     p = pages(columns=1 << 23, table_stride=1 << 23)    # 2^27 positions, 8 KV heads
     assert prefill(lib, p) == -1
+
+
+A = 1 << 30   # an address space of its own for these
+
+
+@pytest.mark.parametrize("call,kw", [
+    (append, dict(out=A + 256)),                                      # part of q
+    (append, dict(out=FAKE)), (append, dict(q=4 * A, out=A - 4096)),  # the pages; k
+    (append, dict(q=4 * A, k=8 * A, out=2 * A + 4 * 2048 + 2032)),    # the end of v
+    (decode, dict(out=A)), (decode, dict(out=A - 16)), (decode, dict(out=FAKE + 130000)),
+    (prefill, dict(out=A)), (prefill, dict(out=A + 4 * 8192 + 8176)), (prefill, dict(out=FAKE + 130000)),
+    (packed, dict(out=A)), (packed, dict(q=4 * A, out=A + 16)), (packed, dict(q=4 * A, k=8 * A, out=2 * A))])
+def test_outputs_that_overlap_inputs_are_refused(lib, call, kw):
+    a = dict(q=A, out=16 * A)
+    if call in (append, packed):
+        a.update(k=A, v=2 * A)
+    a.update(kw)
+    assert call(lib, **a) == -1
 
 
 def test_no_tokens_is_no_launch(lib):
@@ -336,6 +355,31 @@ def test_prefill_ranges_cover_every_key_tile_once(tiles, n_kv):
             at = j1
         assert at == tiles[e] and [x[2] for x in got] == list(range(got[0][3], got[0][4] + 1))
     assert len(seen) == n_kv * sum(n > 0 for n in tiles)
+
+
+@pytest.mark.parametrize("n_kv", [1, 2, 8, 32])
+@pytest.mark.parametrize("few", [True, False])
+def test_prefill_ranges_bound_the_parts_of_an_item(n_kv, few):
+    """Ranges of half the longest item: three parts at most; shorter ones: no
+    more than the second kernel has room for."""
+    rng = random.Random(n_kv)
+    for _ in range(300):
+        top = rng.choice([4, 20, 300, 8192])
+        tiles = [rng.randint(0, top) for _ in range(rng.randint(1, 320))]
+        cum = [0]
+        for n in tiles:
+            cum.append(cum[-1] + n)
+        units, longest = cum[-1] * n_kv, max(tiles)
+        if units < 6:
+            continue
+        mean = max((units + 151) // 152, 3)
+        size = max(mean, (longest + 1) // 2 if few else (longest + 61) // 62)
+        parts = min(152, max(1, units // size))
+        split = Split(units, parts)
+        for e, n in enumerate(tiles):
+            for g in range(n_kv if n else 0):
+                base = cum[e] * n_kv + g * n
+                assert split.holder(base + n - 1) - split.holder(base) < (3 if few else 64)
 
 
 def sequence_of(cu, B, m):
