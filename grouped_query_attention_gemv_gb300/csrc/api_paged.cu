@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "api_internal.h"
+#include "paged.h"
 
 using namespace gqa;
 

@@ -22,7 +22,6 @@ constexpr int ROPE_PAIRS = HEAD_DIM / 2;
 // Device status codes (mirrors GQA_DEV_* in gqa.h).
 constexpr int DEV_BAD_POSITION = 1;
 constexpr int DEV_WAIT_TIMEOUT = 2;
-constexpr int DEV_BAD_PAGE = 3;
 
 // A bounded wait gives up after this long and records DEV_WAIT_TIMEOUT.
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;
@@ -140,18 +139,6 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
-}
-
-// 16 bytes global -> shared, asynchronously; zeros when `bytes` is 0 (src is
-// then not read).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Wait until at most N of this thread's committed groups are in flight.
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
 // ----------------------------------------------------------------- mbarrier

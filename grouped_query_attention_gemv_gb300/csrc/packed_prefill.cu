@@ -68,7 +68,7 @@
 // key tile the tensor pipe works 2 x 1,024 of 2,900 cycles.
 #include <math.h>
 
-#include "kernels.h"
+#include "paged.h"
 
 namespace gqa {
 

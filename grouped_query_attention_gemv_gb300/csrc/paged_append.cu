@@ -10,7 +10,7 @@
 // sequence -> start position -> table entry -> RoPE row is three dependent
 // loads. A lane's four pairs have the same place in every head, so the (cos,
 // sin) of a token are loaded once for the warp's 8 rows.
-#include "kernels.h"
+#include "paged.h"
 
 namespace gqa {
 

@@ -45,7 +45,7 @@
 // row]) are 2 to 4% faster than [page, row, KV head]: longer runs per CTA.
 #include <math.h>
 
-#include "kernels.h"
+#include "paged.h"
 
 namespace gqa {
 
