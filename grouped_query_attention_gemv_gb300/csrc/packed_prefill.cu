@@ -349,6 +349,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const
   const Item it = reinterpret_cast<const Item*>(a.joins)[blockIdx.x];
   const int np = it.last - it.first + 1;
   if (np <= 1 + DIRECT) return;
+  // an item of another call (a workspace that two calls use at once, or that
+  // was not zeroed): nothing of it is read or written
+  const long long keys = a.start ? a.pages.capacity() : it.T;
+  if (np > MAX_PARTS || it.first < 0 || it.last >= a.ctas || it.b < 0 || it.b >= a.B || it.g < 0 || it.g >= a.n_kv ||
+      it.q0 < 0 || it.q0 >= it.T || it.row0 < 0 || it.T > a.N - it.row0 || it.start < 0 || it.kv_end > keys)
+    return;
   const int nrep = a.n_heads / a.n_kv, qp = ROWS / nrep, tid = threadIdx.x, lane = tid & 31;
   const Rows n(it, qp, nrep);
   const int r0 = blockIdx.y * JOIN_SLICE;
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!claim) return false;
           int c = 0;
           if (lane == 0) c = atomicAdd(a.claims, 1);
-          wi = static_cast<long long>(G) + __shfl_sync(0xffffffffu, c, 0);
+          wi = static_cast<long long>(G) + static_cast<unsigned>(__shfl_sync(0xffffffffu, c, 0));
         }
         asked = true;
         if (wi >= nitems) return false;

@@ -370,12 +370,12 @@ int gqa_host_stage_release(void* stage);
  *
  * Every entry enqueues on `stream` of the current device, allocates nothing
  * and can be captured into a graph; no length is read by the host, so a
- * captured step replays with other lengths, tables and contents. The
- * workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled before its first
- * use, and serves one call at a time; its status word is read with
- * gqa_device_status. One launch each; two for the prefill attention where a
- * sequence may have more than 2,048 keys. After GQA_DEV_WAIT_TIMEOUT zero-fill it again
- * (gqa_workspace_init). */
+ * captured step replays with other lengths, tables and contents. One launch
+ * each; two for the prefill attention where a sequence may have more than
+ * 2,048 keys. The workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled
+ * before its first use, serves one call at a time and no other entries than
+ * these; its status word is read with gqa_device_status. After
+ * GQA_DEV_WAIT_TIMEOUT zero-fill it again (gqa_workspace_init). */
 
 #define GQA_PAGED_WORKSPACE_BYTES (64u << 20)
 #define GQA_PAGED_MAX_SEQS 2048   /* sequences per call */

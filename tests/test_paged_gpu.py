@@ -589,6 +589,48 @@ def test_a_captured_step_replays_with_other_lengths(gen):
     assert G.device_status(ws) == 0
 
 
+def test_a_captured_prefill_replays_between_shared_and_whole_items(gen):
+    heads, n_kv, page = 8, 2, 64
+    ws = G.make_paged_workspace()
+    k_pages, v_pages, table, rows = fill_cache(gen, [9100, 9100], page, n_kv)
+    q = P.normal(gen, 120, heads, P.D)
+    cu, start = offsets([100, 20]), ints([0, 0])
+    out = torch.empty_like(q)
+    G.paged_prefill(q, cu, start, k_pages, v_pages, table, out=out, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        G.paged_prefill(q, cu, start, k_pages, v_pages, table, out=out, workspace=ws)
+    for lens, starts in (([100, 20], [9000, 9080]), ([100, 20], [0, 3]), ([3, 60], [8000, -1]), ([1, 119], [9099, 500])):
+        cu.copy_(offsets(lens))
+        start.copy_(ints(starts))
+        out.fill_(9.0)
+        g.replay()
+        ends = [(k[:s + t], v[:s + t]) for (k, v), t, s in zip(rows, lens, starts)]
+        check_prefill(out, q, ends, lens, starts)
+        assert (out[sum(lens):] == 9.0).all()
+    assert G.device_status(ws) == 0
+
+
+def test_sequences_that_share_pages(gen, ws):
+    # one prompt's pages under two sequences, each with a last page of its own
+    k_pages, v_pages, table, rows = fill_cache(gen, [3000, 3000], 64, 2)
+    table[1, :40] = table[0, :40]
+    for x, other in zip(rows[1], rows[0]):
+        x[:40 * 64] = other[:40 * 64]
+    q = P.normal(gen, 2, 8, P.D)
+    check_decode(G.paged_decode(q, ints([2999, 2999]), k_pages, v_pages, table, workspace=ws), q, rows)
+    q = P.normal(gen, 50, 8, P.D)
+    out = G.paged_prefill(q, offsets([30, 20]), ints([2970, 2980]), k_pages, v_pages, table, workspace=ws)
+    check_prefill(out, q, rows, [30, 20], [2970, 2980])
+    assert G.device_status(ws) == 0
+
+
+def test_most_sequences_and_most_heads_per_kv_head(gen, ws):
+    lens = [(31 * b) % 40 for b in range(2048)]
+    run_decode(gen, ws, 16, 1, 16, lens)
+    run_paged_prefill(gen, ws, 16, 1, 16, [n % 2 for n in lens], [n // 2 for n in lens])
+
+
 def test_calls_on_two_streams_with_their_own_workspaces(gen):
     k_pages, v_pages, table, rows = fill_cache(gen, [3000, 40, 700], 32, 4)
     start = ints([2999, 39, 699])
