@@ -29,13 +29,14 @@
 //     shared memory among the CTA's warps, then, where several CTAs hold
 //     parts, by the CTA that arrives last at a ticket, in CTA order: the
 //     result does not depend on the order of arrival, and no CTA waits.
-//   * Joining across CTAs (fence, ticket, read back) takes about 4 us. Where
-//     one CTA per (sequence, KV head) is no more than that behind the equal
-//     ranges, the ranges are those. Both measured, own / equal: 16 sequences
-//     of 2,001 rows and 8 KV heads 25.7 / 30.4 us, of 8,192 rows 83.4 / 87.5,
-//     12 of 4,001 37.2 / 39.4, 8 of 2,001 20.1 / 20.6, 4 of 1,001 11.7 / 10.2,
-//     one of 2,001 18.2 / 9.6. The longest sequence's time alone on a CTA, or
-//     the batch's at the memory's rate, tells them apart.
+//   * Joining across CTAs (ticket, read back) takes 2.5 to 4 us. Where one CTA
+//     per (sequence, KV head) is no more than 2.5 us behind the equal ranges,
+//     the ranges are those. Both measured, own / equal: 16 sequences of 2,001
+//     rows and 8 KV heads 25.7 / 29.7 us, of 8,192 rows 83.3 / 86.8, of 301
+//     7.4 / 10.2, 12 of 4,001 37.3 / 38.5, 8 of 2,001 20.4 / 20.0, 4 of 1,001
+//     11.9 / 9.7, of 401 8.2 / 8.6, one of 2,001 18.6 / 9.3. The longest
+//     sequence's time alone on a CTA, or the batch's at the memory's rate,
+//     tells them apart.
 //   * Code that runs once a CTA, and the join that runs in a few CTAs, wait
 //     for instructions more than for data: their loops are not unrolled.
 // Measured (GB300, 6.8 TB/s copied): 171.8 us for 1.108 GB (64 sequences of
@@ -59,9 +60,9 @@ constexpr int STAGES = 2;
 constexpr int WARPS = 8;
 // In 1/800 us, what a chunk takes at the whole memory's rate: a chunk of a CTA
 // by itself (it streams 9 or 10 a us, 64 to 128 KB in flight), and joining
-// across CTAs (about 4 us).
-constexpr float ALONE = 85.f, JOIN_COST = 3200.f;
-constexpr int BATCH = 8;                          // partials a warp has in flight when it joins
+// across CTAs (2.5 us).
+constexpr float ALONE = 85.f, JOIN_COST = 2000.f;
+constexpr int BATCH = 5;                          // partials a warp has in flight when it joins
 constexpr int PART = HEAD_DIM + 2;                // floats of a partial row: o, max, sum
 
 // Row r, 16-byte piece c of a 256-byte-row tile: eight rows of one piece fall
@@ -124,6 +125,22 @@ struct Part {
 __device__ __forceinline__ void store_row(__nv_bfloat16* out, int row, float4 o, float inv) {
   *(reinterpret_cast<uint2*>(out + static_cast<long long>(row) * HEAD_DIM) + (threadIdx.x & 31)) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
+// Counts this CTA at a ticket: behind the barrier before it, it publishes all
+// the CTA's stores, and to the barrier behind it those of the CTAs before.
+__device__ __forceinline__ int arrive(int* ticket) {
+  int n;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
+  return n;
+}
+
+// A running (max, sum, output) taken to the max mx.
+__device__ __forceinline__ void rescale(float& m, float mx, float& l, float4& o) {
+  const float s = ex2_approx(m - (mx == -INFINITY ? 0.f : mx));
+  m = mx;
+  l *= s;
+  o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
 }
 
 // NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16).
@@ -485,25 +502,23 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   if (cross[0].first < 0 && cross[1].first < 0) return;
 
   // ---- across CTAs: the ticket is that of the CTA with the first chunk
-  __threadfence();
   __syncthreads();
   if (threadIdx.x < 2) {
     const Part seg = threadIdx.x ? cross[1] : cross[0];
     int last = 0;
     if (seg.first >= 0) {
       const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
-      __threadfence();
-      last = atomicAdd(p.tickets + a, 1) == z - a;
+      last = arrive(p.tickets + a) == z - a;
       if (last) p.tickets[a] = 0;
-      __threadfence();
       joint[threadIdx.x] = {a, z, seg.row};
     }
     is_last[threadIdx.x] = last;
   }
   __syncthreads();
-  // Per query head `ways` warps share the partials, then the first of them
-  // adds up. Few CTAs come here and their instruction caches are cold: the
-  // loops are kept short (16 partials unrolled took as long as one at a time).
+  // Per query head `ways` warps share the partials, each with a running max,
+  // then the first of them adds up. Few CTAs come here and their instruction
+  // caches are cold: the loops are kept short (one sequence of 1,001 rows: 8.8
+  // us with batches of 5, 9.2 with 8 or 4; 9.35 with a pass for the max before).
   const int ways = max(1, W / n_rep);
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
@@ -521,11 +536,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         const float2* mls = reinterpret_cast<const float2*>(p.part_ml);
         const float4* os = reinterpret_cast<const float4*>(p.part_o) + lane;
 #pragma unroll 1
-        for (int c = a + lane; c <= z; c += 32) m = fmaxf(m, __ldcg(mls + at(c)).x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
         for (int c0 = a + way; c0 <= z; c0 += BATCH * ways) {
           float2 ml[BATCH];
           float4 x[BATCH];
@@ -539,6 +549,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
               x[k] = __ldcg(os + at(c) * (HEAD_DIM / 4));
             }
           }
+          float mx = m;
+#pragma unroll
+          for (int k = 0; k < BATCH; ++k) mx = fmaxf(mx, ml[k].x);
+          rescale(m, mx, l, o);
+          const float ref = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
           for (int k = 0; k < BATCH; ++k) {
             const float w = ex2_approx(ml[k].x - ref);
@@ -556,20 +571,23 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         if (on && way) {
           *reinterpret_cast<float2*>(mine + 4 * lane) = make_float2(o.x, o.y);
           *reinterpret_cast<float2*>(mine + 4 * lane + 2) = make_float2(o.z, o.w);
-          if (lane == 0) mine[HEAD_DIM] = l;
+          if (lane == 0) *reinterpret_cast<float2*>(mine + HEAD_DIM) = make_float2(m, l);
         }
         __syncthreads();
         if (on && !way)
 #pragma unroll 1
           for (int g = 1; g < ways; ++g) {
             const float* row = mine + g * PART;
-            l += row[HEAD_DIM];
+            const float2 ml = *reinterpret_cast<const float2*>(row + HEAD_DIM);
             const float2 x = *reinterpret_cast<const float2*>(row + 4 * lane);
             const float2 y = *reinterpret_cast<const float2*>(row + 4 * lane + 2);
-            o.x += x.x;
-            o.y += x.y;
-            o.z += y.x;
-            o.w += y.y;
+            rescale(m, fmaxf(m, ml.x), l, o);
+            const float w = ex2_approx(ml.x - (m == -INFINITY ? 0.f : m));
+            l += w * ml.y;
+            o.x += w * x.x;
+            o.y += w * x.y;
+            o.z += w * y.x;
+            o.w += w * y.y;
           }
       }
       if (on && !way) store_row(p.out, joint[side].row + r, o, 1.f / l);
