@@ -326,6 +326,12 @@ __device__ __forceinline__ float4* part_o(const PackedPrefillParams& a, size_t s
   return reinterpret_cast<float4*>(a.part_o) + slot * NQ * ROWS * (HEAD_DIM / 4);
 }
 
+// The sum of three parts' terms, this CTA's and the others' in CTA order, so
+// that it does not depend on whose it is: the first two, then the last.
+__device__ __forceinline__ float in_order(bool behind, float own, float x, float y) {
+  return behind ? __fadd_rn(__fadd_rn(x, y), own) : __fadd_rn(__fadd_rn(own, x), y);
+}
+
 // The real rows of an item's Q tiles, each tile's first ones, and the rows
 // 0 .. span - 1 that hold them all (tile 1 from row 128 on).
 struct Rows {
@@ -980,10 +986,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       float w_own = 1.f, w_part[DIRECT] = {};
       size_t at_part[DIRECT] = {};
       int nparts = 0;
+      bool behind = false;  // its part comes after the others
       if (it.first != it.last) {
         // Of few parts, the CTA that arrives last at the item's ticket adds the
         // others (they have arrived, so they are running and about to write
-        // theirs) to its own. More are left to the second kernel.
+        // theirs) to its own, in CTA order all the same. More are left to the
+        // second kernel.
         const int c = blockIdx.x, others = it.last - it.first;
         int* arrived = a.tickets + 2 * it.first;
         if (others <= DIRECT) {
@@ -1048,12 +1056,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           float m = max3(m2, ml[0].x, ml[1].x);
           if (m == -INFINITY) m = 0.f;
           w_own = ex2_approx(m2 - m);
-          l *= w_own;
 #pragma unroll
-          for (int d = 0; d < DIRECT; ++d) {
-            w_part[d] = ex2_approx(ml[d].x - m);
-            l += w_part[d] * ml[d].y;
-          }
+          for (int d = 0; d < DIRECT; ++d) w_part[d] = ex2_approx(ml[d].x - m);
+          behind = c == it.last;
+          l = in_order(behind, __fmul_rn(w_own, l), __fmul_rn(w_part[0], ml[0].y), __fmul_rn(w_part[1], ml[1].y));
         }
       }
       if (whole && (n_t > 0 || it.first != it.last)) {
@@ -1072,23 +1078,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
           if (nparts > 0 && real) {
-            const int span = Rows(it, qp, nrep).span;
+            const int span = Rows(it, qp, nrep).span, at = (cc / 4) * span + t * ROWS + r;
+            const float4 *o0 = part_o(a, at_part[0]) + at, *o1 = part_o(a, at_part[1]) + at;
+            float4 x[8], y[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w_own);
-#pragma unroll 1
-            for (int d = 0; d < nparts; ++d) {
-              const float w = d ? w_part[1] : w_part[0];
-              const float4* o4 = part_o(a, d ? at_part[1] : at_part[0]) + (cc / 4) * span + t * ROWS + r;
-              float4 x[8];
+            for (int e = 0; e < 8; ++e) {
+              x[e] = __ldcg(o0 + e * span);
+              y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (nparts > 1) y[e] = __ldcg(o1 + e * span);
+            }
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __ldcg(o4 + e * span);
+            for (int e = 0; e < 8; ++e) {
+              const float xe[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ye[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + w * x[e].x);
-                o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + w * x[e].y);
-                o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + w * x[e].z);
-                o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + w * x[e].w);
-              }
+              for (int k = 0; k < 4; ++k)
+                o[4 * e + k] = __float_as_uint(in_order(behind, __fmul_rn(__uint_as_float(o[4 * e + k]), w_own),
+                                                        __fmul_rn(xe[k], w_part[0]), __fmul_rn(ye[k], w_part[1])));
             }
           }
 #pragma unroll

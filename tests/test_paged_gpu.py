@@ -399,6 +399,16 @@ def test_paged_prefill_items_shared_by_few_and_many(gen, ws, heads, n_kv, lens, 
     run_paged_prefill(gen, ws, heads, n_kv, 64, lens, starts, behind=2)
 
 
+@pytest.mark.parametrize("heads,n_kv,lens,starts", [(32, 8, [600, 40], [5000, 3000]), (32, 8, [1024], [7168])])
+def test_paged_prefill_does_not_depend_on_who_is_last(gen, ws, heads, n_kv, lens, starts):
+    k_pages, v_pages, table, rows = fill_cache(gen, [s + t for s, t in zip(starts, lens)], 64, n_kv)
+    q = P.normal(gen, sum(lens), heads, P.D, scale=1.5)
+    args = (q, offsets(lens), ints(starts), k_pages, v_pages, table)
+    first = G.paged_prefill(*args, workspace=ws)
+    for _ in range(40):
+        assert torch.equal(first, G.paged_prefill(*args, workspace=ws))
+
+
 def test_paged_prefill_joins_only_its_own_items(gen, ws):
     # the second call has none to join: what the first left stays unread
     k_pages, v_pages, table, ((k, v),) = fill_cache(gen, [9000], 64, 2)
