@@ -262,8 +262,9 @@ int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, c
   const int r = check_pages(pages, &p.pages);
   if (r != GQA_OK) return r;
   if (!aligned4(start_pos)) return GQA_EALIGN;
-  // the key tiles of the (at most 320) items that are cut into ranges are counted in 31 bits over the KV heads
-  if ((static_cast<long long>(pages->columns) * pages->page_size / PACKED_TILE + 1) * 320 * pages->n_kv_heads >
+  // the key tiles of the (at most 320) items that are cut into ranges, and two
+  // units for each item, are counted in 31 bits over the KV heads
+  if ((static_cast<long long>(pages->columns) * pages->page_size / PACKED_TILE + 3) * 320 * pages->n_kv_heads >
       0x7fffffffLL)
     return GQA_EINVAL;
   p.start = start_pos;

@@ -33,14 +33,18 @@
 // and the cheapest of the three by the costs below is taken:
 //   - Ranges of half the longest item at least. An item then has three parts
 //     at most, and the CTA that arrives last at its count adds the others to
-//     its own in its epilogue: it waits only for CTAs that have arrived, which
-//     are running and about to write. 1,024 tokens after 7,168 (128 items on
-//     152 SMs): 100 us, 112 with all parts left to a second kernel.
+//     its own in its epilogue, all in CTA order: it waits only for CTAs that
+//     have arrived, which are running and about to write. 1,024 tokens after
+//     7,168 (128 items on 152 SMs): 100 us, 112 with all parts left to a second
+//     kernel.
 //   - Shorter ranges, whose items' parts a second kernel joins, in CTA order:
 //     25 us for 40 tokens after 8,000 (8 heads, 2 KV heads), where a join by
-//     the last CTA took 47; 33 for 256 after 4,000 (32 and 8 heads) against 52.
+//     the last CTA took 47; 32 for 256 after 4,000 (32 and 8 heads) against 52.
 //     Empty, that kernel takes 2 us, so it is not launched where no sequence
 //     can have more than 2,048 keys.
+// An item counts ITEM_UNITS key tiles more than it has, or a range of many
+// short items ends last: 45 us against 59 for one prompt of 4,000 tokens (8 and
+// 2 heads), 32 against 36 for 2,340.
 //
 // Masked and foreign values. Q boxes may reach into the next sequence (rows
 // that are never stored), K and V boxes into the next sequence's rows, a
@@ -62,9 +66,9 @@
 // Every wait is bounded; one that gives up records DEV_WAIT_TIMEOUT, lets
 // issued copies and products finish (bounded) and frees TMEM before the CTA
 // exits.
-// Measured: 400 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,445
-// TFLOP/s of 1,962 measured), 100 for 1,024 tokens after 7,168, 35.3 for
-// 2,048 tokens, 7.0 for 17. What bounds the long ones is the alternation: per
+// Measured: 402 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,437
+// TFLOP/s of 1,962 measured), 100 to 106 for 1,024 tokens after 7,168, 35.2 for
+// 2,048 tokens, 7.1 for 17. What bounds the long ones is the alternation: per
 // key tile the tensor pipe works 2 x 1,024 of 2,900 cycles.
 #include <math.h>
 
@@ -101,6 +105,7 @@ constexpr int SLOTS = 2;                  // items handed from the producer to t
 // last CTA writes none and reads two); with more 14 us for writing two parts
 // and the second kernel, and 9 us per 40 MB of parts that it reads.
 constexpr float DIRECT_ROW = 10.f / (NQ * ROWS), JOIN_TILES = 9.f, JOIN_ROW = 1.4e-4f;
+constexpr int ITEM_UNITS = 2;             // what an item takes beside its key tiles, in those (2.8 us)
 constexpr int MAX_PARTS = 64;             // of an item
 constexpr int MIN_TILES = 3;              // key tiles of a part at least
 constexpr uint32_t TMEM_COLS = 512;
@@ -189,25 +194,28 @@ struct Split {
   }
 };
 
-// Equal ranges: the key tiles in (entry, KV head, key tile) order are the
-// units, cum[e] x n_kv of them before entry e. The item with unit u, from u on
-// as far as the range that ends at `end` goes.
-__device__ __forceinline__ Item ranged_item(int u, int end, const Split& split, int E, const int* cum, const int* pre,
+// Equal ranges: an item is its key tiles and, before them, ITEM_UNITS units for
+// what else it takes; in (entry, KV head, key tile) order there are cum[e] x
+// n_kv units before entry e. The item with unit u, from u on as far as the range
+// that ends at `end` goes (n = 0: it has no tile there); u becomes the first
+// unit behind that.
+__device__ __forceinline__ Item ranged_item(int& u, int end, const Split& split, int E, const int* cum, const int* pre,
                                             int qp, const PackedPrefillParams& a) {
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (cum[mid] * a.n_kv <= u) lo = mid; else hi = mid;
   }
-  const int n = cum[lo + 1] - cum[lo], x = u - cum[lo] * a.n_kv;
+  const int w = cum[lo + 1] - cum[lo], x = u - cum[lo] * a.n_kv;
   Item it = entry_at(lo, pre, qp, a);
-  it.g = x / n;
-  it.j0 = x - it.g * n;
-  const int base = u - it.j0;  // the item's first unit
-  const int j1 = min(n, end - base);
+  it.g = x / w;
+  const int base = cum[lo] * a.n_kv + it.g * w + ITEM_UNITS;  // the unit of the item's first tile
+  const int j1 = min(w - ITEM_UNITS, end - base);
+  it.j0 = max(0, u - base);
   it.first = split.holder(base);
-  it.last = split.holder(base + n - 1);
-  it.n = j1 - it.j0;
+  it.last = split.holder(base + w - ITEM_UNITS - 1);
+  it.n = max(0, j1 - it.j0);
+  u = min(end, base + w - ITEM_UNITS);
 #pragma unroll
   for (int t = 0; t < NQ; ++t) it.nt[t] = max(0, min(it.nt[t], j1) - it.j0);
   return it;
@@ -524,7 +532,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // nothing to plan where every CTA has one short item at most
   if (E <= MAX_SORT && (__syncthreads_or(own_n > 2 * MIN_TILES) || nitems > G)) {
     const int e = threadIdx.x;
-    if (e < E) bs.cum[e + 1] = own_n;
+    const int own_w = own_n ? own_n + ITEM_UNITS : 0;
+    if (e < E) bs.cum[e + 1] = own_w;
     if (e == 0) bs.cum[0] = 0;
     __syncthreads();
     int before = 0, rank = 0;
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int f = 0; f < E; ++f) {
         const int m = bs.cum[f + 1];
         before += f <= e ? m : 0;
-        rank += m > own_n || (m == own_n && f < e);
+        rank += m > own_w || (m == own_w && f < e);
       }
     __syncthreads();
     if (e < E) {
@@ -601,10 +610,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         return true;
       }
       // units in (entry, KV head, key tile) order; this CTA's range of them
-      if (ru < rend) {
+      while (ru < rend) {
         it = ranged_item(ru, rend, split, E, bs.cum, pre, qp, a);
-        ru += it.n;
-        return true;
+        if (it.n > 0) return true;
       }
       // entries without keys (unused slots), whose rows are zero
       for (;;) {
@@ -1159,7 +1167,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (equal && static_cast<int>(blockIdx.x) < parts) {
       const Split split(units, parts);
       const int end = split.start(blockIdx.x + 1);
-      it = ranged_item(end - 1, end, split, E, bs.cum, pre, qp, a);
+      int u = end - 1;
+      it = ranged_item(u, end, split, E, bs.cum, pre, qp, a);
       if (it.first != static_cast<int>(blockIdx.x)) it.last = it.first;
     }
     reinterpret_cast<Item*>(a.joins)[blockIdx.x] = it;

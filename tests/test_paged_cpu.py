@@ -315,39 +315,56 @@ def test_decode_ranges_cover_every_chunk_once_and_tickets_count(lens, n_kv, warp
         assert len(set(arrivals)) == 1 and len(arrivals) == arrivals[0][1]
 
 
+ITEM_UNITS = 2
+
+
 @pytest.mark.parametrize("tiles", [[64] * 4, [57, 58, 59, 60, 61, 62, 63, 64], [157, 1, 0, 3], [469], [1, 1, 20]])
 @pytest.mark.parametrize("n_kv", [1, 2, 8])
 def test_prefill_ranges_cover_every_key_tile_once(tiles, n_kv):
-    """Equal ranges of key tiles: every tile of every item in one part; the
-    parts of an item come from the CTAs its first and last unit lie in, one
-    each, at most two shared items per CTA, begun before it and going on behind."""
+    """Equal ranges of units (an item: its key tiles and two units before
+    them): every tile of every item in one part; the parts of an item come from
+    the CTAs that its first and last tile lie in, one each, at most two shared
+    items per CTA, begun before it and going on behind; the item of a range's
+    last unit is the one that goes on."""
     cum = [0]
     for n in tiles:
-        cum.append(cum[-1] + n)
+        cum.append(cum[-1] + (n + ITEM_UNITS if n else 0))
     units = cum[-1] * n_kv
     parts = min(152, units // 3)
     if parts < 2:
         return
     split = Split(units, parts)
+
+    def item(u, end):
+        e = max(i for i in range(len(tiles)) if cum[i] * n_kv <= u)
+        w = cum[e + 1] - cum[e]
+        assert w > 0
+        g = (u - cum[e] * n_kv) // w
+        base = cum[e] * n_kv + g * w + ITEM_UNITS
+        j1, j0 = min(w - ITEM_UNITS, end - base), max(0, u - base)
+        return e, g, j0, j1, split.holder(base), split.holder(base + w - ITEM_UNITS - 1), min(end, base + w - ITEM_UNITS)
+
     seen, slots = {}, set()
     for c in range(parts):
         u, end = split.start(c), split.start(c + 1)
         assert end > u
+        goes_on = None
         while u < end:
-            e = max(i for i in range(len(tiles)) if cum[i] * n_kv <= u)
-            n = cum[e + 1] - cum[e]
-            assert n > 0
-            g, j0 = divmod(u - cum[e] * n_kv, n)
-            base = u - j0
-            j1 = min(n, end - base)
-            first, last = split.holder(base), split.holder(base + n - 1)
+            e, g, j0, j1, first, last, after = item(u, end)
+            assert after > u
+            u = after
+            if j1 <= j0:
+                continue
             assert first <= c <= last and (j0 == 0) == (c == first)
             if first != last:
                 slot = 2 * c + (c == first)
                 assert slot not in slots
                 slots.add(slot)
+                if c == first:
+                    goes_on = e, g, last
             seen.setdefault((e, g), []).append((j0, j1, c, first, last))
-            u = base + j1
+        e, g, _, _, first, last, _ = item(end - 1, end)
+        assert goes_on == ((e, g, last) if first == c and last > c else None)
     for (e, g), got in seen.items():
         at = 0
         for j0, j1, c, first, last in got:
@@ -368,8 +385,8 @@ def test_prefill_ranges_bound_the_parts_of_an_item(n_kv, few):
         tiles = [rng.randint(0, top) for _ in range(rng.randint(1, 320))]
         cum = [0]
         for n in tiles:
-            cum.append(cum[-1] + n)
-        units, longest = cum[-1] * n_kv, max(tiles)
+            cum.append(cum[-1] + (n + ITEM_UNITS if n else 0))
+        units, longest = cum[-1] * n_kv, max(tiles) + ITEM_UNITS
         if units < 6:
             continue
         mean = max((units + 151) // 152, 3)
@@ -378,7 +395,7 @@ def test_prefill_ranges_bound_the_parts_of_an_item(n_kv, few):
         split = Split(units, parts)
         for e, n in enumerate(tiles):
             for g in range(n_kv if n else 0):
-                base = cum[e] * n_kv + g * n
+                base = cum[e] * n_kv + g * (n + ITEM_UNITS) + ITEM_UNITS
                 assert split.holder(base + n - 1) - split.holder(base) < (3 if few else 64)
 
 
