@@ -38,7 +38,7 @@
 //     7,168 (128 items on 152 SMs): 100 us, 112 with all parts left to a second
 //     kernel.
 //   - Shorter ranges, whose items' parts a second kernel joins, in CTA order:
-//     25 us for 40 tokens after 8,000 (8 heads, 2 KV heads), where a join by
+//     22 us for 40 tokens after 8,000 (8 heads, 2 KV heads), where a join by
 //     the last CTA took 47; 32 for 256 after 4,000 (32 and 8 heads) against 52.
 //     Empty, that kernel takes 2 us, so it is not launched where no sequence
 //     can have more than 2,048 keys.
@@ -100,11 +100,14 @@ constexpr int SMEM_BYTES = OUT_OFF + 8 * OUT_WARP + 1024;
 constexpr int THREADS = 352;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                  // items handed from the producer to the other warps
-// What sharing items costs, in key tiles of one CTA (about 1.6 us), measured on
-// full items of 256 rows and scaled: with up to 1 + DIRECT parts 18 us (the
-// last CTA writes none and reads two); with more 14 us for writing two parts
-// and the second kernel, and 9 us per 40 MB of parts that it reads.
-constexpr float DIRECT_ROW = 10.f / (NQ * ROWS), JOIN_TILES = 9.f, JOIN_ROW = 1.4e-4f;
+// What sharing items costs, in key tiles of one CTA (about 1.6 us), by the rows
+// of an item: with up to 1 + DIRECT parts, of which the last CTA reads two; with
+// more, for the second kernel, writing two parts and reading all. Measured: 18
+// and 14 us for full items of 256 rows and 9 us per 40 MB that the second kernel
+// reads, little for few rows (5 tokens after 2,100, 8 and 2 heads: 17 us by
+// short ranges, 29 by halves).
+constexpr float DIRECT_TILES = 2.f, DIRECT_ROW = 8.f / (NQ * ROWS);
+constexpr float JOIN_TILES = 4.f, JOIN_ROW = 5.f / (NQ * ROWS), JOIN_PART_ROW = 1.4e-4f;
 constexpr int ITEM_UNITS = 2;             // what an item takes beside its key tiles, in those (2.8 us)
 constexpr int MAX_PARTS = 64;             // of an item
 constexpr int MIN_TILES = 3;              // key tiles of a part at least
@@ -354,10 +357,15 @@ struct Rows {
 // that CTA x of the first kernel began, if it is shared, block y a slice of its
 // rows. One part per (CTA, item), in CTA order: the result does not depend on
 // who was first.
-constexpr int JOIN_THREADS = 256, JOIN_SLICE = 32, JOIN_SLICES = NQ * ROWS / JOIN_SLICE;
+// Short slices are faster (40 tokens after 8,000: 21.7 us with 16 rows, 25.3
+// with 32), many blocks slower where there is nothing to join (16 a CTA 1.2 us
+// more than 8): 16 rows where an item can have no more than 160.
+constexpr int JOIN_THREADS = 256;
+template <int SLICE>
 __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const __grid_constant__ PackedPrefillParams a) {
-  __shared__ float weight[MAX_PARTS][JOIN_SLICE];
-  __shared__ int off[JOIN_SLICE], bad[JOIN_SLICE];
+  constexpr int LANES = JOIN_THREADS / SLICE;  // of a row
+  __shared__ float weight[MAX_PARTS][SLICE];
+  __shared__ int off[SLICE], bad[SLICE];
   pdl_trigger();
   pdl_wait();
   const Item it = reinterpret_cast<const Item*>(a.joins)[blockIdx.x];
@@ -371,31 +379,31 @@ __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const
     return;
   const int nrep = a.n_heads / a.n_kv, qp = ROWS / nrep, tid = threadIdx.x, lane = tid & 31;
   const Rows n(it, qp, nrep);
-  const int r0 = blockIdx.y * JOIN_SLICE;
+  const int r0 = blockIdx.y * SLICE;
   if (r0 >= n.span) return;
   {
-    // eight lanes a row: its max over the parts, the parts' factors, the sum
-    const int r = tid >> 3, row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep;
+    // a row's lanes: its max over the parts, the parts' factors, the sum
+    const int r = tid / LANES, row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep;
     const bool real = row < n.span && rr < (t ? n.rows1 : n.rows0);
     float m = -INFINITY, l = 0.f;
     if (real)
-      for (int c = tid & 7; c < np; c += 8) m = fmaxf(m, __ldcg(part_ml(a, part_slot(it.first + c, it.first)) + row).x);
+      for (int c = tid % LANES; c < np; c += LANES) m = fmaxf(m, __ldcg(part_ml(a, part_slot(it.first + c, it.first)) + row).x);
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int d = LANES / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if (m == -INFINITY) m = 0.f;
     if (real)
-      for (int c = tid & 7; c < np; c += 8) {
+      for (int c = tid % LANES; c < np; c += LANES) {
         const float2 ml = __ldcg(part_ml(a, part_slot(it.first + c, it.first)) + row);
         const float w = ex2_approx(ml.x - m);
         l += w * ml.y;
         weight[c][r] = w;
       }
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    for (int d = LANES / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float inv = 1.f / l;
     if (real)
-      for (int c = tid & 7; c < np; c += 8) weight[c][r] *= inv;
-    if ((tid & 7) == 0) {
+      for (int c = tid % LANES; c < np; c += LANES) weight[c][r] *= inv;
+    if (tid % LANES == 0) {
       off[r] = real ? ((t * qp + rp) * a.n_heads + it.g * nrep + rr - rp * nrep) * HEAD_DIM : -1;
       bad[r] = 0;
     }
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const
   // a warp: 8 rows x 4 column groups, so that whole sectors are read and stored
   __nv_bfloat16* out = a.out + (static_cast<size_t>(it.row0) + it.q0) * a.n_heads * HEAD_DIM;
   const int g = (tid >> 5) * 4 + (lane >> 3);
-  constexpr int EACH = JOIN_SLICE / 8;
+  constexpr int EACH = SLICE / 8;
   float4 o[EACH];
 #pragma unroll
   for (int i = 0; i < EACH; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -432,7 +440,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const
     *(reinterpret_cast<uint2*>(out + off[r]) + g) = make_uint2(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i].z, o[i].w));
   }
   __syncthreads();
-  for (int r = tid >> 5; r < JOIN_SLICE; r += JOIN_THREADS / 32) {
+  for (int r = tid >> 5; r < SLICE; r += JOIN_THREADS / 32) {
     const int row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep, pos = it.q0 + t * qp + rp;
     if (bad[r] && it.start + pos < it.kv_end - 1)
       masked_row(a, it.b, it.row0, it.g, it.start, pos, it.g * nrep + rr - rp * nrep, it.kv_end);
@@ -568,10 +576,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int mean = max((units + G - 1) / G, MIN_TILES);
     // ranges of half an item: each in three at most
     const int few = max(mean, (longest + 1) / 2);
-    const float few_cost = few + DIRECT_ROW * bs.rows;
+    const float few_cost = few + DIRECT_TILES + DIRECT_ROW * bs.rows;
     // whole tiles: no item then lies in more than MAX_PARTS ranges
     const int many = max(mean, (longest + MAX_PARTS - 3) / (MAX_PARTS - 2));
-    const float many_cost = a.joins ? many + JOIN_TILES + JOIN_ROW * (units / many) * bs.rows : INFINITY;
+    const float many_cost = a.joins ? many + JOIN_TILES + (JOIN_ROW + JOIN_PART_ROW * (units / many)) * bs.rows : INFINITY;
     equal = __syncthreads_or(static_cast<float>(load) > fminf(few_cost, many_cost));
     if (equal) parts = min(G, max(1, units / (few_cost <= many_cost ? few : many)));
   }
@@ -1193,7 +1201,12 @@ bool packed_prefill_may_join(int N, int n_rep, long long most_keys) {
 size_t packed_prefill_join_bytes(int ctas) { return ctas * sizeof(Item); }
 
 cudaError_t launch_packed_prefill_join(const PackedPrefillParams& a, cudaStream_t s) {
-  return launch_behind(packed_prefill_join_kernel, dim3(a.ctas, JOIN_SLICES), JOIN_THREADS, 0, s, a);
+  // the most rows that an item can span
+  const int n_rep = a.n_heads / a.n_kv, qp = ROWS / n_rep;
+  const int rows = a.N <= qp ? a.N * n_rep : ROWS + (a.N - qp < qp ? a.N - qp : qp) * n_rep;
+  if (rows <= 160)
+    return launch_behind(packed_prefill_join_kernel<16>, dim3(a.ctas, (rows + 15) / 16), JOIN_THREADS, 0, s, a);
+  return launch_behind(packed_prefill_join_kernel<32>, dim3(a.ctas, (rows + 31) / 32), JOIN_THREADS, 0, s, a);
 }
 
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& a, cudaStream_t s) {
