@@ -394,7 +394,10 @@ def test_paged_prefill_one_item_over_every_cta(gen, ws):
 
 @pytest.mark.parametrize("heads,n_kv,lens,starts", [
     (8, 2, [300], [9000]), (28, 4, [100], [5000]), (28, 4, [1, 90], [7000, 2500]), (16, 16, [130], [4000]),
-    (32, 8, [600, 40], [5000, 3000]), (32, 8, [1000], [1500]), (4, 1, [2500], [0]), (16, 1, [40], [30000])])
+    (32, 8, [600, 40], [5000, 3000]), (32, 8, [1000], [1500]), (4, 1, [2500], [0]), (16, 1, [40], [30000]),
+    # around the most rows that an item can span in the join's short slices
+    (8, 2, [5], [2100]), (8, 2, [40], [8000]), (8, 2, [41], [8000]), (28, 4, [18], [3000]), (28, 4, [19], [3000]),
+    (28, 4, [23], [3000]), (4, 4, [129], [3000]), (4, 4, [161], [3000]), (16, 1, [9, 3], [5000, 9000])])
 def test_paged_prefill_items_shared_by_few_and_many(gen, ws, heads, n_kv, lens, starts):
     run_paged_prefill(gen, ws, heads, n_kv, 64, lens, starts, behind=2)
 
