@@ -501,7 +501,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Seq s = seq_at(a, b);
       if (a.start && blockIdx.x == 0 && s.T > 0) {
         const int st = a.start[b];
-        if (st < -1 || st + static_cast<long long>(s.T) > a.pages.capacity()) report(a.status, DEV_BAD_POSITION);
+        // an unused slot (-1) holds any number of tokens
+        if (st < -1 || (st >= 0 && st + static_cast<long long>(s.T) > a.pages.capacity()))
+          report(a.status, DEV_BAD_POSITION);
       }
       const int n = (s.T + NQ * qp - 1) / (NQ * qp);
       pre[b + 1] = n;

@@ -452,6 +452,23 @@ def test_bad_positions_are_reported_and_skipped(gen, ws):
     assert G.device_status(ws, clear=True) == 1
 
 
+@pytest.mark.parametrize("padding", [16, 17, 18, 300])
+def test_an_unused_slot_may_be_longer_than_its_table(gen, ws, padding):
+    # a padded batch keeps its padding tokens in one slot without pages
+    k_pages, v_pages, table, rows = fill_cache(gen, [16, 0], 16, 2)
+    q, k, v = (P.normal(gen, 2 + padding, h, P.D) for h in (8, 2, 2))
+    cu, start = offsets([2, padding]), ints([14, -1])
+    out = torch.full_like(q, 9.0)
+    G.paged_prefill(q, cu, start, k_pages, v_pages, table, out=out, workspace=ws)
+    assert G.device_status(ws, clear=True) == 0
+    check_prefill(out, q, rows, [2, padding], [14, -1])
+    G.paged_append(q, k, v, start, G.rope_table(16), k_pages, v_pages, table, cu_tokens=cu, workspace=ws)
+    assert G.device_status(ws, clear=True) == 0
+    # a sequence of as many tokens is reported all the same
+    G.paged_prefill(q, cu, ints([14, 0 if padding > 16 else 1]), k_pages, v_pages, table, workspace=ws)
+    assert G.device_status(ws, clear=True) == 1
+
+
 @pytest.mark.parametrize("entry", [-1, 1 << 20])
 def test_bad_pages_are_reported(gen, ws, entry):
     k_pages, v_pages, table, rows = fill_cache(gen, [40, 40], 16, 2)
