@@ -334,8 +334,9 @@ def set_decode_fusion(enable: bool) -> bool:
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Limit (ns) of the decode kernels' grid-wide waits on this thread; 0
-    restores the default (2 s). Returns the previous limit."""
+    """Limit (ns) of the packed prefill attention's waits and of the block's
+    decode kernels' grid-wide waits on this thread; 0 restores the default (2 s).
+    Returns the previous limit."""
     if ns < 0:
         raise ValueError("the wait limit is a non-negative number of nanoseconds")
     return int(lib().gqa_set_wait_limit_ns(int(ns)))

@@ -17,7 +17,7 @@ thread_local void* const* t_prof_events = nullptr;
 thread_local int t_prof_count = 0;
 thread_local int t_fused = 1;
 thread_local int t_attn_split = 0;  // fused decode attention: 0 chosen per call, 1 position-major, 2 head-major
-thread_local unsigned long long t_wait_ns = WAIT_LIMIT_NS;  // grid-wide waits of the decode kernels
+thread_local unsigned long long t_wait_ns = WAIT_LIMIT_NS;  // gqa_set_wait_limit_ns
 thread_local int t_prof_base = 0;  // 1 while a layer call's norm kernel occupies events[0..1]
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -78,6 +78,8 @@ int fail_cuda(cudaError_t e) {
   t_last_cuda = e;
   return GQA_ECUDA;
 }
+
+unsigned long long wait_limit_ns() { return t_wait_ns; }
 
 void begin_call() {
   t_launches = 0;

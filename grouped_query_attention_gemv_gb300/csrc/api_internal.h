@@ -13,6 +13,7 @@ int launch_sms();  // min(sm_count(), REF_SMS)
 
 bool aligned16(const void* p);
 int fail_cuda(cudaError_t e);                // remembers e for gqa_strerror; GQA_ECUDA
+unsigned long long wait_limit_ns();          // gqa_set_wait_limit_ns of this thread
 void begin_call();                           // no kernel enqueued yet by the current call
 int launched(cudaError_t e);                 // counts a launch that returned e; GQA_OK or GQA_ECUDA
 void prof_mark(int i, cudaStream_t s);       // gqa_set_profile_events: event i, if set

@@ -231,6 +231,7 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   p.tickets = reinterpret_cast<int*>(ws + TICKETS_OFFSET);
   p.part_ml = reinterpret_cast<float*>(ws + PART_ML_OFFSET);
   p.part_o = reinterpret_cast<float*>(ws + PART_ML_OFFSET + PREFILL_ML_BYTES);
+  p.wait_ns = wait_limit_ns();
   p.ctas = launch_sms();
   const int n_rep = n_heads / n_kv;
   if (packed_prefill_may_join(N, n_rep, most_keys)) p.joins = ws + JOINS_OFFSET;

@@ -63,7 +63,8 @@
 // P is rounded to bf16 (the product takes no wider operand); sums are fp32 of
 // the unrounded values. O is rescaled only when a row's max grows by more than
 // 2^8 over the max its P values were taken against.
-// Every wait is bounded; one that gives up records DEV_WAIT_TIMEOUT, lets
+// Every wait is bounded (gqa_set_wait_limit_ns); one that gives up records
+// DEV_WAIT_TIMEOUT, lets
 // issued copies and products finish (bounded) and frees TMEM before the CTA
 // exits.
 // Measured: 402 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,437
@@ -224,14 +225,19 @@ __device__ __forceinline__ Item ranged_item(int& u, int end, const Split& split,
   return it;
 }
 
+// Wait of a whole warp for phase `parity` of a barrier; false when it gave up.
+__device__ __forceinline__ bool wait_bar(uint64_t& bar, unsigned parity, const PackedPrefillParams& a) {
+  return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, a.wait_ns));
+}
+
 // The items of this CTA in order, as the other warps take them from the
 // producer's slots.
 struct ItemWalk {
   int k = 0;
   bool ok = true;
-  __device__ __forceinline__ bool next(Bars& bs, Item& it) {
+  __device__ __forceinline__ bool next(Bars& bs, Item& it, const PackedPrefillParams& a) {
     const int s = k % SLOTS;
-    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.item_full[s]), (k / SLOTS) & 1));
+    ok = wait_bar(bs.item_full[s], (k / SLOTS) & 1, a);
     if (!ok) return false;
     it = bs.item[s];
     __syncwarp();
@@ -319,10 +325,10 @@ __device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int
 }
 
 // Barrier of the softmax warps, the n-th of a CTA; false when it gave up.
-__device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n) {
+__device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n, const PackedPrefillParams& a) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bs.joint));
-  return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.joint), n++ & 1));
+  return wait_bar(bs.joint, n++ & 1, a);
 }
 
 // Parts of an item that several CTAs share: slot 2 c + 1 for the CTA with the
@@ -641,8 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int puts = 0;
     auto put = [&](const Item& x) {
       const int s = puts % SLOTS;
-      if (puts >= SLOTS && !__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.item_empty[s]), (puts / SLOTS - 1) & 1)))
-        return false;
+      if (puts >= SLOTS && !wait_bar(bs.item_empty[s], (puts / SLOTS - 1) & 1, a)) return false;
       if (lane == 0) {
         bs.item[s] = x;
         mbar_arrive(smem_u32(&bs.item_full[s]));
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int cs[NQ] = {};  // score tiles of each Q tile so far (as its issuer counts them)
     bool ok = true, stop = false;
     auto go_on = [&](uint64_t& bar, int parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity));
+      ok = wait_bar(bar, parity, a);
       return ok && !__any_sync(0xffffffffu, aborted(bs));
     };
     auto copy = [&](const CUtensorMap* map, uint64_t& full, uint32_t dst, int held, int g, int row, int page) {
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned u0 = 0, cs = 0, qi = 0, step = 0;
     bool ok = true;
     auto wait = [&](uint64_t& bar, unsigned parity) {
-      return ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity));
+      return ok = wait_bar(bar, parity, a);
     };
     // the stage is free once this issuer's products on it are done (a commit
     // covers every product the thread issued before it)
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     };
-    while (ok && walk.next(bs, it)) {
+    while (ok && walk.next(bs, it, a)) {
       if (it.n == 0) continue;
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
@@ -880,7 +885,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned cs = 0;  // score tiles of this Q tile over the items (as the issuer counts them)
     unsigned syncs = 0, items = 0;  // items with keys of this Q tile
     bool ok = true;
-    while (ok && walk.next(bs, it)) {
+    while (ok && walk.next(bs, it, a)) {
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int pos = it.q0 + t * qp + rp;  // query index within the sequence
       const bool real = used && pos < it.T;
@@ -898,7 +903,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m_limit = -INFINITY, neg = 0.f;  // max that P is still taken against m_ref with; -m_ref in log2 units
       for (int j = 0; j < n_t; ++j) {
         // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.s_full[t]), (cs + j) & 1))) {
+        if (!wait_bar(bs.s_full[t], (cs + j) & 1, a)) {
           ok = false;
           break;
         }
@@ -991,7 +996,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       if (n_t > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bs.o_done[t]), items & 1))) {
+        if (!wait_bar(bs.o_done[t], items & 1, a)) {
           ok = false;
           break;
         }
@@ -1014,7 +1019,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int* arrived = a.tickets + 2 * it.first;
         if (others <= DIRECT) {
           if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
-          if (!softmax_sync(bs, syncs)) {
+          if (!softmax_sync(bs, syncs, a)) {
             ok = false;
             break;
           }
@@ -1051,11 +1056,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (others <= DIRECT) {
           if (whole && threadIdx.x == 0) {
             // the others' parts are written
-            bs.parts_there = wait_counter(arrived + 1, others);
+            bs.parts_there = wait_counter(arrived + 1, others, a.wait_ns);
             arrived[0] = 0;
             arrived[1] = 0;
           }
-          if (!softmax_sync(bs, syncs) || (whole && !bs.parts_there)) {
+          if (!softmax_sync(bs, syncs, a) || (whole && !bs.parts_there)) {
             ok = false;
             break;
           }

@@ -124,6 +124,7 @@ struct PackedPrefillParams {
   void* joins;
   int *tickets, *claims;
   int* status;
+  unsigned long long wait_ns;  // limit of the waits
   int ctas;
 };
 // q: (dim, head, token), boxes of 64 dims x n_rep heads x 128 / n_rep tokens.

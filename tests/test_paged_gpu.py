@@ -1,6 +1,7 @@
 """The paged serving operators against 64-bit references, at the sizes, masks
 and layouts where they can go wrong."""
 import math
+import time
 
 import pytest
 import torch
@@ -485,6 +486,44 @@ def test_bad_pages_are_reported(gen, ws, entry):
     assert G.device_status(ws, clear=True) == 3
     # the same workspace serves the next call
     run_decode(gen, ws, 8, 2, 16, [300, 40])
+
+
+TICKETS = 256   # byte offset in the workspace: of each CTA, parts that arrived and parts that are written
+
+
+def test_a_wait_that_runs_out_is_reported_and_recovered(gen):
+    """Failure injected on the host: the counts of written parts are set so far
+    back that the CTA that adds them up waits in vain. The call ends after the
+    limit, records GQA_DEV_WAIT_TIMEOUT and touches nothing but its rows; zero-filled,
+    the workspace serves the next call."""
+    ws = G.make_paged_workspace()
+    k_pages, v_pages, table, rows = fill_cache(gen, [8192], 64, 8)
+    q = P.normal(gen, 1026, 32, P.D)
+    out = torch.full_like(q, 9.0)
+    args = (q, offsets([1024]), ints([7168]), k_pages, v_pages, table)
+    G.paged_prefill(*args, out=out, workspace=ws)
+    check_prefill(out, q, rows, [1024], [7168])
+    before = [x.view(torch.int16).clone() for x in (k_pages, v_pages)]
+    counts = ws[TICKETS:TICKETS + 152 * 8].view(torch.int32)
+    assert int(counts.abs().sum()) == 0
+    counts[1::2] = -(1 << 30)
+    torch.cuda.synchronize()
+    prev = G.set_wait_limit_ns(1_000_000)
+    try:
+        t0 = time.perf_counter()
+        G.paged_prefill(*args, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - t0
+    finally:
+        G.set_wait_limit_ns(prev)
+    assert G.device_status(ws) == 2
+    assert took < 0.5, f"a limit of 1 ms ended the call after {took:.2f} s"
+    assert (out[1024:] == 9.0).all()
+    assert all(torch.equal(x.view(torch.int16), y) for x, y in zip((k_pages, v_pages), before))
+    ws.zero_()
+    G.paged_prefill(*args, out=out, workspace=ws)
+    assert G.device_status(ws) == 0
+    check_prefill(out, q, rows, [1024], [7168])
 
 
 # ------------------------------------------------------------------ as a server uses them
