@@ -136,6 +136,8 @@ struct Bars {
   uint64_t item_full[SLOTS], item_empty[SLOTS], joint;
   uint32_t tmem_slot;
   int abort;
+  unsigned long long wait_ns;  // limit of the waits
+  unsigned alive;             // counts up while rows are computed again
   int q_issued[NQ], k_issued, v_issued;
   int warp_sum[THREADS / 32];
   int rows;                   // most query rows of an item
@@ -225,9 +227,23 @@ __device__ __forceinline__ Item ranged_item(int& u, int end, const Split& split,
   return it;
 }
 
-// Wait of a whole warp for phase `parity` of a barrier; false when it gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t& bar, unsigned parity, const PackedPrefillParams& a) {
-  return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity, a.wait_ns));
+// Wait of a whole warp for phase `parity` of a barrier; false when it gave up:
+// after bs.wait_ns in which no row was computed again either (masked_row takes
+// as long as the row's keys are many, and the others wait for its warp). All
+// but the first try is out of line: inlined at the eleven waits the loop cost
+// 3% (2,048 tokens 35.9 us against 34.3, nine prompts 439 against 424).
+__device__ __noinline__ bool wait_longer(const Bars& bs, uint32_t bar, unsigned parity) {
+  unsigned alive = 0;
+  while (!__all_sync(0xffffffffu, mbar_wait(bar, parity, bs.wait_ns))) {
+    const unsigned now = *const_cast<const volatile unsigned*>(&bs.alive);
+    if (!__any_sync(0xffffffffu, now != alive)) return false;
+    alive = now;
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_bar(const Bars& bs, uint64_t& bar, unsigned parity) {
+  const uint32_t at = smem_u32(&bar);
+  return __all_sync(0xffffffffu, mbar_try_wait(at, parity)) || wait_longer(bs, at, parity);
 }
 
 // The items of this CTA in order, as the other warps take them from the
@@ -235,9 +251,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t& bar, unsigned parity, const P
 struct ItemWalk {
   int k = 0;
   bool ok = true;
-  __device__ __forceinline__ bool next(Bars& bs, Item& it, const PackedPrefillParams& a) {
+  __device__ __forceinline__ bool next(Bars& bs, Item& it) {
     const int s = k % SLOTS;
-    ok = wait_bar(bs.item_full[s], (k / SLOTS) & 1, a);
+    ok = wait_bar(bs, bs.item_full[s], (k / SLOTS) & 1);
     if (!ok) return false;
     it = bs.item[s];
     __syncwarp();
@@ -262,9 +278,11 @@ __device__ __forceinline__ long long key_row(const PackedPrefillParams& a, int b
 // fp32: 32 keys at a time, a key a lane for the scores, 4 dims a lane for the
 // values. For rows whose result is not finite and that share tiles with later
 // keys of their item (up to kv_end): nothing is done where those values are
-// all finite, because the row's own keys then made it so.
+// all finite, because the row's own keys then made it so. A row takes 0.37 us
+// a key (48 ms after 131,072), so `alive`, if there is one, is counted up on
+// the way: waits on this warp then go on.
 __device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int row0, int g, int start, int pos,
-                                        int head, int kv_end) {
+                                        int head, int kv_end, unsigned* alive) {
   const size_t row = static_cast<size_t>(row0) + pos;
   const __nv_bfloat16* q = a.q + static_cast<long long>(row) * a.q_stride + head * HEAD_DIM;
   __nv_bfloat16* dst = a.out + (row * a.n_heads + head) * HEAD_DIM;
@@ -284,6 +302,7 @@ __device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int
   if (!dirty) return;
   float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 <= lim; j0 += 32) {
+    if (alive && lane == 0) atomicAdd(alive, 1u);
     float s = -INFINITY;
     if (j0 + lane <= lim) {
       const uint4* k4 = reinterpret_cast<const uint4*>(a.pages.k + key_row(a, b, row0, g, j0 + lane, false));
@@ -325,10 +344,10 @@ __device__ __noinline__ void masked_row(const PackedPrefillParams& a, int b, int
 }
 
 // Barrier of the softmax warps, the n-th of a CTA; false when it gave up.
-__device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n, const PackedPrefillParams& a) {
+__device__ __forceinline__ bool softmax_sync(Bars& bs, unsigned& n) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bs.joint));
-  return wait_bar(bs.joint, n++ & 1, a);
+  return wait_bar(bs, bs.joint, n++ & 1);
 }
 
 // Parts of an item that several CTAs share: slot 2 c + 1 for the CTA with the
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) packed_prefill_join_kernel(const
   for (int r = tid >> 5; r < SLICE; r += JOIN_THREADS / 32) {
     const int row = r0 + r, t = row / ROWS, rr = row & (ROWS - 1), rp = rr / nrep, pos = it.q0 + t * qp + rp;
     if (bad[r] && it.start + pos < it.kv_end - 1)
-      masked_row(a, it.b, it.row0, it.g, it.start, pos, it.g * nrep + rr - rp * nrep, it.kv_end);
+      masked_row(a, it.b, it.row0, it.g, it.start, pos, it.g * nrep + rr - rp * nrep, it.kv_end, nullptr);
   }
 }
 
@@ -485,6 +504,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&bs.item_empty[s]), 10);  // issuers, softmax warps
     }
     bs.abort = 0;
+    bs.alive = 0;
+    bs.wait_ns = a.wait_ns;
     bs.rows = 0;
     bs.q_issued[0] = bs.q_issued[1] = 0;
     bs.k_issued = bs.v_issued = 0;
@@ -647,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int puts = 0;
     auto put = [&](const Item& x) {
       const int s = puts % SLOTS;
-      if (puts >= SLOTS && !wait_bar(bs.item_empty[s], (puts / SLOTS - 1) & 1, a)) return false;
+      if (puts >= SLOTS && !wait_bar(bs, bs.item_empty[s], (puts / SLOTS - 1) & 1)) return false;
       if (lane == 0) {
         bs.item[s] = x;
         mbar_arrive(smem_u32(&bs.item_full[s]));
@@ -670,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int cs[NQ] = {};  // score tiles of each Q tile so far (as its issuer counts them)
     bool ok = true, stop = false;
     auto go_on = [&](uint64_t& bar, int parity) {
-      ok = wait_bar(bar, parity, a);
+      ok = wait_bar(bs, bar, parity);
       return ok && !__any_sync(0xffffffffu, aborted(bs));
     };
     auto copy = [&](const CUtensorMap* map, uint64_t& full, uint32_t dst, int held, int g, int row, int page) {
@@ -773,7 +794,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned u0 = 0, cs = 0, qi = 0, step = 0;
     bool ok = true;
     auto wait = [&](uint64_t& bar, unsigned parity) {
-      return ok = wait_bar(bar, parity, a);
+      return ok = wait_bar(bs, bar, parity);
     };
     // the stage is free once this issuer's products on it are done (a commit
     // covers every product the thread issued before it)
@@ -784,7 +805,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     };
-    while (ok && walk.next(bs, it, a)) {
+    while (ok && walk.next(bs, it)) {
       if (it.n == 0) continue;
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int end_t = min(it.kv_end, it.start + it.q0 + (t + 1) * qp);  // keys of this Q tile
@@ -885,7 +906,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned cs = 0;  // score tiles of this Q tile over the items (as the issuer counts them)
     unsigned syncs = 0, items = 0;  // items with keys of this Q tile
     bool ok = true;
-    while (ok && walk.next(bs, it, a)) {
+    while (ok && walk.next(bs, it)) {
       const int n_t = t ? it.nt[1] : it.nt[0];
       const int pos = it.q0 + t * qp + rp;  // query index within the sequence
       const bool real = used && pos < it.T;
@@ -903,7 +924,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m_limit = -INFINITY, neg = 0.f;  // max that P is still taken against m_ref with; -m_ref in log2 units
       for (int j = 0; j < n_t; ++j) {
         // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
-        if (!wait_bar(bs.s_full[t], (cs + j) & 1, a)) {
+        if (!wait_bar(bs, bs.s_full[t], (cs + j) & 1)) {
           ok = false;
           break;
         }
@@ -996,7 +1017,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!ok) break;
       if (n_t > 0) {
-        if (!wait_bar(bs.o_done[t], items & 1, a)) {
+        if (!wait_bar(bs, bs.o_done[t], items & 1)) {
           ok = false;
           break;
         }
@@ -1014,12 +1035,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Of few parts, the CTA that arrives last at the item's ticket adds the
         // others (they have arrived, so they are running and about to write
         // theirs) to its own, in CTA order all the same. More are left to the
-        // second kernel.
+        // second kernel. Only the item's first CTA can have had an item before,
+        // with rows to compute again: it is then the last one here.
         const int c = blockIdx.x, others = it.last - it.first;
         int* arrived = a.tickets + 2 * it.first;
         if (others <= DIRECT) {
           if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
-          if (!softmax_sync(bs, syncs, a)) {
+          if (!softmax_sync(bs, syncs)) {
             ok = false;
             break;
           }
@@ -1060,7 +1082,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             arrived[0] = 0;
             arrived[1] = 0;
           }
-          if (!softmax_sync(bs, syncs, a) || (whole && !bs.parts_there)) {
+          if (!softmax_sync(bs, syncs) || (whole && !bs.parts_there)) {
             ok = false;
             break;
           }
@@ -1148,7 +1170,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (; again; again &= again - 1) {
           const int src = __ffs(again) - 1;
           masked_row(a, it.b, it.row0, it.g, it.start, __shfl_sync(0xffffffffu, pos, src),
-                     it.g * nrep + __shfl_sync(0xffffffffu, hh, src), it.kv_end);
+                     it.g * nrep + __shfl_sync(0xffffffffu, hh, src), it.kv_end, &bs.alive);
         }
       }
       cs += n_t;

@@ -438,7 +438,9 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
  *   q    [N, n_heads, 128], row n at element n * q_stride, heads dense
  *   out  [N, n_heads, 128] dense; rows of no sequence are left as they were
  * Scores, softmax and sums in fp32; the probabilities enter the value product
- * rounded to bf16. (columns * page_size + 384) * n_kv_heads must stay below
+ * rounded to bf16. A value that is not finite shows in the rows that see it
+ * only; up to 256 / n_rep - 1 tokens before it are then computed again, one
+ * head and token at a time, at about 0.4 us for each of their keys. (columns * page_size + 384) * n_kv_heads must stay below
  * 858,993,459 (107 million positions for 8 KV heads), else GQA_EINVAL. */
 int gqa_paged_prefill(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
                       const int32_t* start_pos, const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace,
