@@ -559,8 +559,9 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     of each sequence; -1 an unused slot. k_pages, v_pages [pages, page_size,
     n_kv, 128], page_size a power of two >= 16; block_table device int32 [B,
     columns]. Returns the rotated queries (q_out, which may be q), or None
-    without q. Otherwise no output of the paged operators may share memory with
-    their inputs or the pages."""
+    without q. Otherwise no output of the paged operators, and here none of the
+    pages, may share memory with their inputs (a tensor counts from its first
+    byte to its last); key and value pages may interleave but not meet."""
     if workspace is None or (q_out is None and q is not None):
         x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
         q_out = None if q is None else x

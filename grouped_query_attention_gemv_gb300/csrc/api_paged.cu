@@ -70,25 +70,67 @@ int check_workspace(const void* ws, size_t bytes) {
   return bytes < GQA_PAGED_WORKSPACE_BYTES ? GQA_EWORKSPACE : GQA_OK;
 }
 
-// Whether an output of n_out elements shares memory with n_in elements (counted
-// in 128 bits: strides times counts of a faulty call may pass 64).
-bool overlaps(const gqa_bf16* out, __int128 n_out, const gqa_bf16* in, __int128 n_in) {
-  const __int128 o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
-  return n_out > 0 && n_in > 0 && o < i + 2 * n_in && i < o + 2 * n_out;
+// A tensor's memory, from its first byte to its last (counted in 128 bits:
+// strides times counts of a faulty call may pass 64).
+struct Span {
+  __int128 first, end;
+  Span(const void* p, __int128 bytes) : first(reinterpret_cast<uintptr_t>(p)), end(first + (p ? bytes : 0)) {}
+  bool meets(const Span& o) const { return end > first && o.end > o.first && first < o.end && o.first < end; }
+};
+// n packed rows of `row` elements
+Span span_of(const gqa_bf16* p, int n, int64_t stride, int64_t row) {
+  return {p, n > 0 ? (static_cast<__int128>(n - 1) * stride + row) * 2 : 0};
 }
-// ... with n packed rows of `row` elements
-bool overlaps(const gqa_bf16* out, __int128 n_out, const gqa_bf16* in, int n, int64_t stride, int64_t row) {
-  return n > 0 && overlaps(out, n_out, in, static_cast<__int128>(n - 1) * stride + row);
+Span span_of(const int32_t* p, __int128 n) { return {p, n * 4}; }
+// rows of keys or values in pages
+Span span_of(const __nv_bfloat16* p, const PagedCache& c, int pages, int rows, int n_kv, long long row_stride) {
+  return {p, (static_cast<__int128>(pages - 1) * c.page_stride + static_cast<__int128>(n_kv - 1) * c.head_stride +
+              HEAD_DIM + static_cast<__int128>(rows - 1) * row_stride) * 2};
 }
-// ... with rows of keys or values in pages
-bool overlaps(const gqa_bf16* out, __int128 n_out, const PagedCache& c, int pages, int rows, int n_kv,
-              long long v_row_stride) {
-  const __int128 others = static_cast<__int128>(pages - 1) * c.page_stride +
-                          static_cast<__int128>(n_kv - 1) * c.head_stride + HEAD_DIM;
-  return overlaps(out, n_out, reinterpret_cast<const gqa_bf16*>(c.k),
-                  others + static_cast<__int128>(rows - 1) * c.row_stride) ||
-         overlaps(out, n_out, reinterpret_cast<const gqa_bf16*>(c.v),
-                  others + static_cast<__int128>(rows - 1) * v_row_stride);
+Span span_of_table(const PagedCache& c, int B) {
+  return span_of(c.table, static_cast<__int128>(B - 1) * c.table_stride + c.columns);
+}
+
+// Whether some row of 128 elements of the key pages and some of the value pages
+// share memory. The two may interleave (both halves of one [pages, 2, ...]
+// tensor, say), so spans do not tell: rows at x page_stride + y row_stride + z
+// head_stride are `d` apart for some |x| < pages, |y| < rows, |z| < heads. Taken
+// from the largest stride down, what is left must be within the smaller
+// strides' reach, so each count is one of two.
+bool pages_meet(const PagedCache& c, int pages, int rows, int n_kv) {
+  struct Axis {
+    long long stride, n;
+  } axes[3] = {{c.page_stride, pages}, {c.row_stride, rows}, {c.head_stride, n_kv}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (axes[j].stride < axes[j + 1].stride) {
+        const Axis x = axes[j];
+        axes[j] = axes[j + 1];
+        axes[j + 1] = x;
+      }
+  const long long between = (reinterpret_cast<intptr_t>(c.v) - reinterpret_cast<intptr_t>(c.k)) / 2;
+  for (int pick = 0; pick < 8; ++pick) {
+    long long d = between;
+    for (int i = 0; i < 3; ++i) {
+      const long long s = axes[i].stride, most = axes[i].n - 1;
+      long long x = d / s - (d % s < 0) + (pick >> i & 1);
+      x = x > most ? most : x < -most ? -most : x;
+      d -= x * s;
+    }
+    if (d < HEAD_DIM && d > -HEAD_DIM) return true;
+  }
+  return false;
+}
+
+// Whether the output of an attention call shares memory with what it reads.
+bool out_meets(const Span& out, const Span& q, const PagedCache& c, int pages, int rows, int n_kv, long long v_row_stride,
+               int B, const int32_t* start, const int32_t* cu, const void* workspace) {
+  const Span read[] = {q, span_of(c.k, c, pages, rows, n_kv, c.row_stride), span_of(c.v, c, pages, rows, n_kv, v_row_stride),
+                       span_of(start, B), span_of(cu, static_cast<__int128>(B) + 1),
+                       span_of_table(c, B), {workspace, GQA_PAGED_WORKSPACE_BYTES}};
+  for (const Span& r : read)
+    if (out.meets(r)) return true;
+  return false;
 }
 
 int check_scale(float scale) { return scale > 0.f && scale < 1e30f ? GQA_OK : GQA_EINVAL; }
@@ -130,10 +172,25 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
       !aligned4(start_pos) || (cu_tokens && !aligned4(cu_tokens)))
     return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
-  if (q && ((q != q_out && overlaps(q_out, N * q_row, q, N, q_stride, q_row)) ||
-            overlaps(q_out, N * q_row, k, N, k_stride, kv_row) || overlaps(q_out, N * q_row, v, N, v_stride, kv_row) ||
-            overlaps(q_out, N * q_row, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride)))
-    return GQA_EINVAL;
+  if (N > 0) {
+    // what the call writes: the queries, the key and the value pages
+    const Span written[3] = {
+        span_of(q_out, N, q_row, q_row),
+        span_of(p.pages.k, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride),
+        span_of(p.pages.v, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride)};
+    const Span read[] = {span_of(k, N, k_stride, kv_row), span_of(v, N, v_stride, kv_row), span_of(start_pos, B),
+                         span_of(cu_tokens, static_cast<__int128>(B) + 1), span_of_table(p.pages, B),
+                         {rope, static_cast<__int128>(rope_rows) * ROPE_PAIRS * 8},
+                         {workspace, GQA_PAGED_WORKSPACE_BYTES}};
+    for (const Span& w : written)
+      for (const Span& r : read)
+        if (w.meets(r)) return GQA_EINVAL;
+    const Span queries = span_of(q, N, q_stride, q_row);
+    if ((q != q_out && written[0].meets(queries)) || written[1].meets(queries) || written[2].meets(queries) ||
+        written[0].meets(written[1]) || written[0].meets(written[2]) ||
+        (written[1].meets(written[2]) && pages_meet(p.pages, pages->num_pages, pages->page_size, p.n_kv)))
+      return GQA_EINVAL;
+  }
   begin_call();
   if (N == 0) return GQA_OK;
   p.q = bf(q);
@@ -174,8 +231,8 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
   if (!aligned16(q) || !aligned16(out) || !aligned4(start_pos)) return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
   const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
-  if (overlaps(out, B * row, q, B, q_stride, row) ||
-      overlaps(out, B * row, p.pages, pages->num_pages, pages->page_size, pages->n_kv_heads, p.pages.row_stride))
+  if (out_meets(span_of(out, B, row, row), span_of(q, B, q_stride, row), p.pages, pages->num_pages, pages->page_size,
+                pages->n_kv_heads, p.pages.row_stride, B, start_pos, nullptr, workspace))
     return GQA_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = bf(q);
@@ -212,7 +269,8 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
   const PagedCache& c = p.pages;
   const long long v_row = p.v_row_stride ? p.v_row_stride : c.row_stride;
-  if (overlaps(out, N * row, q, N, q_stride, row) || overlaps(out, N * row, c, kv_pages, kv_rows, n_kv, v_row))
+  if (N > 0 && out_meets(span_of(out, N, row, row), span_of(q, N, q_stride, row), c, kv_pages, kv_rows, n_kv, v_row, B,
+                         p.start, cu_tokens, workspace))
     return GQA_EINVAL;
   begin_call();
   if (N == 0) return GQA_OK;

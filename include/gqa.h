@@ -367,8 +367,11 @@ int gqa_host_stage_release(void* stage);
  * rows are zero. Other values with a token at or past columns * page_size (or
  * rope_rows), and values below -1, are reported as GQA_DEV_BAD_POSITION.
  *
- * Outputs share no memory with inputs or pages, but for q_out = q below (else
- * GQA_EINVAL).
+ * Outputs share no memory with inputs, pages or the workspace, but for q_out = q
+ * below (else GQA_EINVAL); the pages that an append writes are outputs too. A
+ * tensor counts from its first byte to its last. Key and value pages may
+ * interleave (two halves of one [pages, 2, ...] tensor); an append refuses them
+ * where a key row and a value row meet, the other entries only read them.
  *
  * Every entry enqueues on `stream` of the current device, allocates nothing
  * and can be captured into a graph; no length is read by the host, so a

@@ -148,6 +148,61 @@ def test_outputs_that_overlap_inputs_are_refused(lib, call, kw):
     assert call(lib, **a) == -1
 
 
+def test_an_append_refuses_inputs_in_the_pages(lib):
+    # the pages (8 heads, 4 pages of 16 rows: 131,072 bytes each) are outputs too
+    def call(k=4 * A, v=5 * A, **kw):
+        p = Pages(A, 2 * A, 16 * 1024, 1024, 128, 3 * A, 4, 16, 8, 4, 4)
+        a = dict(q=6 * A, k=k, v=v, cu=7 * A, start=8 * A, rope=9 * A, out=10 * A, ws=11 * A)
+        a.update(kw)
+        return append(lib, (ctypes.addressof(p), p), **a)
+    end = 131072
+    assert call(k=A) == -1 and call(k=A + end - 16) == -1 and call(k=2 * A + 4096) == -1
+    assert call(v=A) == -1 and call(v=2 * A) == -1 and call(v=2 * A - 1024) == -1
+    assert call(q=A + 256, ks=1024) == -1 and call(q=2 * A + 256) == -1
+    # without queries as well
+    for kw in (dict(k=A), dict(v=2 * A + end - 16), dict(start=A), dict(cu=2 * A), dict(rope=A + 16), dict(ws=A)):
+        assert call(q=None, out=None, **kw) == -1
+    # the queries on other inputs
+    assert call(out=8 * A) == -1 and call(out=7 * A) == -1 and call(out=9 * A) == -1 and call(out=11 * A + 4096) == -1
+
+
+@pytest.mark.parametrize("between,strides,meet", [
+    (0, (16384, 1024, 128), True), (8, (16384, 1024, 128), True), (-120, (16384, 1024, 128), True),
+    (16384 * 3 + 1024 * 15, (16384, 1024, 128), True), (-16384 * 3, (16384, 1024, 128), True),
+    (16384 * 2 - 1024 * 5 + 128 * 7 + 64, (16384, 1024, 128), True), (16384 * 4, (16384, 1024, 128), False),
+    # interleaved by page, by row, by head
+    (16384, (32768, 1024, 128), False), (-16384, (32768, 1024, 128), False), (16376, (32768, 1024, 128), True),
+    (1024, (32768, 2048, 128), False), (1016, (32768, 2048, 128), True), (-1032, (32768, 2048, 128), True),
+    (128, (32768, 2048, 256), False), (120, (32768, 2048, 256), True),
+    # head-major pages: one head further on, and side by side
+    (2048, (16384, 128, 2048), True), (-128 * 15, (16384, 128, 2048), True), (16384, (32768, 128, 2048), False),
+    (128, (32768, 256, 4096), False), (136, (32768, 256, 4096), True)])
+def test_an_append_refuses_key_and_value_rows_that_meet(lib, between, strides, meet):
+    p = Pages(A, A + 2 * between, *strides, 3 * A, 4, 16, 8, 4, 4)
+    k, v = ({x * strides[0] + y * strides[1] + z * strides[2] + o for x in range(4) for y in range(16) for z in range(8)}
+            for o in (0, between))
+    assert meet == any(r + d in v for r in k for d in range(-120, 128, 8))
+    if meet or not torch.cuda.is_available():   # accepted, the call reaches the launch, which needs a device
+        got = append(lib, (ctypes.addressof(p), p), q=None, out=None, k=4 * A, v=5 * A, cu=7 * A, start=8 * A,
+                     rope=9 * A, ws=11 * A)
+        assert got == (-1 if meet else -4)
+
+
+@pytest.mark.parametrize("call", [decode, prefill])
+def test_attention_outputs_on_index_inputs_are_refused(lib, call):
+    p = Pages(A, 2 * A, 16 * 1024, 1024, 128, 3 * A, 4, 16, 8, 4, 4)
+    a = dict(q=6 * A, start=8 * A, ws=11 * A)
+    if call is prefill:
+        a["cu"] = 7 * A
+        assert call(lib, (ctypes.addressof(p), p), out=7 * A, **a) == -1
+    assert call(lib, (ctypes.addressof(p), p), out=8 * A, **a) == -1
+    assert call(lib, (ctypes.addressof(p), p), out=3 * A + 16, **a) == -1
+    assert call(lib, (ctypes.addressof(p), p), out=11 * A + 65536, **a) == -1
+    if call is prefill:
+        assert packed(lib, q=6 * A, k=4 * A, v=5 * A, cu=7 * A, ws=11 * A, out=7 * A) == -1
+        assert packed(lib, q=6 * A, k=4 * A, v=5 * A, cu=7 * A, ws=11 * A, out=11 * A) == -1
+
+
 def test_no_tokens_is_no_launch(lib):
     assert append(lib, N=0) == 0 and lib.gqa_last_launch_count() == 0
     assert prefill(lib, N=0) == 0 and packed(lib, N=0) == 0 and lib.gqa_last_launch_count() == 0

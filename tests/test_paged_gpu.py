@@ -90,6 +90,39 @@ def test_append_forms(gen, ws, kw):
     run_append(gen, ws, 8, 2, 32, [5, 40, 0, 3], [31, -1, 3, 64], **kw)
 
 
+@pytest.mark.parametrize("shape,at", [((9, 2, 16, 2, P.D), 1), ((9, 16, 2, 2, P.D), 2), ((9, 16, 2, 2, P.D), 3),
+                                      ((2, 9, 16, 2, P.D), 0)])
+def test_append_into_interleaved_pages(gen, ws, shape, at):
+    # keys and values in one tensor, beside each other by page, row or head, or one behind the other
+    both = torch.full(shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    k_pages, v_pages = both.unbind(at)
+    table = torch.randperm(9, generator=gen, device="cuda")[:8].view(2, 4).int()
+    k, v = P.normal(gen, 70, 2, P.D), P.normal(gen, 70, 2, P.D)
+    rope = G.rope_table(64)
+    G.paged_append(None, k, v, ints([3, 0]), rope, k_pages, v_pages, table, cu_tokens=offsets([20, 50]), workspace=ws)
+    assert G.device_status(ws) == 0
+    for b, (rows, s) in enumerate(((slice(0, 20), 3), (slice(20, 70), 0))):
+        t = rows.stop - rows.start
+        p, r = P.slots(table, 16, b, s, t)
+        P.check_rotated(k_pages[p, r], k[rows], rope[s:s + t], f"k of sequence {b}")
+        assert torch.equal(v_pages[p, r], v[rows])
+        k_pages[p, r], v_pages[p, r] = 3.0, 3.0
+    assert (both == 3.0).all()
+
+
+def test_append_refuses_rows_that_lie_in_the_pages(gen, ws):
+    k_pages, v_pages = (P.normal(gen, 6, 16, 2, P.D) for _ in range(2))
+    before = k_pages.clone(), v_pages.clone()
+    table, rope = ints([[0, 1], [2, 3]]), G.rope_table(32)
+    k, v = P.normal(gen, 2, 2, P.D), P.normal(gen, 2, 2, P.D)
+    for args in ((k_pages[5, :2], v), (k, k_pages[5, :2]), (v_pages[4, 3:5], v), (k, v_pages[4, 3:5])):
+        with pytest.raises(G.GQAError):
+            G.paged_append(None, *args, ints([3, 9]), rope, k_pages, v_pages, table, workspace=ws)
+    with pytest.raises(G.GQAError):
+        G.paged_append(None, k, v, ints([3, 9]), rope, k_pages, k_pages, table, workspace=ws)
+    assert torch.equal(k_pages, before[0]) and torch.equal(v_pages, before[1])
+
+
 @pytest.mark.parametrize("B", [1, 2, 33, 300])
 def test_append_one_token_each(gen, ws, B):
     run_append(gen, ws, 4, 2, 16, [1] * B, [(37 * b) % 50 - 1 for b in range(B)], cu=False)
