@@ -13,7 +13,7 @@ entries ``block_forward_host`` / ``decode_host`` (with ``make_host_stage``,
 ``rope_table``, ``workspace_bytes``, ``device_status``, ``last_launch_count``;
 and the serving operators over a paged cache ``paged_append`` /
 ``paged_decode`` / ``paged_prefill`` / ``packed_prefill`` (with
-``make_paged_workspace``), whose argument checks are compiled
+``make_paged_workspace``, ``default_paged_workspace``), whose argument checks are compiled
 (``csrc/binding.cpp``).
 If the library has not been built every call raises ``ImportError``; there is
 no fallback path.
@@ -36,8 +36,8 @@ __all__ = [
     "set_decode_fusion", "set_decode_attention_split", "set_wait_limit_ns", "decode_static", "rms_norm", "layer_forward", "layer_decode", "static_device_status",
     "STATIC_SCRATCH_BYTES", "make_host_stage", "default_host_stage", "host_stage_wait", "release_host_stage",
     "decode_host",
-    "block_forward_host", "PAGED_WORKSPACE_BYTES", "make_paged_workspace", "paged_append", "paged_decode",
-    "paged_prefill", "packed_prefill",
+    "block_forward_host", "PAGED_WORKSPACE_BYTES", "make_paged_workspace", "default_paged_workspace",
+    "paged_append", "paged_decode", "paged_prefill", "packed_prefill",
 ]
 
 D_MODEL, N_HEADS, N_KV_HEADS, HEAD_DIM = 4096, 32, 8, 128
@@ -515,6 +515,33 @@ def make_paged_workspace(device=None) -> torch.Tensor:
     return torch.zeros(PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device or "cuda")
 
 
+_default_workspaces = {}
+_MAX_DEFAULT_WORKSPACES = 8
+
+
+def default_paged_workspace(device=None, stream=None) -> torch.Tensor:
+    """The workspace that the paged operators use on ``stream`` (None: the
+    current one) when they are given none. It is kept, so that the errors of
+    such calls can be read: ``device_status(default_paged_workspace())``. Of the
+    streams that were used first, those past eight lose theirs. A call that is
+    captured into a graph takes a workspace of its own instead, whose status
+    cannot be read: give it one."""
+    d = torch.device(device or "cuda")
+    index = d.index if d.index is not None else torch.cuda.current_device()
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        if torch.cuda.is_current_stream_capturing():
+            # the graph may be replayed beside other calls of this stream
+            return make_paged_workspace(torch.device("cuda", index))
+        key = (index, _s(stream, torch.device("cuda", index)))
+        ws = _default_workspaces.get(key)
+        if ws is None:
+            if len(_default_workspaces) >= _MAX_DEFAULT_WORKSPACES:
+                # its memory is its stream's, which uses it no sooner than its last call is done
+                _default_workspaces.pop(next(iter(_default_workspaces)))
+            ws = _default_workspaces[key] = make_paged_workspace(torch.device("cuda", index))
+    return ws
+
+
 _paged = None
 
 
@@ -534,7 +561,8 @@ def _binding():
 
 def _defaults(like, name, out, workspace, stream):
     """The output, shaped like packed rows `like`, and the workspace of a call
-    that was given none: memory of the stream that uses it."""
+    that was given none: memory of the stream that uses it, the workspace that
+    of ``default_paged_workspace``."""
     if not isinstance(like, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not like.is_cuda:
@@ -543,7 +571,7 @@ def _defaults(like, name, out, workspace, stream):
         if out is None:
             out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
         if workspace is None:
-            workspace = make_paged_workspace(like.device)
+            workspace = default_paged_workspace(like.device, stream)
     return out, workspace
 
 
@@ -561,7 +589,9 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     columns]. Returns the rotated queries (q_out, which may be q), or None
     without q. Otherwise no output of the paged operators, and here none of the
     pages, may share memory with their inputs (a tensor counts from its first
-    byte to its last); key and value pages may interleave but not meet."""
+    byte to its last); key and value pages may interleave but not meet.
+    Bad positions and table entries are found on the device: ``device_status``
+    of the workspace, or of ``default_paged_workspace()`` where none was given."""
     if workspace is None or (q_out is None and q is not None):
         x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
         q_out = None if q is None else x

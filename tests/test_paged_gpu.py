@@ -792,6 +792,67 @@ def test_defaults_on_a_side_stream(gen):
     check_decode(out, q, rows)
 
 
+def test_errors_of_calls_without_a_workspace_can_be_read(gen):
+    k_pages, v_pages, table, rows = fill_cache(gen, [40, 40], 16, 2)
+    q, start = P.normal(gen, 2, 8, P.D), ints([39, 39])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        mine, other = (G.default_paged_workspace(stream=s) for s in (stream, side if stream is None else None))
+        assert mine is G.default_paged_workspace("cuda", stream) and mine is not other
+        bad = table.clone()
+        bad[0, 1] = 1 << 20
+        torch.cuda.synchronize()
+        out = G.paged_decode(q, start, k_pages, v_pages, bad, stream=stream)
+        assert G.device_status(mine) == 3 and G.device_status(other) == 0
+        check_decode(out[1:], q[1:], rows[1:])
+        assert G.device_status(mine, clear=True) == 3
+        G.paged_prefill(q, offsets([1, 1]), ints([39, 100]), k_pages, v_pages, table, stream=stream)
+        assert G.device_status(mine, clear=True) == 1
+        G.paged_append(None, q[:, :2], q[:, 2:4].contiguous(), ints([-5, -1]), G.rope_table(48), k_pages.clone(),
+                       v_pages.clone(), table, stream=stream)
+        assert G.device_status(mine, clear=True) == 1
+        check_decode(G.paged_decode(q, start, k_pages, v_pages, table, stream=stream), q, rows)
+        assert G.device_status(mine) == 0
+        # none is made call by call
+        at = torch.cuda.memory_allocated()
+        for _ in range(3):
+            G.packed_prefill(q, q[:, :2], q[:, 2:4], offsets([2]), stream=stream)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == at
+
+
+def test_more_streams_than_kept_workspaces(gen):
+    k_pages, v_pages, table, rows = fill_cache(gen, [3000], 64, 2)
+    q, start = P.normal(gen, 1, 8, P.D), ints([2999])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(11)]
+    outs = [G.paged_decode(q, start, k_pages, v_pages, table, stream=s) for _ in range(3) for s in streams]
+    torch.cuda.synchronize()
+    for o in outs:
+        check_decode(o, q, rows)
+
+
+def test_a_captured_call_without_a_workspace_has_its_own(gen):
+    k_pages, v_pages, table, rows = fill_cache(gen, [3000, 40], 64, 2)
+    q, start = P.normal(gen, 2, 8, P.D), ints([2999, 39])
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        G.paged_decode(q, start, k_pages, v_pages, table, out=out)   # this stream's workspace is there
+        kept = G.default_paged_workspace()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        G.paged_decode(q, start, k_pages, v_pages, table, out=out)
+    assert G.default_paged_workspace(stream=side) is kept
+    table[0, 0] = -1
+    for _ in range(3):
+        g.replay()
+    assert G.device_status(kept) == 0    # the graph's errors are not this workspace's
+    check_decode(out[1:], q[1:], rows[1:])
+
+
 def test_launch_counts_and_empty_calls(gen, ws):
     k_pages, v_pages, table, rows = fill_cache(gen, [40], 16, 2)
     q = P.normal(gen, 1, 8, P.D)
