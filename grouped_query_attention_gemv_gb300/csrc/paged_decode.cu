@@ -355,13 +355,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         // P^T as B fragments, (head gr, keys 2t, 2t + 1) and 8 keys further
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          // hi: the upper 16 bits; lo: the rest, kept above 0 where P is, so
-          // that an infinite value row gives an infinite sum and not a NaN
+          // hi: the upper 16 bits; lo: the rest, kept above 0 where P is (P is
+          // 0 or 2^-126 and more; 2^-133 is the least bf16 above 0), so that an
+          // infinite value row gives an infinite sum and not a NaN
           const float x0 = pr[2 * e], x1 = pr[2 * e + 1];
           const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
           hi[nt][e] = movmatrix_t(__byte_perm(u0, u1, 0x7632));
           const float y0 = x0 - __uint_as_float(u0 & 0xffff0000u), y1 = x1 - __uint_as_float(u1 & 0xffff0000u);
-          lo[nt][e] = movmatrix_t(pack_bf16(fmaxf(y0, x0 * 0x1p-24f), fmaxf(y1, x1 * 0x1p-24f)));
+          lo[nt][e] = movmatrix_t(pack_bf16(fmaxf(y0, fminf(x0, 0x1p-133f)), fmaxf(y1, fminf(x1, 0x1p-133f))));
         }
       }
       const int vr = (lane & 7) + (half << 3);  // key row of this lane's ldmatrix address

@@ -233,6 +233,30 @@ def test_decode_visible_infinity_and_nan_stay_where_they_are(gen, ws):
         P.check(out[b:b + 1][keep], ref[keep], tol[keep], f"sequence {b}")
 
 
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_decode_infinity_of_little_weight(gen, ws, value):
+    # an infinite value is one however little its key weighs, down to 2^-126 of the largest
+    scale = math.log(2.0) * (1 - 2.0 ** -20)   # scores count powers of two, and stay above 2^-126 where rounded
+    lens = [17] * 127
+    k_pages, v_pages, table, rows = fill_cache(gen, lens, 32, 1, junk=0.0)
+    k_pages.zero_()
+    q = torch.zeros(127, 1, P.D, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 1.0
+    for b in range(127):
+        p, r = P.slots(table, 32, b, 5, 1)
+        k_pages[p, r, 0, 0] = -float(b)
+        v_pages[p, r, 0, 7] = value
+    out = G.paged_decode(q, ints([16] * 127), k_pages, v_pages, table, scale=scale, workspace=ws)
+    assert G.device_status(ws) == 0
+    assert (out[:, 0, 7] == value).all(), out[:, 0, 7].tolist()
+    keep = [d for d in range(P.D) if d != 7]
+    for b in range(127):
+        k, v = (P.read_rows(x, table, 32, b, 17) for x in (k_pages, v_pages))
+        ref, mean, size = P.attend64(q[b:b + 1], k, torch.nan_to_num(v, 0.0, 0.0, 0.0), 16, scale)
+        tol = P.bound(ref, mean, size, 17, P.P_TWO_TERMS)
+        P.check(out[b:b + 1, :, keep], ref[..., keep], tol[..., keep], f"weight 2^-{b}")
+
+
 def test_decode_far_pages(gen, ws):
     # element offsets past 2^32
     n_kv, page = 8, 64
