@@ -109,9 +109,6 @@ constexpr int SLOTS = 2;                  // items handed from the producer to t
 // short ranges, 29 by halves).
 constexpr float DIRECT_TILES = 2.f, DIRECT_ROW = 8.f / (NQ * ROWS);
 constexpr float JOIN_TILES = 4.f, JOIN_ROW = 5.f / (NQ * ROWS), JOIN_PART_ROW = 1.4e-4f;
-constexpr int ITEM_UNITS = 2;             // what an item takes beside its key tiles, in those (2.8 us)
-constexpr int MAX_PARTS = 64;             // of an item
-constexpr int MIN_TILES = 3;              // key tiles of a part at least
 constexpr uint32_t TMEM_COLS = 512;
 // TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
 constexpr uint32_t S_COLS = 128, O_COL = 256, O_COLS = 128;
@@ -189,41 +186,21 @@ __device__ __forceinline__ Item entry_at(int e, const int* pre, int qp, const Pa
   return it;
 }
 
-// `total` units over `parts` ranges, the first `more` of them one longer.
-struct Split {
-  int each, more;
-  __device__ __forceinline__ Split(int total, int parts) : each(total / parts), more(total - each * parts) {}
-  __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int holder(int u) const {  // the range that holds unit u (each > 0)
-    const int x = more * (each + 1);
-    return u < x ? u / (each + 1) : more + (u - x) / each;
-  }
-};
-
-// Equal ranges: an item is its key tiles and, before them, ITEM_UNITS units for
-// what else it takes; in (entry, KV head, key tile) order there are cum[e] x
-// n_kv units before entry e. The item with unit u, from u on as far as the range
-// that ends at `end` goes (n = 0: it has no tile there); u becomes the first
-// unit behind that.
+// Equal ranges: the item with unit u, from u on as far as the range that ends
+// at `end` goes (n = 0: it has no tile there); u becomes the first unit behind
+// that.
 __device__ __forceinline__ Item ranged_item(int& u, int end, const Split& split, int E, const int* cum, const int* pre,
                                             int qp, const PackedPrefillParams& a) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cum[mid] * a.n_kv <= u) lo = mid; else hi = mid;
-  }
-  const int w = cum[lo + 1] - cum[lo], x = u - cum[lo] * a.n_kv;
-  Item it = entry_at(lo, pre, qp, a);
-  it.g = x / w;
-  const int base = cum[lo] * a.n_kv + it.g * w + ITEM_UNITS;  // the unit of the item's first tile
-  const int j1 = min(w - ITEM_UNITS, end - base);
-  it.j0 = max(0, u - base);
-  it.first = split.holder(base);
-  it.last = split.holder(base + w - ITEM_UNITS - 1);
-  it.n = max(0, j1 - it.j0);
-  u = min(end, base + w - ITEM_UNITS);
+  const Piece p = piece_at(u, end, split, E, cum, a.n_kv);
+  Item it = entry_at(p.entry, pre, qp, a);
+  it.g = p.g;
+  it.j0 = p.j0;
+  it.first = p.first;
+  it.last = p.last;
+  it.n = max(0, p.j1 - p.j0);
+  u = p.behind;
 #pragma unroll
-  for (int t = 0; t < NQ; ++t) it.nt[t] = max(0, min(it.nt[t], j1) - it.j0);
+  for (int t = 0; t < NQ; ++t) it.nt[t] = max(0, min(it.nt[t], p.j1) - p.j0);
   return it;
 }
 
@@ -602,15 +579,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     const int o = bs.order[0], longest = bs.cum[o + 1] - bs.cum[o];
-    const int mean = max((units + G - 1) / G, MIN_TILES);
-    // ranges of half an item: each in three at most
-    const int few = max(mean, (longest + 1) / 2);
+    const int mean = mean_range(units, G);
+    const int few = few_parts_range(mean, longest);
     const float few_cost = few + DIRECT_TILES + DIRECT_ROW * bs.rows;
-    // whole tiles: no item then lies in more than MAX_PARTS ranges
-    const int many = max(mean, (longest + MAX_PARTS - 3) / (MAX_PARTS - 2));
+    const int many = many_parts_range(mean, longest);
     const float many_cost = a.joins ? many + JOIN_TILES + (JOIN_ROW + JOIN_PART_ROW * (units / many)) * bs.rows : INFINITY;
     equal = __syncthreads_or(static_cast<float>(load) > fminf(few_cost, many_cost));
-    if (equal) parts = min(G, max(1, units / (few_cost <= many_cost ? few : many)));
+    if (equal) parts = range_count(units, few_cost <= many_cost ? few : many, G);
   }
   const bool claim = !equal && nitems > G;  // items are claimed as CTAs get to them
   tc_fence_before();

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "kernels.h"
+#include "work_split.h"
 
 namespace gqa {
 
@@ -58,16 +59,9 @@ __device__ __forceinline__ void cp_async_wait() {
 // cu[j] <= m, so empty sequences are passed over. B: m is past the last one.
 __device__ __forceinline__ int sequence_of(const int* cu, int B, int m) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, size = B;  // cu[lo + 1 .. lo + size] is undecided
-  while (size > 0) {
-    const int step = (size + 31) / 32;
-    const int j = (lane + 1) * step;  // last of this lane's stretch of `step`
-    const bool le = j <= size && cu[lo + j] <= m;
-    const int n = __popc(__ballot_sync(0xffffffffu, le));
-    lo += n * step;
-    size = min(step - 1, size - n * step);
-  }
-  return lo;
+  return search_sequence(B, [&](int lo, int size, int step) {
+    return __popc(__ballot_sync(0xffffffffu, search_at_or_before(cu, lo, size, step, lane, m)));
+  });
 }
 
 // RoPE of packed queries and keys, keys and values into the pages.

@@ -104,17 +104,6 @@ __device__ __forceinline__ void advance(Cursor& c, const int* pre, int B, int n_
   } while (c.n == 0);
 }
 
-// `total` chunks over `parts` ranges, the first `more` of them one longer.
-struct Split {
-  int each, more;
-  __device__ __forceinline__ Split(int total, int parts) : each(total / parts), more(total - each * parts) {}
-  __device__ __forceinline__ int start(int c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int holder(int u) const {  // the range that holds chunk u (each > 0)
-    const int x = more * (each + 1);
-    return u < x ? u / (each + 1) : more + (u - x) / each;
-  }
-};
-
 // A part of a (sequence, KV head), left for joining: its chunks
 // [first, end) identify it, `row` is its first row of the output.
 struct Part {
@@ -217,8 +206,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
 
   total *= p.n_kv;
   if (total == 0) return;
-  // no more CTAs than leave each warp a chunk
-  const int ctas = min(static_cast<int>(gridDim.x), (total + W - 1) / W);
+  const int ctas = decode_ctas(total, gridDim.x, W);
   const Split split(total, ctas);
   // One CTA per (sequence, KV head) instead of equal ranges where that costs
   // less than joining parts across CTAs.
@@ -237,7 +225,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     c0 = split.start(blockIdx.x);
     c1 = split.start(blockIdx.x + 1);
   }
-  const int a0 = c0 + (c1 - c0) * warp / W, a1 = c0 + (c1 - c0) * (warp + 1) / W;
+  const int a0 = warp_start(c0, c1, warp, W), a1 = warp_start(c0, c1, warp + 1, W);
   const int n = a1 - a0;
 
   const int gr = lane >> 2, t = lane & 3;
