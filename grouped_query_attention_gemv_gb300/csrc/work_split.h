@@ -12,6 +12,8 @@ namespace gqa {
 
 GQA_HD int least(int a, int b) { return a < b ? a : b; }
 GQA_HD int most(int a, int b) { return a > b ? a : b; }
+// a / b rounded up, a > 0 up to the largest int
+GQA_HD int ceil_div(int a, int b) { return (a - 1) / b + 1; }
 
 // `total` units over `parts` ranges, the first `more` of them one longer.
 struct Split {
@@ -49,7 +51,7 @@ GQA_HD int search_sequence(int B, Count count) {
 // ---- decode attention: chunks in (sequence, KV head, position) order
 
 // CTAs with a range of `total` > 0 chunks: no more than leave each warp a chunk.
-GQA_HD int decode_ctas(int total, int grid, int warps) { return least(grid, (total + warps - 1) / warps); }
+GQA_HD int decode_ctas(int total, int grid, int warps) { return least(grid, ceil_div(total, warps)); }
 // The first chunk of a warp's share of [c0, c1); warp = warps: c1.
 GQA_HD int warp_start(int c0, int c1, int warp, int warps) { return c0 + (c1 - c0) * warp / warps; }
 
@@ -61,7 +63,7 @@ constexpr int MIN_TILES = 3;   // key tiles of a part at least
 
 // Units of a range: of half the longest item at least, each item in three at
 // most; as short as MAX_PARTS allows. No shorter than the mean of `grid` ranges.
-GQA_HD int mean_range(int units, int grid) { return most((units + grid - 1) / grid, MIN_TILES); }
+GQA_HD int mean_range(int units, int grid) { return most(ceil_div(units, grid), MIN_TILES); }
 GQA_HD int few_parts_range(int mean, int longest) { return most(mean, (longest + 1) / 2); }
 GQA_HD int many_parts_range(int mean, int longest) { return most(mean, (longest + MAX_PARTS - 3) / (MAX_PARTS - 2)); }
 GQA_HD int range_count(int units, int range, int grid) { return least(grid, most(1, units / range)); }

@@ -159,3 +159,16 @@ def test_sequence_search(split, B):
     for m, b in enumerate(owner):
         assert split.sequence(ptr(cu), B, 3 + m) == b
     assert split.sequence(ptr(cu), B, int(cu[-1])) == B
+
+
+@pytest.mark.parametrize("total", [(1 << 31) - 1 - n for n in (0, 1, 6, 7, 8, 150, 151, 152, 400)])
+def test_counts_up_to_their_limit(split, total):
+    # a batch may have 2^31 - 1 chunks (units); rounding up must not pass that
+    assert split.ctas(total, GRID, WARPS) == GRID
+    assert split.range_units(total, GRID, 5, 1) == -(-total // GRID)
+    assert split.parts_of(total, -(-total // GRID), GRID) in (GRID, GRID - 1)
+
+
+@pytest.mark.parametrize("total", [1, 7, 8, 9, 1215, 1216, 1217])
+def test_ctas_leave_each_warp_a_chunk(split, total):
+    assert split.ctas(total, GRID, WARPS) == min(GRID, -(-total // WARPS))
