@@ -592,6 +592,8 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     byte to its last); key and value pages may interleave but not meet.
     Bad positions and table entries are found on the device: ``device_status``
     of the workspace, or of ``default_paged_workspace()`` where none was given."""
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
     if workspace is None or (q_out is None and q is not None):
         x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
         q_out = None if q is None else x

@@ -221,6 +221,14 @@ def test_binding_refuses_host_tensors():
         G.packed_prefill(None, bf, bf, i)
 
 
+@pytest.mark.parametrize("workspace", [None, torch.zeros(8, dtype=torch.uint8)])
+def test_binding_refuses_an_output_without_queries(workspace):
+    a = good()
+    a.update(q=None, workspace=workspace)
+    with pytest.raises(ValueError, match="q_out needs q"):
+        G.paged_append(**a)
+
+
 def good():
     """Arguments of paged_append that only their device is wrong with."""
     x = torch.zeros(6, 12, 128, dtype=torch.bfloat16)
