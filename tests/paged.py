@@ -120,3 +120,43 @@ def check_rotated(got, x, cs, what):
     """fp32: two products and a sum, each half a step of 2^-23 off, then one rounding to bf16."""
     y, m = rotate64(x, cs)
     check(got, y, BF16_HALF_STEP * y.abs() + 2.0 ** -22 * m, what)
+
+
+# Relative L2 error of a whole output, for values that are independent of the
+# weights: a rounding to bf16 is even within half a step, which is 0.0015 to
+# 0.0017 of what is rounded in the mean square (2^-8 / sqrt(3 x 2.16) for evenly
+# spread exponents). The output's own and the probabilities' add up to 0.0023;
+# losing m of n keys costs sqrt(m / n) (0.046 for 148 of 70,001), which the
+# bound above, whose share grows with n, does not see.
+L2_BAR = 2.0 ** -8
+
+
+def check_l2(got, ref, what):
+    err = float((got.double() - ref).norm() / ref.norm())
+    assert err <= L2_BAR, f"{what}: off by {err:.5f} of its norm"
+
+
+CODE_KEYS, CODE_WINDOW = 16, 16 * D
+
+
+def coded_values(n, window, device):
+    """[n, D] of zeros and ones: key j of the window of 2,048 positions shows in
+    dim (j % 2048) // 16 alone. With equal weights dim d of the mean is the
+    number of its keys that were summed over the number of all: one key lost or
+    taken twice is a sixteenth."""
+    j = torch.arange(n, device=device)
+    at = (j % CODE_WINDOW) // CODE_KEYS
+    v = torch.zeros(n, D, dtype=torch.bfloat16, device=device)
+    v[j, at] = (j // CODE_WINDOW == window).to(v.dtype)
+    return v
+
+
+def check_counts(got, window, first, what):
+    """got [t, H, D]: equal weights over keys 0 .. first + i of coded values."""
+    t = got.shape[0]
+    seen = first + 1 + torch.arange(t, device=got.device).double()[:, None]
+    begin = window * CODE_WINDOW + CODE_KEYS * torch.arange(D, device=got.device).double()
+    want = ((seen - begin).clamp(0, CODE_KEYS) / seen)[:, None].expand(got.shape)
+    # whole numbers up to 2^24 are exact in fp32; one division, one product, one rounding
+    over = (got.double() - want).abs() - (BF16_HALF_STEP + 2.0 ** -20) * want
+    assert (over <= 0).all(), f"{what}, window {window}: {int((over > 0).sum())} counts are wrong"

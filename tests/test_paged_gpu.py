@@ -485,6 +485,82 @@ def test_paged_prefill_joins_only_its_own_items(gen, ws):
     assert (out[3:] == 9.0).all()
 
 
+# ------------------------------------------------------------------ nothing lost, nothing twice
+
+@pytest.mark.parametrize("heads,n_kv,page,lens", [(8, 2, 64, [70001, 3, 20000]), (32, 8, 16, [1001] * 16),
+                                                  (16, 1, 128, [131072]), (32, 8, 64, [8192, 1, 4000, 17, 300]),
+                                                  (32, 32, 32, [1001] * 3)])
+def test_decode_is_close_in_the_mean(gen, ws, heads, n_kv, page, lens):
+    k_pages, v_pages, table, rows = fill_cache(gen, lens, page, n_kv)
+    q = P.normal(gen, len(lens), heads, P.D, scale=1.5)
+    out = G.paged_decode(q, ints([n - 1 for n in lens]), k_pages, v_pages, table, workspace=ws)
+    for b, (k, v) in enumerate(rows):
+        P.check_l2(out[b:b + 1], P.attend64(q[b:b + 1], k, v, lens[b] - 1)[0], f"sequence {b} of {lens[b]} rows")
+
+
+SHARED = [(16, 1, 128, [8], [60000]), (32, 8, 64, [1024], [7168]), (8, 2, 64, [40, 5], [8000, 2100]),
+          (32, 8, 64, [600, 40], [5000, 3000]), (28, 4, 64, [100], [5000]), (4, 1, 64, [2500], [0]),
+          (8, 2, 64, [700, 1, 300], [20, 12000, 0])]
+
+
+@pytest.mark.parametrize("heads,n_kv,page,lens,starts", SHARED)
+def test_paged_prefill_is_close_in_the_mean(gen, ws, heads, n_kv, page, lens, starts):
+    k_pages, v_pages, table, rows = fill_cache(gen, [s + t for s, t in zip(starts, lens)], page, n_kv)
+    q = P.normal(gen, sum(lens), heads, P.D, scale=1.5)
+    out = G.paged_prefill(q, offsets(lens), ints(starts), k_pages, v_pages, table, workspace=ws)
+    at = 0
+    for b, (t, s) in enumerate(zip(lens, starts)):
+        ref = P.attend64(q[at:at + t], *rows[b], s)[0]
+        P.check_l2(out[at:at + t], ref, f"sequence {b}: {t} tokens after {s}")
+        at += t
+
+
+def test_packed_prefill_is_close_in_the_mean(gen, ws):
+    lens = [2048, 5, 700]
+    q, k, v = (P.normal(gen, sum(lens), h, P.D, scale=1.5) for h in (32, 8, 8))
+    out = G.packed_prefill(q, k, v, offsets(lens), workspace=ws)
+    at = 0
+    for t in lens:
+        r = slice(at, at + t)
+        at += t
+        P.check_l2(out[r], P.attend64(q[r], k[r], v[r], 0)[0], f"{t} tokens")
+
+
+def coded(k_pages, v_pages, table, page, ends, window):
+    for b, n in enumerate(ends):
+        if n:
+            P.write_rows(v_pages, table, page, b, 0,
+                         P.coded_values(n, window, "cuda")[:, None].expand(-1, v_pages.shape[2], -1))
+
+
+@pytest.mark.parametrize("heads,n_kv,page,lens", [(8, 2, 64, [70001, 3, 20000]), (16, 1, 16, [9001]),
+                                                  (4, 4, 32, [4100, 17, 2049])])
+def test_decode_counts_every_key_once(gen, ws, heads, n_kv, page, lens):
+    k_pages, v_pages, table, _ = fill_cache(gen, lens, page, n_kv)
+    q = torch.zeros(len(lens), heads, P.D, dtype=torch.bfloat16, device="cuda")
+    start = ints([n - 1 for n in lens])
+    for window in range(-(-max(lens) // P.CODE_WINDOW)):
+        coded(k_pages, v_pages, table, page, lens, window)
+        out = G.paged_decode(q, start, k_pages, v_pages, table, workspace=ws)
+        for b, n in enumerate(lens):
+            P.check_counts(out[b:b + 1], window, n - 1, f"sequence {b} of {n} rows")
+
+
+@pytest.mark.parametrize("heads,n_kv,page,lens,starts", SHARED)
+def test_paged_prefill_counts_every_key_once(gen, ws, heads, n_kv, page, lens, starts):
+    ends = [s + t for s, t in zip(starts, lens)]
+    k_pages, v_pages, table, _ = fill_cache(gen, ends, page, n_kv)
+    q = torch.zeros(sum(lens), heads, P.D, dtype=torch.bfloat16, device="cuda")
+    cu, start = offsets(lens), ints(starts)
+    for window in range(-(-max(ends) // P.CODE_WINDOW)):
+        coded(k_pages, v_pages, table, page, ends, window)
+        out = G.paged_prefill(q, cu, start, k_pages, v_pages, table, workspace=ws)
+        at = 0
+        for b, (t, s) in enumerate(zip(lens, starts)):
+            P.check_counts(out[at:at + t], window, s, f"sequence {b}: {t} tokens after {s}")
+            at += t
+
+
 # ------------------------------------------------------------------ errors on the device
 
 def test_bad_positions_are_reported_and_skipped(gen, ws):
