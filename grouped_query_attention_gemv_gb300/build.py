@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import fcntl
 import os
 import shutil
 import subprocess
@@ -66,8 +67,15 @@ def _stale(target: str, inputs) -> bool:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
-    """Compile and link; return the path of libgqa.so. Raises on failure."""
+    """Compile and link; return the path of libgqa.so. Raises on failure. One
+    build at a time works on the tree: another waits for it, and finds its files."""
     os.makedirs(OBJ_DIR, exist_ok=True)
+    with open(os.path.join(OUT_DIR, ".lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        return _build(force, verbose_ptxas, quiet)
+
+
+def _build(force: bool, verbose_ptxas: bool, quiet: bool) -> str:
     cc = nvcc()
     deps = _deps()
     jobs = []

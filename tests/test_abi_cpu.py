@@ -206,3 +206,40 @@ def test_host_entries_reject_bad_arguments(lib):
         assert f(*bad) == code, (i, v)
     assert lib.gqa_host_stage_release(None) == -1
     assert lib.gqa_host_stage_wait(None, None) == -1
+
+
+def test_builds_at_once_do_not_write_each_others_files(monkeypatch, tmp_path):
+    """Two builds of one stale tree (two test workers, say): the second waits for
+    the first, finds nothing left to do, and no object is linked half-written."""
+    import subprocess
+    import threading
+    import time
+
+    out = tmp_path / "lib"
+    monkeypatch.setattr(gbuild, "OUT_DIR", str(out))
+    monkeypatch.setattr(gbuild, "OBJ_DIR", str(out / "obj"))
+    monkeypatch.setattr(gbuild, "LIB", str(out / "libgqa.so"))
+    monkeypatch.setattr(gbuild, "BINDING", str(out / "gqa_binding.so"))
+    monkeypatch.setattr(gbuild, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    made, torn = [], []
+
+    def run(cmd, **kw):   # stands in for the compilers: writes its output slowly
+        target = cmd[cmd.index("-o") + 1]
+        if "-c" not in cmd:
+            torn.extend(x for x in cmd if x.endswith(".o") and open(x).read() != "whole")
+        with open(target, "w") as f:
+            f.write("wh")
+            f.flush()
+            time.sleep(0.05)
+            f.write("ole")
+        made.append(target)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(gbuild.subprocess, "run", run)
+    threads = [threading.Thread(target=gbuild.build) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not torn
+    assert len(made) == len(set(made)) == len(gbuild.sources()) + 3   # each object, binding.o, two links
