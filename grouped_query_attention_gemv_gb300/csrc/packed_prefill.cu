@@ -22,7 +22,7 @@
 // S of the next), so that one tile's softmax (~1,400 cycles from S to all of
 // P) runs beside the other's products (~1,430 a step). Left alone they fall
 // into step, both softmaxes and then all products: 3,900 cycles a key tile
-// against 3,150. One issuer for both took 3,700.
+// against 3,150 (2,800 as it stands). One issuer for both took 3,700.
 //
 // Ragged sequences. Entries (pairs of Q tiles of a sequence) x KV heads are
 // the items. Up to 320 entries are sorted longest first, and the CTAs claim
@@ -41,7 +41,10 @@
 //     22 us for 40 tokens after 8,000 (8 heads, 2 KV heads), where a join by
 //     the last CTA took 47; 32 for 256 after 4,000 (32 and 8 heads) against 52.
 //     Empty, that kernel takes 2 us, so it is not launched where no sequence
-//     can have more than 2,048 keys.
+//     can have more than 2,048 keys (packed_prefill_may_join: what that costs).
+// Above 320 entries nothing is sorted or cut, and a long sequence among them is
+// walked by one CTA per KV head: 320 single tokens and one after 131,071 take
+// 1,280 us, 319 and one 180.
 // An item counts ITEM_UNITS key tiles more than it has, or a range of many
 // short items ends last: 45 us against 59 for one prompt of 4,000 tokens (8 and
 // 2 heads), 32 against 36 for 2,340.
@@ -67,10 +70,11 @@
 // DEV_WAIT_TIMEOUT, lets
 // issued copies and products finish (bounded) and frees TMEM before the CTA
 // exits.
-// Measured: 402 us for nine prompts of up to 4,095 tokens (578 GFLOP: 1,437
-// TFLOP/s of 1,962 measured), 100 to 106 for 1,024 tokens after 7,168, 35.2 for
-// 2,048 tokens, 7.1 for 17. What bounds the long ones is the alternation: per
-// key tile the tensor pipe works 2 x 1,024 of 2,900 cycles.
+// Measured: 382 us for nine prompts of up to 4,095 tokens in a short run (578
+// GFLOP: 1,515 TFLOP/s of 1,962 measured), 420 under the power cap, 98 to 104
+// for 1,024 tokens after 7,168, 34.2 for 2,048 tokens, 7.1 for 17. What bounds
+// the long ones is the alternation: per key tile the tensor pipe works 2 x 1,024
+// of about 2,800 cycles.
 #include <math.h>
 
 #include "paged.h"
@@ -1198,7 +1202,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 }  // namespace
 
 // Whether items can come to have parts for the second kernel: no more entries
-// than are sorted, and keys enough to repay it (an empty one takes 2 us).
+// than are sorted, and more than 2,048 keys that a sequence may have. The host
+// knows only that bound, so this weighs calls that share nothing, which pay for
+// an empty kernel (17 tokens 7.1 us without and 9.0 with, 2,048 tokens 36.9 and
+// 38.8), against those that would share more (without / with the second kernel,
+// 8 and 2 heads: 5 tokens at 512 keys 11.3 / 12.5 us, 1,024 15.7 / 17.2, 1,500
+// 18.3 / 15.0, 2,048 20.9 / 15.4; 256 tokens 12.9 / 15.4, 19.0 / 21.6, 24.5 /
+// 20.2, 30.0 / 21.7; 32 and 8 heads: 5 tokens 11.4 / 12.7, 16.3 / 20.9, 18.9 /
+// 16.5, 21.7 / 16.7; 256 tokens 13.1 / 15.5, 19.1 / 21.8, 24.6 / 27.3, 30.1 /
+// 32.9). Few rows after 1,500 to 2,048 keys lose 2 to 8 us by it; whole prompts
+// of that length, which it was set for, gain 2.
 bool packed_prefill_may_join(int N, int n_rep, long long most_keys) {
   return N / (NQ * (ROWS / n_rep)) <= MAX_SORT && most_keys > 2048;
 }
