@@ -142,6 +142,7 @@ struct Bars {
   int q_issued[NQ], k_issued, v_issued;
   int warp_sum[THREADS / 32];
   int rows;                   // most query rows of an item
+  int warps_here;             // softmax warps with their rows of a shared item
   int is_last;                // of an item's parts, this CTA's is the last
   int parts_there;            // the others are written
   Item item[SLOTS];           // g < 0: no more
@@ -486,6 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     bs.abort = 0;
     bs.alive = 0;
+    bs.warps_here = 0;
     bs.wait_ns = a.wait_ns;
     bs.rows = 0;
     bs.q_issued[0] = bs.q_issued[1] = 0;
@@ -1014,12 +1016,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Of few parts, the CTA that arrives last at the item's ticket adds the
         // others (they have arrived, so they are running and about to write
         // theirs) to its own, in CTA order all the same. More are left to the
-        // second kernel. Only the item's first CTA can have had an item before,
-        // with rows to compute again: it is then the last one here.
+        // second kernel. A CTA arrives with the last of its warps: one may still
+        // be computing rows of the item before again, which takes any time.
         const int c = blockIdx.x, others = it.last - it.first;
         int* arrived = a.tickets + 2 * it.first;
         if (others <= DIRECT) {
-          if (threadIdx.x == 0) bs.is_last = atomicAdd(arrived, 1) == others;
+          if (lane == 0 && atomicAdd(&bs.warps_here, 1) == 7) {
+            bs.warps_here = 0;
+            bs.is_last = atomicAdd(arrived, 1) == others;
+          }
           if (!softmax_sync(bs, syncs)) {
             ok = false;
             break;

@@ -687,6 +687,40 @@ def test_rows_computed_again_are_no_stall(gen, ws):
         P.check(out[:, g:g + 1][keep], ref[keep], tol[keep], f"head {g}")
 
 
+@pytest.mark.parametrize("heads,short,long", [(104, 4, 73), (79, 10, 37), (57, 3, 21), (51, 2, 33), (123, 4, 60)])
+def test_rows_computed_again_before_a_shared_item_are_no_stall(gen, ws, heads, short, long):
+    """Two sequences of `short` and `long` key tiles: a range ends one tile into
+    the second one's first head, and the last item before that has rows to
+    compute again in its second query tile alone. The CTA that adds up the
+    shared item's parts must not take that CTA for arrived meanwhile."""
+    k_pages, v_pages = (P.normal(gen, 5, 128, heads, P.D) for _ in range(2))
+    table = torch.zeros(2, long, dtype=torch.int32, device="cuda")   # prefixes are page 0 over and over
+    table[0, short - 2:short], table[1, long - 2:] = ints([1, 2]), ints([3, 4])
+    v_pages[2, 100, heads - 1, 5] = math.nan
+    q = P.normal(gen, 512, heads, P.D)
+    starts = [128 * (short - 2), 128 * (long - 2)]
+    out = torch.full_like(q, 9.0)
+    prev = G.set_wait_limit_ns(500_000)
+    try:
+        for _ in range(10):
+            G.paged_prefill(q, offsets([256, 256]), ints(starts), k_pages, v_pages, table, out=out, workspace=ws)
+            assert G.device_status(ws) == 0
+    finally:
+        G.set_wait_limit_ns(prev)
+        ws.zero_()
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[228:256, heads - 1, 5] = True
+    assert torch.isnan(out[hit]).all()
+    for b, s in enumerate(starts):
+        rows = slice(256 * b, 256 * b + 256)
+        for g in (0, 1, heads // 2, heads - 1):
+            k, v = (P.read_rows(x[:, :, g:g + 1], table, 128, b, s + 256) for x in (k_pages, v_pages))
+            ref, mean, size = P.attend64(q[rows, g:g + 1], k, torch.nan_to_num(v), s)
+            tol = P.bound(ref, mean, size, s + 256, P.P_ONE_TERM)
+            keep = ~hit[rows, g:g + 1]
+            P.check(out[rows, g:g + 1][keep], ref[keep], tol[keep], f"sequence {b}, head {g}")
+
+
 # ------------------------------------------------------------------ as a server uses them
 
 def test_prompt_chunks_and_decode_steps_together(gen, ws):
