@@ -44,92 +44,24 @@
 // 1,001, 32 KV heads), 16.2 for 66 MB (8 KV heads), 3.4 for one sequence of
 // 16 rows. Head-major pages ([page, KV head,
 // row]) are 2 to 4% faster than [page, row, KV head]: longer runs per CTA.
-#include <math.h>
-
-#include "paged.h"
+#include "decode_parts.cuh"
 
 namespace gqa {
 
 namespace {
+
+using namespace decode;
 
 constexpr int KEYS = 16;                          // positions of a chunk
 constexpr int ROW_BYTES = HEAD_DIM * 2;
 constexpr int TILE_BYTES = KEYS * ROW_BYTES;      // K or V of a chunk
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
 constexpr int STAGES = 2;
-constexpr int WARPS = 8;
-// In 1/800 us, what a chunk takes at the whole memory's rate: a chunk of a CTA
-// by itself (it streams 9 or 10 a us, 64 to 128 KB in flight), and joining
-// across CTAs (2.5 us).
-constexpr float ALONE = 85.f, JOIN_COST = 2000.f;
-constexpr int BATCH = 5;                          // partials a warp has in flight when it joins
-constexpr int PART = HEAD_DIM + 2;                // floats of a partial row: o, max, sum
 
 // Row r, 16-byte piece c of a 256-byte-row tile: eight rows of one piece fall
 // into eight different 16-byte columns.
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return static_cast<uint32_t>(r * ROW_BYTES + ((c ^ (r & 7)) << 4));
-}
-
-// A place in the chunk order.
-struct Cursor {
-  int b, h, j;  // sequence, KV head, chunk of it
-  int n;        // chunks of the sequence (for each KV head)
-};
-
-// pre[b]: chunks per KV head of the sequences before b.
-__device__ __forceinline__ Cursor locate(int u, const int* pre, int B, int n_kv) {
-  const int x = u / n_kv;  // pre[b] <= x < pre[b + 1] exactly when u lies in sequence b
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] <= x) lo = mid; else hi = mid;
-  }
-  Cursor c;
-  c.b = lo;
-  c.n = pre[lo + 1] - pre[lo];
-  const int r = u - pre[lo] * n_kv;
-  c.h = r / c.n;
-  c.j = r - c.h * c.n;
-  return c;
-}
-__device__ __forceinline__ void advance(Cursor& c, const int* pre, int B, int n_kv) {
-  if (++c.j < c.n) return;
-  c.j = 0;
-  if (++c.h < n_kv) return;
-  c.h = 0;
-  do {
-    if (++c.b >= B) return;
-    c.n = pre[c.b + 1] - pre[c.b];
-  } while (c.n == 0);
-}
-
-// A part of a (sequence, KV head), left for joining: its chunks
-// [first, end) identify it, `row` is its first row of the output.
-struct Part {
-  int first, end, row;
-};
-
-// This lane's 4 dims of an output row.
-__device__ __forceinline__ void store_row(__nv_bfloat16* out, int row, float4 o, float inv) {
-  *(reinterpret_cast<uint2*>(out + static_cast<long long>(row) * HEAD_DIM) + (threadIdx.x & 31)) =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-}
-
-// Counts this CTA at a ticket: behind the barrier before it, it publishes all
-// the CTA's stores, and to the barrier behind it those of the CTAs before.
-__device__ __forceinline__ int arrive(int* ticket) {
-  int n;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
-  return n;
-}
-
-// A running (max, sum, output) taken to the max mx.
-__device__ __forceinline__ void rescale(float& m, float mx, float& l, float4& o) {
-  const float s = ex2_approx(m - (mx == -INFINITY ? 0.f : mx));
-  m = mx;
-  l *= s;
-  o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
 }
 
 // NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16).
@@ -145,57 +77,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   float* stash = reinterpret_cast<float*>(smem + W * (STAGES * STAGE_BYTES));
   int* pre = reinterpret_cast<int*>(stash + W * n_rep * PART);
   int* last = pre + p.B + 1;  // last row of each sequence
-  __shared__ Part parts[2 * WARPS];  // each warp's two, first = -1: none
-  __shared__ int warp_sum[WARPS], warp_max[WARPS];
-  __shared__ int is_last[2];
-  __shared__ Part joint[2];  // of the shared segments: first and last CTA, first output row
+  __shared__ Shared sh;
 
   // nothing is read or written before the previous kernel of the stream is done
   pdl_trigger();
   pdl_wait();
   // chunks per sequence, prefix-summed; unused slots and bad positions have none
-  int total, longest;
-  {
-    const int per = (p.B + blockDim.x - 1) / blockDim.x;
-    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
-    int sum = 0, most = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const int s = p.start[b];
-      const bool ok = s >= 0 && s < p.pages.capacity();
-      if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
-      const int n = ok ? s / KEYS + 1 : 0;
-      pre[b + 1] = n;
-      last[b] = s;
-      sum += n;
-      most = max(most, n);
-    }
-    int run = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += x;
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    if (lane == 31) warp_sum[warp] = run;
-    if (lane == 0) warp_max[warp] = most;
-    if (threadIdx.x < 2 * WARPS) parts[threadIdx.x].first = -1;
-    if (threadIdx.x == 0) pre[0] = 0;
-    __syncthreads();
-    run -= sum;
-    total = longest = 0;
-    for (int w = 0; w < W; ++w) {
-      if (w == warp) run += total;
-      total += warp_sum[w];
-      longest = max(longest, warp_max[w]);
-    }
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      run += pre[b + 1];
-      pre[b + 1] = run;
-    }
-    __syncthreads();
-  }
+  const Count count = count_chunks(sh, pre, p.B, [&](int b) {
+    const int s = p.start[b];
+    const bool ok = s >= 0 && s < p.pages.capacity();
+    if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
+    last[b] = s;
+    return ok ? s / KEYS + 1 : 0;
+  });
   // rows of sequences without keys
 #pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
@@ -204,27 +98,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
       for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
         reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
 
-  total *= p.n_kv;
+  const int total = count.total * p.n_kv;
   if (total == 0) return;
   const int ctas = decode_ctas(total, gridDim.x, W);
   const Split split(total, ctas);
-  // One CTA per (sequence, KV head) instead of equal ranges where that costs
-  // less than joining parts across CTAs.
-  const float memory = static_cast<float>(total);
-  const bool own = p.B * p.n_kv <= static_cast<int>(gridDim.x) &&
-                   fmaxf(static_cast<float>(longest) * ALONE, memory) <=
-                       fmaxf(static_cast<float>(split.each) * ALONE, memory) + JOIN_COST;
   int c0, c1;
-  if (own) {
-    if (static_cast<int>(blockIdx.x) >= p.B * p.n_kv) return;
-    const int b = blockIdx.x / p.n_kv, h = blockIdx.x - b * p.n_kv, n = pre[b + 1] - pre[b];
-    c0 = pre[b] * p.n_kv + h * n;
-    c1 = c0 + n;
-  } else {
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
-    c0 = split.start(blockIdx.x);
-    c1 = split.start(blockIdx.x + 1);
-  }
+  if (!cta_range(total, count.longest, split, ctas, pre, p.B, p.n_kv, c0, c1)) return;
   const int a0 = warp_start(c0, c1, warp, W), a1 = warp_start(c0, c1, warp + 1, W);
   const int n = a1 - a0;
 
@@ -422,166 +301,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
               row[HEAD_DIM + 1] = l_run[nt][e];
             }
           }
-        if (lane == 0) parts[2 * warp + slot] = seg;
+        if (lane == 0) sh.parts[2 * warp + slot] = seg;
       }
     }
   }
   __syncthreads();
 
-  // ---- join this CTA's parts: lane e < 2W looks at entry e; those of one
-  // (sequence, KV head) follow each other. (part, query head) pairs are dealt
-  // to the warps.
-  auto part_at = [&](int e) -> const float* {
-    return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
-                   : stash + (e >> 1) * n_rep * PART;
-  };
-  Part cross[2] = {{-1, 0, 0}, {-1, 0, 0}};  // with parts in other CTAs too: begun before this one, going on behind it
-  {
-    Part mine{-1, 0, 0};
-    if (lane < 2 * W) mine = parts[lane];
-    const unsigned peers = __match_any_sync(0xffffffffu, mine.first);
-    unsigned heads = __ballot_sync(0xffffffffu, mine.first >= 0 && __ffs(peers) - 1 == lane);
-#pragma unroll 1
-    for (int k = 0; heads; heads &= heads - 1) {
-      const int e = __ffs(heads) - 1;
-      const unsigned members = __shfl_sync(0xffffffffu, peers, e);
-      const Part seg{__shfl_sync(0xffffffffu, mine.first, e), __shfl_sync(0xffffffffu, mine.end, e),
-                     __shfl_sync(0xffffffffu, mine.row, e)};
-      const int side = seg.first < c0 ? 0 : seg.end > c1 ? 1 : 2;  // 2: all of it is here
-      if (side == 0) cross[0] = seg;
-      if (side == 1) cross[1] = seg;
-#pragma unroll 1
-      for (int r = 0; r < n_rep; ++r, ++k) {
-        if (k % W != warp) continue;
-        float m_e = -INFINITY, l_e = 0.f;
-        if (members >> lane & 1) {
-          const float2 ml = *reinterpret_cast<const float2*>(part_at(lane) + r * PART + HEAD_DIM);
-          m_e = ml.x;
-          l_e = ml.y;
-        }
-        float m = m_e;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float w_e = ex2_approx(m_e - (m == -INFINITY ? 0.f : m));
-        float l = w_e * l_e;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (unsigned g = members; g; g &= g - 1) {
-          const int f = __ffs(g) - 1;
-          const float w = __shfl_sync(0xffffffffu, w_e, f);
-          const float* row = part_at(f) + r * PART + 4 * lane;
-          const float2 x = *reinterpret_cast<const float2*>(row), y = *reinterpret_cast<const float2*>(row + 2);
-          o.x += w * x.x;
-          o.y += w * x.y;
-          o.z += w * y.x;
-          o.w += w * y.y;
-        }
-        if (side == 2) {
-          store_row(p.out, seg.row + r, o, 1.f / l);
-        } else {
-          const long long at = (2LL * blockIdx.x + side) * n_rep + r;
-          __stcg(reinterpret_cast<float4*>(p.part_o + at * HEAD_DIM) + lane, o);
-          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + at, make_float2(m, l));
-        }
-      }
-    }
-  }
-  if (cross[0].first < 0 && cross[1].first < 0) return;
-
-  // ---- across CTAs: the ticket is that of the CTA with the first chunk
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const Part seg = threadIdx.x ? cross[1] : cross[0];
-    int last = 0;
-    if (seg.first >= 0) {
-      const int a = split.holder(seg.first), z = split.holder(seg.end - 1);
-      last = arrive(p.tickets + a) == z - a;
-      if (last) p.tickets[a] = 0;
-      joint[threadIdx.x] = {a, z, seg.row};
-    }
-    is_last[threadIdx.x] = last;
-  }
-  __syncthreads();
-  // Per query head `ways` warps share the partials, each with a running max,
-  // then the first of them adds up. Few CTAs come here and their instruction
-  // caches are cold: the loops are kept short (one sequence of 1,001 rows: 8.8
-  // us with batches of 5, 9.2 with 8 or 4; 9.35 with a pass for the max before).
-  const int ways = max(1, W / n_rep);
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    if (!is_last[side]) continue;
-    const int a = joint[side].first, z = joint[side].end;
-#pragma unroll 1
-    for (int r0 = 0; r0 < n_rep; r0 += W / ways) {
-      const int r = r0 + warp / ways, way = warp % ways;
-      const bool on = warp / ways < W / ways && r < n_rep;
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (on) {
-        // the part of its first CTA goes on behind that CTA (slot 1), the others began before theirs (slot 0)
-        auto at = [&](int c) { return (2 * c + (c == a)) * n_rep + r; };
-        const float2* mls = reinterpret_cast<const float2*>(p.part_ml);
-        const float4* os = reinterpret_cast<const float4*>(p.part_o) + lane;
-#pragma unroll 1
-        for (int c0 = a + way; c0 <= z; c0 += BATCH * ways) {
-          float2 ml[BATCH];
-          float4 x[BATCH];
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const int c = c0 + k * ways;
-            ml[k] = make_float2(-INFINITY, 0.f);
-            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c <= z) {
-              ml[k] = __ldcg(mls + at(c));
-              x[k] = __ldcg(os + at(c) * (HEAD_DIM / 4));
-            }
-          }
-          float mx = m;
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) mx = fmaxf(mx, ml[k].x);
-          rescale(m, mx, l, o);
-          const float ref = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-          for (int k = 0; k < BATCH; ++k) {
-            const float w = ex2_approx(ml[k].x - ref);
-            l += w * ml[k].y;
-            o.x += w * x[k].x;
-            o.y += w * x[k].y;
-            o.z += w * x[k].z;
-            o.w += w * x[k].w;
-          }
-        }
-      }
-      if (ways > 1) {
-        float* mine = reinterpret_cast<float*>(smem) + warp * PART;
-        __syncthreads();
-        if (on && way) {
-          *reinterpret_cast<float2*>(mine + 4 * lane) = make_float2(o.x, o.y);
-          *reinterpret_cast<float2*>(mine + 4 * lane + 2) = make_float2(o.z, o.w);
-          if (lane == 0) *reinterpret_cast<float2*>(mine + HEAD_DIM) = make_float2(m, l);
-        }
-        __syncthreads();
-        if (on && !way)
-#pragma unroll 1
-          for (int g = 1; g < ways; ++g) {
-            const float* row = mine + g * PART;
-            const float2 ml = *reinterpret_cast<const float2*>(row + HEAD_DIM);
-            const float2 x = *reinterpret_cast<const float2*>(row + 4 * lane);
-            const float2 y = *reinterpret_cast<const float2*>(row + 4 * lane + 2);
-            rescale(m, fmaxf(m, ml.x), l, o);
-            const float w = ex2_approx(ml.x - (m == -INFINITY ? 0.f : m));
-            l += w * ml.y;
-            o.x += w * x.x;
-            o.y += w * x.y;
-            o.z += w * y.x;
-            o.w += w * y.y;
-          }
-      }
-      if (on && !way) store_row(p.out, joint[side].row + r, o, 1.f / l);
-    }
-  }
+  join_parts(
+      sh, reinterpret_cast<float*>(smem), split, c0, c1, n_rep, p.part_o, p.part_ml, p.tickets,
+      [&](int e) -> const float* {
+        return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
+                       : stash + (e >> 1) * n_rep * PART;
+      },
+      [&](int row, float4 o, float m, float l) { store_row(p.out, row, o, 1.f / l); });
 }
 
 template <int NT>
