@@ -37,7 +37,8 @@ __all__ = [
     "STATIC_SCRATCH_BYTES", "make_host_stage", "default_host_stage", "host_stage_wait", "release_host_stage",
     "decode_host",
     "block_forward_host", "PAGED_WORKSPACE_BYTES", "make_paged_workspace", "default_paged_workspace",
-    "paged_append", "paged_decode", "paged_prefill", "packed_prefill",
+    "paged_append", "paged_decode", "paged_prefill", "packed_prefill", "paged_append_fp8", "paged_read_fp8",
+    "paged_decode_fp8",
 ]
 
 D_MODEL, N_HEADS, N_KV_HEADS, HEAD_DIM = 4096, 32, 8, 128
@@ -74,6 +75,13 @@ _SIGNATURES = {
     "gqa_host_stage_wait": (_i, [_vp, _vp]),
     "gqa_host_stage_release": (_i, [_vp]),
     "gqa_paged_append": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "gqa_rope_table_dim": (_i, [_vp, _i, _i, _d, _i, _d, _d, _d, _d, _vp]),
+    "gqa_paged_append_rotary": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp,
+                                     _vp, _sz, _vp]),
+    "gqa_paged_append_fp8": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp,
+                                  _sz, _vp]),
+    "gqa_paged_read_fp8": (_i, [_vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "gqa_paged_decode_fp8": (_i, [_vp, _ll, _i, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_paged_decode": (_i, [_vp, _ll, _i, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_paged_prefill": (_i, [_vp, _ll, _i, _i, _vp, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_packed_prefill": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i, _vp, _i, _f, _vp, _vp, _sz, _vp]),
@@ -170,11 +178,14 @@ def make_workspace(B: int, T: int, max_keys: int, device=None) -> torch.Tensor:
 
 def rope_table(rows: int, theta: float = 500000.0, scaled: bool = True, factor: float = 8.0,
                low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
-               original_context: float = 8192.0, device=None, stream=None) -> torch.Tensor:
-    """fp32 [rows, 64, 2] table of (cos, sin), built on the device."""
-    out = torch.empty(rows, 64, 2, dtype=torch.float32, device=device or "cuda")
-    r = lib().gqa_rope_table(_p(out), rows, theta, int(scaled), factor, low_freq_factor,
-                             high_freq_factor, original_context, _s(stream, out.device))
+               original_context: float = 8192.0, device=None, stream=None, dim: int = HEAD_DIM) -> torch.Tensor:
+    """fp32 [rows, dim / 2, 2] table of (cos, sin), built on the device; dim: the
+    dims of a head that are turned (even, 2 to 128)."""
+    if not 2 <= dim <= HEAD_DIM or dim % 2:
+        raise ValueError(f"dim must be even, 2 to {HEAD_DIM}, got {dim}")
+    out = torch.empty(rows, dim // 2, 2, dtype=torch.float32, device=device or "cuda")
+    r = lib().gqa_rope_table_dim(_p(out), rows, dim, theta, int(scaled), factor, low_freq_factor,
+                                 high_freq_factor, original_context, _s(stream, out.device))
     if r:
         raise GQAError(r, "gqa_rope_table")
     return out
@@ -576,7 +587,7 @@ def _defaults(like, name, out, workspace, stream):
 
 
 def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens=None, q_out=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, rotary_dim: int = HEAD_DIM, halves: bool = False):
     """Rotate packed queries and keys by RoPE and write keys and values into
     cache pages.
 
@@ -587,7 +598,9 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     of each sequence; -1 an unused slot. k_pages, v_pages [pages, page_size,
     n_kv, 128], page_size a power of two >= 16; block_table device int32 [B,
     columns]. Returns the rotated queries (q_out, which may be q), or None
-    without q. Otherwise no output of the paged operators, and here none of the
+    without q. rotary_dim: the first dims of a head that are turned (a multiple
+    of 16; rope [rows, rotary_dim / 2, 2]), the others are kept; halves: dims i
+    and i + rotary_dim / 2 are a pair instead of 2i and 2i + 1. No other output of the paged operators, and here none of the
     pages, may share memory with their inputs (a tensor counts from its first
     byte to its last); key and value pages may interleave but not meet.
     Bad positions and table entries are found on the device: ``device_status``
@@ -597,11 +610,58 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     if workspace is None or (q_out is None and q is not None):
         x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
         q_out = None if q is None else x
-    r = (_paged or _binding()).paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens, q_out,
-                                            workspace, None if stream is None else stream.cuda_stream)
+    s = None if stream is None else stream.cuda_stream
+    if rotary_dim == HEAD_DIM and not halves:
+        r = (_paged or _binding()).paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens,
+                                                q_out, workspace, s)
+    else:
+        r = (_paged or _binding()).paged_append_rotary(q, k, v, start_pos, rope, k_pages, v_pages, block_table,
+                                                       cu_tokens, q_out, rotary_dim, halves, workspace, s)
     if r:
         raise GQAError(r, "gqa_paged_append")
     return q_out
+
+
+def paged_append_fp8(q, k, v, start_pos, rope, k_pages, v_pages, k_scales, v_scales, block_table, cu_tokens=None,
+                     q_out=None, rotary_dim: int = HEAD_DIM, halves: bool = False, workspace=None, stream=None):
+    """``paged_append`` into a cache of 8 bits: rows of 128 values are held as
+    e4m3 (k_pages, v_pages torch.float8_e4m3fn [pages, page_size, n_kv, 128])
+    times 2^(s - 127), s the row's byte in k_scales, v_scales (torch.uint8
+    [pages, page_size, n_kv], any strides, memory of their own). The exponent is
+    the least in [-100, 120] for which the row's finite values fit, so a value
+    is off by 2^-4 of itself at most (by 2^-10 of the scale below 2^-6 of it);
+    what is not finite is held as NaN. The queries are rotated and returned as
+    by ``paged_append``."""
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    if workspace is None or (q_out is None and q is not None):
+        x, workspace = _defaults(k if q is None else q, "k" if q is None else "q", q_out, workspace, stream)
+        q_out = None if q is None else x
+    r = (_paged or _binding()).paged_append_fp8(q, k, v, start_pos, rope, k_pages, v_pages, k_scales, v_scales,
+                                                block_table, cu_tokens, q_out, rotary_dim, halves, workspace,
+                                                None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_append_fp8")
+    return q_out
+
+
+def paged_read_fp8(rows, k_pages, v_pages, k_scales, v_scales, block_table, k_out, v_out, out_table, workspace=None,
+                   stream=None) -> None:
+    """Read cache rows 0..rows[b]-1 of every sequence (device int32 [B]; 0 or -1:
+    none) from 8-bit pages into bf16 pages k_out, v_out [pages, page_size, n_kv,
+    128] under out_table, exactly; page sizes may differ. For
+    ``paged_prefill`` of a chunk after a quantised prefix, for instance. Other
+    rows of k_out and v_out are left as they were."""
+    if workspace is None:
+        if not isinstance(rows, torch.Tensor):
+            raise TypeError("rows must be a torch.Tensor")
+        if not rows.is_cuda:
+            raise ValueError("rows must be a CUDA tensor")
+        workspace = default_paged_workspace(rows.device, stream)
+    r = (_paged or _binding()).paged_read_fp8(rows, k_pages, v_pages, k_scales, v_scales, block_table, k_out, v_out,
+                                              out_table, workspace, None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_read_fp8")
 
 
 def paged_decode(q, start_pos, k_pages, v_pages, block_table, scale: float = HEAD_DIM ** -0.5, out=None,
@@ -616,6 +676,18 @@ def paged_decode(q, start_pos, k_pages, v_pages, block_table, scale: float = HEA
                                             None if stream is None else stream.cuda_stream)
     if r:
         raise GQAError(r, "gqa_paged_decode")
+    return out
+
+
+def paged_decode_fp8(q, start_pos, k_pages, v_pages, k_scales, v_scales, block_table, scale: float = HEAD_DIM ** -0.5,
+                     out=None, workspace=None, stream=None) -> torch.Tensor:
+    """``paged_decode`` over an 8-bit cache (``paged_append_fp8``)."""
+    if out is None or workspace is None:
+        out, workspace = _defaults(q, "q", out, workspace, stream)
+    r = (_paged or _binding()).paged_decode_fp8(q, start_pos, k_pages, v_pages, k_scales, v_scales, block_table, scale,
+                                                out, workspace, None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_decode_fp8")
     return out
 
 

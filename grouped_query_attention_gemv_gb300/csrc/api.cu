@@ -37,8 +37,9 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Every tensor map of this library: bf16, 128-byte swizzle, no interleave,
-// 256-byte L2 promotion, zero fill. Encoding one costs the host about a
+// Every tensor map of this library: bf16 with 256-byte L2 promotion, or bytes
+// with 128-byte promotion (a box row is then 128 bytes); 128-byte swizzle, no
+// interleave, zero fill. Encoding one costs the host about a
 // microsecond and a decode call needs ~16, so each thread keeps the last
 // ones it encoded (a map depends only on these arguments; the buffers behind
 // the pointers are the caller's and are not read).
@@ -48,8 +49,9 @@ struct MapKey {
   cuuint64_t dims[4];
   cuuint64_t strides[3];
   cuuint32_t box[4];
+  bool bytes;
   bool operator==(const MapKey& o) const {
-    if (ptr != o.ptr || rank != o.rank) return false;
+    if (ptr != o.ptr || rank != o.rank || bytes != o.bytes) return false;
     for (cuuint32_t i = 0; i < rank; ++i)
       if (dims[i] != o.dims[i] || box[i] != o.box[i] || (i + 1 < rank && strides[i] != o.strides[i])) return false;
     return true;
@@ -91,13 +93,14 @@ int launched(cudaError_t e) {
   return GQA_OK;
 }
 
-bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
-                 const cuuint32_t* box) {
+static bool encode_map(CUtensorMap* m, bool bytes, cuuint32_t rank, const void* ptr, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = encode_fn();
   if (!enc || rank < 1 || rank > 4) return false;
   MapKey k{};
   k.ptr = ptr;
   k.rank = rank;
+  k.bytes = bytes;
   uint64_t h = reinterpret_cast<uintptr_t>(ptr) * 0x9E3779B97F4A7C15ull ^ rank;
   for (cuuint32_t i = 0; i < rank; ++i) {
     k.dims[i] = dims[i];
@@ -116,14 +119,23 @@ bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint6
     return true;
   }
   const cuuint32_t es[4] = {1, 1, 1, 1};
-  if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, es,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  if (enc(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims,
+          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          bytes ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return false;
   e.key = k;
   e.map = *m;
   e.used = true;
   return true;
+}
+bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+  return encode_map(m, false, rank, ptr, dims, strides, box);
+}
+bool encode_bytes(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box) {
+  return encode_map(m, true, rank, ptr, dims, strides, box);
 }
 
 int sm_count() {
@@ -574,19 +586,26 @@ int gqa_device_status(void* workspace, int* status, int clear) {
   return *status ? GQA_EDEVICE : GQA_OK;
 }
 
-int gqa_rope_table(float* rope, int rows, double theta, int scaled, double factor, double low_freq_factor,
-                   double high_freq_factor, double original_context, void* stream) {
+int gqa_rope_table_dim(float* rope, int rows, int rotary_dim, double theta, int scaled, double factor,
+                       double low_freq_factor, double high_freq_factor, double original_context, void* stream) {
   if (!rope || rows <= 0 || !(theta > 1.0)) return GQA_EINVAL;
+  if (rotary_dim < 2 || rotary_dim > HEAD_DIM || rotary_dim % 2) return GQA_EINVAL;
   if (scaled && !(factor > 0.0 && high_freq_factor > low_freq_factor && low_freq_factor > 0.0 &&
                   original_context > 0.0))
     return GQA_EINVAL;
   if (!aligned16(rope)) return GQA_EALIGN;
   t_launches = 0;
-  cudaError_t e = launch_rope_table(rope, rows, theta, scaled, factor, low_freq_factor, high_freq_factor,
+  cudaError_t e = launch_rope_table(rope, rows, rotary_dim, theta, scaled, factor, low_freq_factor, high_freq_factor,
                                     original_context, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail_cuda(e);
   t_launches = 1;
   return GQA_OK;
+}
+
+int gqa_rope_table(float* rope, int rows, double theta, int scaled, double factor, double low_freq_factor,
+                   double high_freq_factor, double original_context, void* stream) {
+  return gqa_rope_table_dim(rope, rows, HEAD_DIM, theta, scaled, factor, low_freq_factor, high_freq_factor,
+                            original_context, stream);
 }
 
 static bool valid_n_kv(int n_kv) { return n_kv == N_KV || n_kv == N_HEADS; }

@@ -19,5 +19,7 @@ int launched(cudaError_t e);                 // counts a launch that returned e;
 void prof_mark(int i, cudaStream_t s);       // gqa_set_profile_events: event i, if set
 bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box);
+bool encode_bytes(CUtensorMap* m, cuuint32_t rank, const void* ptr, const cuuint64_t* dims, const cuuint64_t* strides,
+                  const cuuint32_t* box);
 
 }  // namespace gqa

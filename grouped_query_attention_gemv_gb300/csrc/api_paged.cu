@@ -64,6 +64,35 @@ int check_pages(const gqa_pages* g, PagedCache* c) {
   return GQA_OK;
 }
 
+bool valid_scale_stride(int64_t s) { return s >= 1 && s < MAX_STRIDE; }
+
+int check_pages(const gqa_fp8_pages* g, Fp8Cache* c) {
+  if (!g || !g->k || !g->v || !g->k_scale || !g->v_scale) return GQA_EINVAL;
+  // bytes as elements of half the size: the same limits, and 16-byte steps
+  gqa_pages b{};
+  b.k = reinterpret_cast<gqa_bf16*>(g->k);
+  b.v = reinterpret_cast<gqa_bf16*>(g->v);
+  b.page_stride = g->page_stride;
+  b.row_stride = g->row_stride;
+  b.head_stride = g->head_stride;
+  b.block_table = g->block_table;
+  b.num_pages = g->num_pages;
+  b.page_size = g->page_size;
+  b.n_kv_heads = g->n_kv_heads;
+  b.table_stride = g->table_stride;
+  b.columns = g->columns;
+  PagedCache p{};
+  const int r = check_pages(&b, &p);
+  if (r != GQA_OK) return r;
+  if (g->page_stride % 16 || g->row_stride % 16 || g->head_stride % 16 || !valid_scale_stride(g->scale_page_stride) ||
+      !valid_scale_stride(g->scale_row_stride) || !valid_scale_stride(g->scale_head_stride))
+    return GQA_EINVAL;
+  *c = {g->k, g->v, g->k_scale, g->v_scale, p.page_stride, p.row_stride, p.head_stride,
+        g->scale_page_stride, g->scale_row_stride, g->scale_head_stride, p.table, p.num_pages, p.page_shift,
+        p.table_stride, p.columns};
+  return GQA_OK;
+}
+
 int check_workspace(const void* ws, size_t bytes) {
   if (!ws) return GQA_EINVAL;
   if (!aligned16(ws)) return GQA_EALIGN;
@@ -87,20 +116,28 @@ Span span_of(const __nv_bfloat16* p, const PagedCache& c, int pages, int rows, i
   return {p, (static_cast<__int128>(pages - 1) * c.page_stride + static_cast<__int128>(n_kv - 1) * c.head_stride +
               HEAD_DIM + static_cast<__int128>(rows - 1) * row_stride) * 2};
 }
-Span span_of_table(const PagedCache& c, int B) {
+// rows of an 8-bit cache and their scales
+Span span_of(const uint8_t* p, long long page_stride, long long row_stride, long long head_stride, int pages, int rows,
+             int n_kv, int width) {
+  return {p, static_cast<__int128>(pages - 1) * page_stride + static_cast<__int128>(rows - 1) * row_stride +
+                 static_cast<__int128>(n_kv - 1) * head_stride + width};
+}
+template <class Cache>
+Span span_of_table(const Cache& c, int B) {
   return span_of(c.table, static_cast<__int128>(B - 1) * c.table_stride + c.columns);
 }
 
-// Whether some row of 128 elements of the key pages and some of the value pages
+// Whether some row of `width` of the key pages and some of the value pages
 // share memory. The two may interleave (both halves of one [pages, 2, ...]
 // tensor, say), so spans do not tell: rows at x page_stride + y row_stride + z
 // head_stride are `d` apart for some |x| < pages, |y| < rows, |z| < heads. Taken
 // from the largest stride down, what is left must be within the smaller
 // strides' reach, so each count is one of two.
-bool pages_meet(const PagedCache& c, int pages, int rows, int n_kv) {
+bool rows_meet(long long between, int width, long long page_stride, int pages, long long row_stride, int rows,
+               long long head_stride, int n_kv) {
   struct Axis {
     long long stride, n;
-  } axes[3] = {{c.page_stride, pages}, {c.row_stride, rows}, {c.head_stride, n_kv}};
+  } axes[3] = {{page_stride, pages}, {row_stride, rows}, {head_stride, n_kv}};
   for (int i = 0; i < 2; ++i)
     for (int j = 0; j < 2 - i; ++j)
       if (axes[j].stride < axes[j + 1].stride) {
@@ -108,7 +145,6 @@ bool pages_meet(const PagedCache& c, int pages, int rows, int n_kv) {
         axes[j] = axes[j + 1];
         axes[j + 1] = x;
       }
-  const long long between = (reinterpret_cast<intptr_t>(c.v) - reinterpret_cast<intptr_t>(c.k)) / 2;
   for (int pick = 0; pick < 8; ++pick) {
     long long d = between;
     for (int i = 0; i < 3; ++i) {
@@ -117,9 +153,34 @@ bool pages_meet(const PagedCache& c, int pages, int rows, int n_kv) {
       x = x > most ? most : x < -most ? -most : x;
       d -= x * s;
     }
-    if (d < HEAD_DIM && d > -HEAD_DIM) return true;
+    if (d < width && d > -width) return true;
   }
   return false;
+}
+long long apart(const void* k, const void* v) { return reinterpret_cast<intptr_t>(v) - reinterpret_cast<intptr_t>(k); }
+bool pages_meet(const PagedCache& c, int pages, int rows, int n_kv) {
+  return rows_meet(apart(c.k, c.v) / 2, HEAD_DIM, c.page_stride, pages, c.row_stride, rows, c.head_stride, n_kv);
+}
+
+// The four tensors of an 8-bit cache.
+struct Fp8Spans {
+  Span s[4];
+  Fp8Spans(const Fp8Cache& c, const gqa_fp8_pages& g)
+      : s{span_of(c.k, c.page_stride, c.row_stride, c.head_stride, g.num_pages, g.page_size, g.n_kv_heads, HEAD_DIM),
+          span_of(c.v, c.page_stride, c.row_stride, c.head_stride, g.num_pages, g.page_size, g.n_kv_heads, HEAD_DIM),
+          span_of(c.k_scale, c.scale_page, c.scale_row, c.scale_head, g.num_pages, g.page_size, g.n_kv_heads, 1),
+          span_of(c.v_scale, c.scale_page, c.scale_row, c.scale_head, g.num_pages, g.page_size, g.n_kv_heads, 1)} {}
+  bool meet(const Span& o) const { return s[0].meets(o) || s[1].meets(o) || s[2].meets(o) || s[3].meets(o); }
+};
+// Whether tensors of an 8-bit cache that is written share memory: values with
+// values, scales with scales by their rows, values with scales by their spans.
+bool pages_meet(const Fp8Cache& c, const gqa_fp8_pages& g, const Fp8Spans& x) {
+  for (int i = 0; i < 2; ++i)
+    if (x.s[i].meets(x.s[2]) || x.s[i].meets(x.s[3])) return true;
+  return (x.s[0].meets(x.s[1]) && rows_meet(apart(c.k, c.v), HEAD_DIM, c.page_stride, g.num_pages, c.row_stride,
+                                            g.page_size, c.head_stride, g.n_kv_heads)) ||
+         (x.s[2].meets(x.s[3]) && rows_meet(apart(c.k_scale, c.v_scale), 1, c.scale_page, g.num_pages, c.scale_row,
+                                            g.page_size, c.scale_head, g.n_kv_heads));
 }
 
 // Whether the output of an attention call shares memory with what it reads.
@@ -149,20 +210,13 @@ bool map_kv(CUtensorMap* m, const void* ptr, int n_kv, long long rows, int pages
   return encode_bf16(m, 4, ptr, dims, strides, box);
 }
 
-}  // namespace
-
-extern "C" {
-
-int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
-                     int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B, const int32_t* start_pos,
-                     const float* rope, int rope_rows, const gqa_pages* pages, gqa_bf16* q_out, void* workspace,
-                     size_t workspace_bytes, void* stream) {
-  PagedAppendParams p{};
-  if (!k || !v || !start_pos || !rope || rope_rows <= 0 || !q != !q_out) return GQA_EINVAL;
-  if (N < 0 || N > MAX_TOKENS || B <= 0 || (!cu_tokens && N != B)) return GQA_EINVAL;
-  int r = check_pages(pages, &p.pages);
-  if (r != GQA_OK) return r;
-  p.n_kv = pages->n_kv_heads;
+// What the appends check and share: everything but the pages that are written.
+int append_args(PagedAppendParams& p, const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride,
+                       const gqa_bf16* v, int64_t v_stride, int N, int n_heads, int n_kv, const int32_t* cu_tokens,
+                       int B, const int32_t* start_pos, const float* rope, int rope_rows, gqa_bf16* q_out,
+                       void* workspace, size_t workspace_bytes) {
+  int r = GQA_OK;
+  p.n_kv = n_kv;
   if (q && (r = check_heads(n_heads, p.n_kv)) != GQA_OK) return r;
   const int64_t kv_row = static_cast<int64_t>(p.n_kv) * HEAD_DIM, q_row = static_cast<int64_t>(n_heads) * HEAD_DIM;
   if (p.n_kv > (1 << 16) || !valid_stride(k_stride, kv_row) || !valid_stride(v_stride, kv_row) ||
@@ -172,27 +226,6 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
       !aligned4(start_pos) || (cu_tokens && !aligned4(cu_tokens)))
     return GQA_EALIGN;
   if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
-  if (N > 0) {
-    // what the call writes: the queries, the key and the value pages
-    const Span written[3] = {
-        span_of(q_out, N, q_row, q_row),
-        span_of(p.pages.k, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride),
-        span_of(p.pages.v, p.pages, pages->num_pages, pages->page_size, p.n_kv, p.pages.row_stride)};
-    const Span read[] = {span_of(k, N, k_stride, kv_row), span_of(v, N, v_stride, kv_row), span_of(start_pos, B),
-                         span_of(cu_tokens, static_cast<__int128>(B) + 1), span_of_table(p.pages, B),
-                         {rope, static_cast<__int128>(rope_rows) * ROPE_PAIRS * 8},
-                         {workspace, GQA_PAGED_WORKSPACE_BYTES}};
-    for (const Span& w : written)
-      for (const Span& r : read)
-        if (w.meets(r)) return GQA_EINVAL;
-    const Span queries = span_of(q, N, q_stride, q_row);
-    if ((q != q_out && written[0].meets(queries)) || written[1].meets(queries) || written[2].meets(queries) ||
-        written[0].meets(written[1]) || written[0].meets(written[2]) ||
-        (written[1].meets(written[2]) && pages_meet(p.pages, pages->num_pages, pages->page_size, p.n_kv)))
-      return GQA_EINVAL;
-  }
-  begin_call();
-  if (N == 0) return GQA_OK;
   p.q = bf(q);
   p.k = bf(k);
   p.v = bf(v);
@@ -208,11 +241,201 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
   p.rope_rows = rope_rows;
   p.q_out = bf(q_out);
   p.status = static_cast<int*>(workspace);
+  return GQA_OK;
+}
+bool append_given(const gqa_bf16* q, const gqa_bf16* k, const gqa_bf16* v, int N, const int32_t* cu_tokens, int B,
+                         const int32_t* start_pos, const float* rope, int rope_rows, const gqa_bf16* q_out) {
+  if (!k || !v || !start_pos || !rope || rope_rows <= 0 || !q != !q_out) return false;
+  return N >= 0 && N <= MAX_TOKENS && B > 0 && (cu_tokens || N == B);
+}
+// Whether something that an append writes (the queries, the spans of the pages)
+// shares memory with what it reads, or the queries with the pages.
+bool append_meets(const PagedAppendParams& p, int n_heads, int pairs, const Span* pages, int n_pages,
+                         const Span& table, const void* workspace) {
+  const int64_t kv_row = static_cast<int64_t>(p.n_kv) * HEAD_DIM, q_row = static_cast<int64_t>(n_heads) * HEAD_DIM;
+  const Span read[] = {{p.k, (static_cast<__int128>(p.N - 1) * p.k_stride + kv_row) * 2},
+                       {p.v, (static_cast<__int128>(p.N - 1) * p.v_stride + kv_row) * 2},
+                       span_of(p.start, p.B),
+                       span_of(p.cu, static_cast<__int128>(p.B) + 1),
+                       table,
+                       {p.rope, static_cast<__int128>(p.rope_rows) * pairs * 8},
+                       {workspace, GQA_PAGED_WORKSPACE_BYTES}};
+  const Span queries{p.q, (static_cast<__int128>(p.N - 1) * p.q_stride + q_row) * 2};
+  const Span q_out{p.q_out, static_cast<__int128>(p.N) * q_row * 2};
+  for (const Span& r : read) {
+    if (q_out.meets(r)) return true;
+    for (int i = 0; i < n_pages; ++i)
+      if (pages[i].meets(r)) return true;
+  }
+  if (p.q != p.q_out && q_out.meets(queries)) return true;
+  for (int i = 0; i < n_pages; ++i)
+    if (pages[i].meets(queries) || pages[i].meets(q_out)) return true;
+  return false;
+}
+bool append_meets(const PagedAppendParams& p, int n_heads, int pairs, const gqa_pages& g, const void* workspace) {
+  const Span pages[2] = {span_of(p.pages.k, p.pages, g.num_pages, g.page_size, p.n_kv, p.pages.row_stride),
+                         span_of(p.pages.v, p.pages, g.num_pages, g.page_size, p.n_kv, p.pages.row_stride)};
+  return append_meets(p, n_heads, pairs, pages, 2, span_of_table(p.pages, p.B), workspace) ||
+         (pages[0].meets(pages[1]) && pages_meet(p.pages, g.num_pages, g.page_size, p.n_kv));
+}
+// A part of a head is whole 16-byte pieces in both layouts.
+bool valid_rotary(int rotary_dim) { return rotary_dim >= 16 && rotary_dim <= HEAD_DIM && rotary_dim % 16 == 0; }
+template <class Launch>
+int one_launch(void* stream, Launch launch) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(0, s);
-  r = launched(launch_paged_append(p, s));
+  const int r = launched(launch(s));
   prof_mark(1, s);
   return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                     int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B, const int32_t* start_pos,
+                     const float* rope, int rope_rows, const gqa_pages* pages, gqa_bf16* q_out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  PagedAppendParams p{};
+  if (!append_given(q, k, v, N, cu_tokens, B, start_pos, rope, rope_rows, q_out)) return GQA_EINVAL;
+  int r = check_pages(pages, &p.pages);
+  if (r == GQA_OK)
+    r = append_args(p, q, q_stride, k, k_stride, v, v_stride, N, n_heads, pages->n_kv_heads, cu_tokens, B, start_pos,
+                    rope, rope_rows, q_out, workspace, workspace_bytes);
+  if (r != GQA_OK) return r;
+  if (N > 0 && append_meets(p, n_heads, ROPE_PAIRS, *pages, workspace)) return GQA_EINVAL;
+  begin_call();
+  if (N == 0) return GQA_OK;
+  return one_launch(stream, [&](cudaStream_t s) { return launch_paged_append(p, s); });
+}
+
+int gqa_paged_append_rotary(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                            int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
+                            const int32_t* start_pos, const float* rope, int rope_rows, int rotary_dim, int halves,
+                            const gqa_pages* pages, gqa_bf16* q_out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  RotaryAppendParams p{};
+  if (!append_given(q, k, v, N, cu_tokens, B, start_pos, rope, rope_rows, q_out) || !valid_rotary(rotary_dim))
+    return GQA_EINVAL;
+  int r = check_pages(pages, &p.a.pages);
+  if (r == GQA_OK)
+    r = append_args(p.a, q, q_stride, k, k_stride, v, v_stride, N, n_heads, pages->n_kv_heads, cu_tokens, B, start_pos,
+                    rope, rope_rows, q_out, workspace, workspace_bytes);
+  if (r != GQA_OK) return r;
+  if (N > 0 && append_meets(p.a, n_heads, rotary_dim / 2, *pages, workspace)) return GQA_EINVAL;
+  begin_call();
+  if (N == 0) return GQA_OK;
+  p.rotary_dim = rotary_dim;
+  p.halves = halves != 0;
+  return one_launch(stream, [&](cudaStream_t s) { return launch_rotary_append(p, s); });
+}
+
+int gqa_paged_append_fp8(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                         int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
+                         const int32_t* start_pos, const float* rope, int rope_rows, int rotary_dim, int halves,
+                         const gqa_fp8_pages* pages, gqa_bf16* q_out, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  RotaryAppendParams p{};
+  if (!append_given(q, k, v, N, cu_tokens, B, start_pos, rope, rope_rows, q_out) || !valid_rotary(rotary_dim))
+    return GQA_EINVAL;
+  int r = check_pages(pages, &p.pages8);
+  if (r == GQA_OK)
+    r = append_args(p.a, q, q_stride, k, k_stride, v, v_stride, N, n_heads, pages->n_kv_heads, cu_tokens, B, start_pos,
+                    rope, rope_rows, q_out, workspace, workspace_bytes);
+  if (r != GQA_OK) return r;
+  if (N > 0) {
+    const Fp8Spans spans(p.pages8, *pages);
+    if (append_meets(p.a, n_heads, rotary_dim / 2, spans.s, 4, span_of_table(p.pages8, B), workspace) ||
+        pages_meet(p.pages8, *pages, spans))
+      return GQA_EINVAL;
+  }
+  begin_call();
+  if (N == 0) return GQA_OK;
+  p.rotary_dim = rotary_dim;
+  p.halves = halves != 0;
+  p.fp8 = 1;
+  return one_launch(stream, [&](cudaStream_t s) { return launch_rotary_append(p, s); });
+}
+
+int gqa_paged_read_fp8(const int32_t* rows, int B, const gqa_fp8_pages* from, const gqa_pages* to, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  Fp8ReadParams p{};
+  if (!rows || B <= 0 || B > PAGED_MAX_SEQS) return GQA_EINVAL;
+  int r = check_pages(from, &p.from);
+  if (r == GQA_OK) r = check_pages(to, &p.to);
+  if (r != GQA_OK) return r;
+  if (from->n_kv_heads != to->n_kv_heads || from->n_kv_heads > (1 << 16)) return GQA_EINVAL;
+  // units of 16 positions are counted in 31 bits
+  const long long most = static_cast<long long>(from->columns) * from->page_size;
+  const long long most_to = static_cast<long long>(to->columns) * to->page_size;
+  if ((most < most_to ? most : most_to) / 16 * B > 0x7fffffffLL) return GQA_EINVAL;
+  if (!aligned4(rows)) return GQA_EALIGN;
+  if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
+  const Span written[2] = {span_of(p.to.k, p.to, to->num_pages, to->page_size, to->n_kv_heads, p.to.row_stride),
+                           span_of(p.to.v, p.to, to->num_pages, to->page_size, to->n_kv_heads, p.to.row_stride)};
+  const Fp8Spans spans(p.from, *from);
+  const Span read[] = {span_of(rows, B), span_of_table(p.from, B), span_of_table(p.to, B),
+                       {workspace, GQA_PAGED_WORKSPACE_BYTES}};
+  for (const Span& w : written) {
+    if (spans.meet(w)) return GQA_EINVAL;
+    for (const Span& x : read)
+      if (w.meets(x)) return GQA_EINVAL;
+  }
+  if (written[0].meets(written[1]) && pages_meet(p.to, to->num_pages, to->page_size, to->n_kv_heads)) return GQA_EINVAL;
+  p.B = B;
+  p.n_kv = from->n_kv_heads;
+  p.rows = rows;
+  p.status = static_cast<int*>(workspace);
+  p.ctas = launch_sms();
+  begin_call();
+  return one_launch(stream, [&](cudaStream_t s) { return launch_fp8_read(p, s); });
+}
+
+int gqa_paged_decode_fp8(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                         const gqa_fp8_pages* pages, float scale, gqa_bf16* out, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  Fp8DecodeParams p{};
+  if (!q || !start_pos || !out || B <= 0 || B > PAGED_MAX_SEQS) return GQA_EINVAL;
+  int r = check_pages(pages, &p.pages);
+  if (r == GQA_OK) r = check_heads(n_heads, pages->n_kv_heads);
+  if (r == GQA_OK) r = check_scale(scale);
+  if (r != GQA_OK) return r;
+  if (!valid_stride(q_stride, static_cast<int64_t>(n_heads) * HEAD_DIM)) return GQA_EINVAL;
+  // the batch's chunks of 32 positions and one KV head are counted in 31 bits
+  if ((p.pages.columns * static_cast<long long>(pages->page_size) / 32 + 1) * B * pages->n_kv_heads > 0x7fffffffLL)
+    return GQA_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(start_pos)) return GQA_EALIGN;
+  if ((r = check_workspace(workspace, workspace_bytes)) != GQA_OK) return r;
+  const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
+  const Span o = span_of(out, B, row, row);
+  if (o.meets(span_of(q, B, q_stride, row)) || Fp8Spans(p.pages, *pages).meet(o) || o.meets(span_of(start_pos, B)) ||
+      o.meets(span_of_table(p.pages, B)) || o.meets({workspace, GQA_PAGED_WORKSPACE_BYTES}))
+    return GQA_EINVAL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.q = bf(q);
+  p.q_stride = q_stride;
+  p.B = B;
+  p.n_heads = n_heads;
+  p.n_kv = pages->n_kv_heads;
+  p.start = start_pos;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = bf(out);
+  p.tickets = reinterpret_cast<int*>(ws + TICKETS_OFFSET);
+  p.part_ml = reinterpret_cast<float*>(ws + PART_ML_OFFSET);
+  p.part_o = reinterpret_cast<float*>(ws + PART_O_OFFSET);
+  p.status = reinterpret_cast<int*>(ws);
+  p.ctas = launch_sms();
+  Fp8DecodeMaps maps;
+  const cuuint64_t dims[4] = {HEAD_DIM, static_cast<cuuint64_t>(p.n_kv), static_cast<cuuint64_t>(pages->page_size),
+                              static_cast<cuuint64_t>(pages->num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.pages.head_stride), static_cast<cuuint64_t>(p.pages.row_stride),
+                                 static_cast<cuuint64_t>(p.pages.page_stride)};
+  const cuuint32_t box[4] = {HEAD_DIM, 1, static_cast<cuuint32_t>(fp8_decode_box_rows(pages->page_size)), 1};
+  if (!encode_bytes(&maps.k, 4, p.pages.k, dims, strides, box) || !encode_bytes(&maps.v, 4, p.pages.v, dims, strides, box))
+    return fail_cuda(cudaErrorInvalidValue);
+  begin_call();
+  return one_launch(stream, [&](cudaStream_t s) { return launch_paged_decode_fp8(maps, p, s); });
 }
 
 int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,

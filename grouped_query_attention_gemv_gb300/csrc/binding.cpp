@@ -31,6 +31,7 @@ const char* type_name(at::ScalarType t) {
     case at::kBFloat16: return "must be torch.bfloat16";
     case at::kInt: return "must be torch.int32";
     case at::kFloat: return "must be torch.float32";
+    case at::kFloat8_e4m3fn: return "must be torch.float8_e4m3fn";
     default: return "must be torch.uint8";
   }
 }
@@ -103,36 +104,79 @@ const int32_t* ints(PyObject* o, const char* name, int64_t n, const Device& d, i
   return static_cast<const int32_t*>(t.data_ptr());
 }
 
-gqa_pages pages(PyObject* k_, PyObject* v_, PyObject* table_, int64_t B, const Device& d) {
-  const at::Tensor& k = tensor(k_, "k_pages", at::kBFloat16);
-  const at::Tensor& v = tensor(v_, "v_pages", at::kBFloat16);
-  const at::Tensor& t = tensor(table_, "block_table", at::kInt);
-  if (k.dim() != 4 || k.size(3) != DIM) refuse(PyExc_ValueError, "k_pages", "must be [pages, page_size, n_kv, 128]");
-  if (v.sizes() != k.sizes() || v.strides() != k.strides())
-    refuse(PyExc_ValueError, "v_pages", "must have the shape and the strides of k_pages");
-  if (k.stride(3) != 1) refuse(PyExc_ValueError, "k_pages", "must have a head's 128 elements one after the other");
+// The pages of k or of v by their common shape and strides, the table.
+struct Pages {
+  const at::Tensor &k, &v, &table;
+  int64_t stride(int axis) const { return k.size(axis) > 1 ? k.stride(axis) : DIM; }
+  template <class C>
+  void put(C& g, int64_t B) const {
+    g.page_stride = stride(0);
+    g.row_stride = stride(1);
+    g.head_stride = stride(2);
+    g.block_table = static_cast<const int32_t*>(table.data_ptr());
+    g.num_pages = static_cast<int>(k.size(0));
+    g.page_size = static_cast<int>(k.size(1));
+    g.n_kv_heads = static_cast<int>(k.size(2));
+    g.columns = static_cast<int>(table.size(1));
+    g.table_stride = B > 1 ? static_cast<int>(table.stride(0)) : g.columns;
+  }
+};
+struct PageNames {
+  const char *k, *v, *table;
+};
+Pages page_tensors(PyObject* k_, PyObject* v_, PyObject* table_, int64_t B, const Device& d, at::ScalarType type,
+                   const PageNames& names) {
+  const at::Tensor& k = tensor(k_, names.k, type);
+  const at::Tensor& v = tensor(v_, names.v, type);
+  const at::Tensor& t = tensor(table_, names.table, at::kInt);
+  if (k.dim() != 4 || k.size(3) != DIM) refuse(PyExc_ValueError, names.k, "must be [pages, page_size, n_kv, 128]");
+  if (v.sizes() != k.sizes() || v.strides() != k.strides()) {
+    PyErr_Format(PyExc_ValueError, "%s must have the shape and the strides of %s", names.v, names.k);
+    throw Refused();
+  }
+  if (k.stride(3) != 1) refuse(PyExc_ValueError, names.k, "must have a head's 128 elements one after the other");
   if (t.dim() != 2 || t.size(0) != B || (t.size(1) > 1 && t.stride(1) != 1)) {
-    PyErr_Format(PyExc_ValueError, "block_table must be [%lld, columns] with adjacent columns", (long long)B);
+    PyErr_Format(PyExc_ValueError, "%s must be [%lld, columns] with adjacent columns", names.table, (long long)B);
     throw Refused();
   }
   for (int i = 0; i < 3; ++i)
-    if (k.size(i) > INT32_MAX) refuse(PyExc_ValueError, "k_pages", "is too large");
-  if (t.size(1) > INT32_MAX || t.stride(0) > INT32_MAX) refuse(PyExc_ValueError, "block_table", "is too wide");
-  d.same(k, "k_pages");
-  d.same(v, "v_pages");
-  d.same(t, "block_table");
+    if (k.size(i) > INT32_MAX) refuse(PyExc_ValueError, names.k, "is too large");
+  if (t.size(1) > INT32_MAX || t.stride(0) > INT32_MAX) refuse(PyExc_ValueError, names.table, "is too wide");
+  d.same(k, names.k);
+  d.same(v, names.v);
+  d.same(t, names.table);
+  return {k, v, t};
+}
+
+gqa_pages pages(PyObject* k, PyObject* v, PyObject* table, int64_t B, const Device& d,
+                const PageNames& names = {"k_pages", "v_pages", "block_table"}) {
+  const Pages p = page_tensors(k, v, table, B, d, at::kBFloat16, names);
   gqa_pages g;
-  g.k = static_cast<gqa_bf16*>(k.data_ptr());
-  g.v = static_cast<gqa_bf16*>(v.data_ptr());
-  g.page_stride = k.size(0) > 1 ? k.stride(0) : DIM;
-  g.row_stride = k.size(1) > 1 ? k.stride(1) : DIM;
-  g.head_stride = k.size(2) > 1 ? k.stride(2) : DIM;
-  g.block_table = static_cast<const int32_t*>(t.data_ptr());
-  g.num_pages = static_cast<int>(k.size(0));
-  g.page_size = static_cast<int>(k.size(1));
-  g.n_kv_heads = static_cast<int>(k.size(2));
-  g.columns = static_cast<int>(t.size(1));
-  g.table_stride = B > 1 ? static_cast<int>(t.stride(0)) : g.columns;
+  g.k = static_cast<gqa_bf16*>(p.k.data_ptr());
+  g.v = static_cast<gqa_bf16*>(p.v.data_ptr());
+  p.put(g, B);
+  return g;
+}
+
+gqa_fp8_pages fp8_pages(PyObject* k, PyObject* v, PyObject* ks_, PyObject* vs_, PyObject* table, int64_t B,
+                        const Device& d) {
+  const Pages p = page_tensors(k, v, table, B, d, at::kFloat8_e4m3fn, {"k_pages", "v_pages", "block_table"});
+  const at::Tensor& ks = tensor(ks_, "k_scales", at::kByte);
+  const at::Tensor& vs = tensor(vs_, "v_scales", at::kByte);
+  if (ks.dim() != 3 || ks.size(0) != p.k.size(0) || ks.size(1) != p.k.size(1) || ks.size(2) != p.k.size(2))
+    refuse(PyExc_ValueError, "k_scales", "must be [pages, page_size, n_kv] like k_pages");
+  if (vs.sizes() != ks.sizes() || vs.strides() != ks.strides())
+    refuse(PyExc_ValueError, "v_scales", "must have the shape and the strides of k_scales");
+  d.same(ks, "k_scales");
+  d.same(vs, "v_scales");
+  gqa_fp8_pages g;
+  g.k = static_cast<uint8_t*>(p.k.data_ptr());
+  g.v = static_cast<uint8_t*>(p.v.data_ptr());
+  g.k_scale = static_cast<uint8_t*>(ks.data_ptr());
+  g.v_scale = static_cast<uint8_t*>(vs.data_ptr());
+  int64_t* strides[3] = {&g.scale_page_stride, &g.scale_row_stride, &g.scale_head_stride};
+  for (int i = 0; i < 3; ++i) *strides[i] = ks.size(i) > 1 ? ks.stride(i) : 1;
+  p.put(g, B);
   return g;
 }
 
@@ -176,43 +220,140 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return nullptr;
 }
 
-// q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens, q_out, workspace, stream
-int paged_append(PyObject* const* a) {
-  const at::Tensor& kt = tensor(a[1], "k", at::kBFloat16);
+int number_of(PyObject* o, const char* name) {
+  const long x = PyLong_AsLong(o);
+  if (x == -1 && PyErr_Occurred()) throw Refused();
+  if (x < INT32_MIN || x > INT32_MAX) refuse(PyExc_ValueError, name, "is out of range");
+  return static_cast<int>(x);
+}
+
+// The tokens of an append: q, k, v, start_pos, rope, cu_tokens, q_out.
+struct Tokens {
+  Device d;
+  Rows q, k, v;
+  int64_t B;
+  const int32_t *start, *cu;
+  const float* rope;
+  int rope_rows;
+};
+Tokens tokens(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* start_, PyObject* rope_, PyObject* cu_, int rotary_dim) {
+  const at::Tensor& kt = tensor(k_, "k", at::kBFloat16);
   const Device d{kt.device()};
   const Rows k = rows(kt, "k");
-  const at::Tensor& vt = tensor(a[2], "v", at::kBFloat16);
+  const at::Tensor& vt = tensor(v_, "v", at::kBFloat16);
   d.same(vt, "v");
   const Rows v = rows(vt, "v", k.n, k.heads);
   int64_t B = 0;
-  const int32_t* start = ints(a[3], "start_pos", -1, d, &B);
-  const int32_t* cu = a[8] == Py_None ? nullptr : ints(a[8], "cu_tokens", B + 1, d);
+  const int32_t* start = ints(start_, "start_pos", -1, d, &B);
+  const int32_t* cu = cu_ == Py_None ? nullptr : ints(cu_, "cu_tokens", B + 1, d);
   if (!cu && B != k.n) refuse(PyExc_ValueError, "start_pos", "must have one value per token without cu_tokens");
-  const at::Tensor& rope = tensor(a[4], "rope", at::kFloat);
-  if (rope.dim() != 3 || rope.size(1) != 64 || rope.size(2) != 2 || !rope.is_contiguous())
-    refuse(PyExc_ValueError, "rope", "must be a contiguous [rows, 64, 2] tensor");
+  const at::Tensor& rope = tensor(rope_, "rope", at::kFloat);
+  if (rope.dim() != 3 || rope.size(1) != rotary_dim / 2 || rope.size(2) != 2 || !rope.is_contiguous()) {
+    PyErr_Format(PyExc_ValueError, "rope must be a contiguous [rows, %d, 2] tensor", rotary_dim / 2);
+    throw Refused();
+  }
   if (rope.size(0) > INT32_MAX) refuse(PyExc_ValueError, "rope", "has too many rows");
   d.same(rope, "rope");
-  const gqa_pages g = pages(a[5], a[6], a[7], B, d);
-  if (g.n_kv_heads != k.heads) refuse(PyExc_ValueError, "k", "must have the KV heads of the pages");
-  Rows q{nullptr, 0, 0, 0};
+  return {d, {nullptr, 0, 0, 0}, k, v, B, start, cu, static_cast<const float*>(rope.data_ptr()),
+          static_cast<int>(rope.size(0))};
+}
+// q and q_out, the last of them to be looked at
+gqa_bf16* queries(Tokens& t, PyObject* q_, PyObject* q_out_, int n_kv) {
+  if (n_kv != t.k.heads) refuse(PyExc_ValueError, "k", "must have the KV heads of the pages");
   gqa_bf16* q_out = nullptr;
-  if (a[0] != Py_None) {
-    const at::Tensor& qt = tensor(a[0], "q", at::kBFloat16);
-    d.same(qt, "q");
-    q = rows(qt, "q", k.n);
-    q_out = output(a[9], "q_out", k.n, q.heads, d);
-  } else if (a[9] != Py_None) {
+  if (q_ != Py_None) {
+    const at::Tensor& qt = tensor(q_, "q", at::kBFloat16);
+    t.d.same(qt, "q");
+    t.q = rows(qt, "q", t.k.n);
+    q_out = output(q_out_, "q_out", t.k.n, t.q.heads, t.d);
+  } else if (q_out_ != Py_None) {
     refuse(PyExc_ValueError, "q_out", "needs q");
   }
-  d.cuda("k");
-  const Workspace w = workspace(a[10], d);
-  if (k.n == 0) return GQA_OK;
+  t.d.cuda("k");
+  return q_out;
+}
+
+// q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens, q_out, workspace, stream
+int paged_append(PyObject* const* a) {
+  Tokens t = tokens(a[0], a[1], a[2], a[3], a[4], a[8], DIM);
+  const gqa_pages g = pages(a[5], a[6], a[7], t.B, t.d);
+  gqa_bf16* q_out = queries(t, a[0], a[9], g.n_kv_heads);
+  const Workspace w = workspace(a[10], t.d);
+  if (t.k.n == 0) return GQA_OK;
+  const c10::cuda::CUDAGuard guard(t.d.d);
+  return gqa_paged_append(t.q.p, t.q.stride, t.k.p, t.k.stride, t.v.p, t.v.stride, static_cast<int>(t.k.n),
+                          static_cast<int>(t.q.heads), t.cu, static_cast<int>(t.B), t.start, t.rope, t.rope_rows, &g,
+                          q_out, w.p, w.bytes, stream(a[11], t.d));
+}
+
+int rotary(PyObject* o) {
+  const int r = number_of(o, "rotary_dim");
+  if (r < 16 || r > DIM || r % 16) refuse(PyExc_ValueError, "rotary_dim", "must be a multiple of 16, 16 to 128");
+  return r;
+}
+
+// q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tokens, q_out, rotary_dim, halves, workspace, stream
+int paged_append_rotary(PyObject* const* a) {
+  const int dim = rotary(a[10]), halves = PyObject_IsTrue(a[11]);
+  if (halves < 0) throw Refused();
+  Tokens t = tokens(a[0], a[1], a[2], a[3], a[4], a[8], dim);
+  const gqa_pages g = pages(a[5], a[6], a[7], t.B, t.d);
+  gqa_bf16* q_out = queries(t, a[0], a[9], g.n_kv_heads);
+  const Workspace w = workspace(a[12], t.d);
+  if (t.k.n == 0) return GQA_OK;
+  const c10::cuda::CUDAGuard guard(t.d.d);
+  return gqa_paged_append_rotary(t.q.p, t.q.stride, t.k.p, t.k.stride, t.v.p, t.v.stride, static_cast<int>(t.k.n),
+                                 static_cast<int>(t.q.heads), t.cu, static_cast<int>(t.B), t.start, t.rope,
+                                 t.rope_rows, dim, halves, &g, q_out, w.p, w.bytes, stream(a[13], t.d));
+}
+
+// q, k, v, start_pos, rope, k_pages, v_pages, k_scales, v_scales, block_table, cu_tokens, q_out, rotary_dim, halves,
+// workspace, stream
+int paged_append_fp8(PyObject* const* a) {
+  const int dim = rotary(a[12]), halves = PyObject_IsTrue(a[13]);
+  if (halves < 0) throw Refused();
+  Tokens t = tokens(a[0], a[1], a[2], a[3], a[4], a[10], dim);
+  const gqa_fp8_pages g = fp8_pages(a[5], a[6], a[7], a[8], a[9], t.B, t.d);
+  gqa_bf16* q_out = queries(t, a[0], a[11], g.n_kv_heads);
+  const Workspace w = workspace(a[14], t.d);
+  if (t.k.n == 0) return GQA_OK;
+  const c10::cuda::CUDAGuard guard(t.d.d);
+  return gqa_paged_append_fp8(t.q.p, t.q.stride, t.k.p, t.k.stride, t.v.p, t.v.stride, static_cast<int>(t.k.n),
+                              static_cast<int>(t.q.heads), t.cu, static_cast<int>(t.B), t.start, t.rope, t.rope_rows,
+                              dim, halves, &g, q_out, w.p, w.bytes, stream(a[15], t.d));
+}
+
+// rows, k_pages, v_pages, k_scales, v_scales, block_table, k_out, v_out, out_table, workspace, stream
+int paged_read_fp8(PyObject* const* a) {
+  const at::Tensor& rt = tensor(a[0], "rows", at::kInt);
+  const Device d{rt.device()};
+  int64_t B = 0;
+  const int32_t* n = ints(a[0], "rows", -1, d, &B);
+  const gqa_fp8_pages from = fp8_pages(a[1], a[2], a[3], a[4], a[5], B, d);
+  const gqa_pages to = pages(a[6], a[7], a[8], B, d, {"k_out", "v_out", "out_table"});
+  if (to.n_kv_heads != from.n_kv_heads) refuse(PyExc_ValueError, "k_out", "must have the KV heads of k_pages");
+  d.cuda("rows");
+  const Workspace w = workspace(a[9], d);
+  if (B == 0) return GQA_OK;
   const c10::cuda::CUDAGuard guard(d.d);
-  return gqa_paged_append(q.p, q.stride, k.p, k.stride, v.p, v.stride, static_cast<int>(k.n),
-                          static_cast<int>(q.heads), cu, static_cast<int>(B), start,
-                          static_cast<const float*>(rope.data_ptr()), static_cast<int>(rope.size(0)), &g, q_out, w.p,
-                          w.bytes, stream(a[11], d));
+  return gqa_paged_read_fp8(n, static_cast<int>(B), &from, &to, w.p, w.bytes, stream(a[10], d));
+}
+
+// q, start_pos, k_pages, v_pages, k_scales, v_scales, block_table, scale, out, workspace, stream
+int paged_decode_fp8(PyObject* const* a) {
+  const at::Tensor& qt = tensor(a[0], "q", at::kBFloat16);
+  const Device d{qt.device()};
+  const Rows q = rows(qt, "q");
+  const int32_t* start = ints(a[1], "start_pos", q.n, d);
+  const gqa_fp8_pages g = fp8_pages(a[2], a[3], a[4], a[5], a[6], q.n, d);
+  const float scale = number(a[7]);
+  gqa_bf16* out = output(a[8], "out", q.n, q.heads, d);
+  d.cuda("q");
+  const Workspace w = workspace(a[9], d);
+  if (q.n == 0) return GQA_OK;
+  const c10::cuda::CUDAGuard guard(d.d);
+  return gqa_paged_decode_fp8(q.p, q.stride, static_cast<int>(q.n), static_cast<int>(q.heads), start, &g, scale, out,
+                              w.p, w.bytes, stream(a[10], d));
 }
 
 // q, start_pos, k_pages, v_pages, block_table, scale, out, workspace, stream
@@ -283,6 +424,10 @@ PyCFunction fast() {
 
 PyMethodDef methods[] = {
     {"paged_append", fast<12, paged_append>(), METH_FASTCALL, nullptr},
+    {"paged_append_rotary", fast<14, paged_append_rotary>(), METH_FASTCALL, nullptr},
+    {"paged_append_fp8", fast<16, paged_append_fp8>(), METH_FASTCALL, nullptr},
+    {"paged_read_fp8", fast<11, paged_read_fp8>(), METH_FASTCALL, nullptr},
+    {"paged_decode_fp8", fast<11, paged_decode_fp8>(), METH_FASTCALL, nullptr},
     {"paged_decode", fast<9, paged_decode>(), METH_FASTCALL, nullptr},
     {"paged_prefill", fast<10, paged_prefill>(), METH_FASTCALL, nullptr},
     {"packed_prefill", fast<8, packed_prefill>(), METH_FASTCALL, nullptr},

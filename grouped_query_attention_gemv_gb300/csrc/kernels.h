@@ -243,7 +243,7 @@ int decode_fused_np(int M);   // padded tokens of the fused grid's projections (
 cudaError_t launch_rmsnorm(const __nv_bfloat16* x, const __nv_bfloat16* g, float eps, int M, __nv_bfloat16* y,
                            cudaStream_t s);
 
-cudaError_t launch_rope_table(float* rope, int rows, double theta, int scaled, double factor, double lo,
+cudaError_t launch_rope_table(float* rope, int rows, int dim, double theta, int scaled, double factor, double lo,
                               double hi, double ctx, cudaStream_t s);
 
 }  // namespace gqa

@@ -42,6 +42,17 @@ struct PagedCache {
   __device__ __forceinline__ long long capacity() const { return static_cast<long long>(columns) << page_shift; }
 };
 
+// A paged cache in 8 bits (gqa_fp8_pages): rows of 128 e4m3 values, a byte
+// beside each row that holds its exponent + 127.
+struct Fp8Cache {
+  uint8_t *k, *v, *k_scale, *v_scale;
+  long long page_stride, row_stride, head_stride;        // values
+  long long scale_page, scale_row, scale_head;           // scales
+  const int* table;
+  int num_pages, page_shift, table_stride, columns;
+  __device__ __forceinline__ long long capacity() const { return static_cast<long long>(columns) << page_shift; }
+};
+
 // 16 bytes global -> shared, asynchronously; zeros when `bytes` is 0 (src is
 // then not read).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -80,6 +91,27 @@ struct PagedAppendParams {
 };
 cudaError_t launch_paged_append(const PagedAppendParams& p, cudaStream_t s);
 
+// The same in any rotary layout: dims 0 .. rotary_dim - 1 of a head are turned,
+// as pairs (2i, 2i + 1) or, with `halves`, (i, i + rotary_dim / 2); rope rows
+// are rotary_dim / 2 pairs. Into `pages`, or with `fp8` set into `pages8`.
+struct RotaryAppendParams {
+  PagedAppendParams a;
+  int rotary_dim, halves, fp8;
+  Fp8Cache pages8;
+};
+cudaError_t launch_rotary_append(const RotaryAppendParams& p, cudaStream_t s);
+
+// Rows 0 .. rows[b] - 1 of sequences from 8-bit pages into bf16 pages.
+struct Fp8ReadParams {
+  int B, n_kv;
+  const int* rows;
+  Fp8Cache from;
+  PagedCache to;
+  int* status;
+  int ctas;
+};
+cudaError_t launch_fp8_read(const Fp8ReadParams& p, cudaStream_t s);
+
 // One new token per sequence over the pages.
 struct PagedDecodeParams {
   const __nv_bfloat16* q;
@@ -96,6 +128,27 @@ struct PagedDecodeParams {
   int ctas;
 };
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s);
+
+// The same over 8-bit pages. k, v: (dim, KV head, row, page), boxes of 128 dims
+// x 1 head x fp8_decode_box_rows(page) rows.
+struct Fp8DecodeParams {
+  const __nv_bfloat16* q;
+  long long q_stride;
+  int B, n_heads, n_kv;
+  const int* start;
+  Fp8Cache pages;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float *part_o, *part_ml;  // as in PagedDecodeParams
+  int* tickets;
+  int* status;
+  int ctas;
+};
+struct Fp8DecodeMaps {
+  CUtensorMap k, v;
+};
+int fp8_decode_box_rows(int page_size);
+cudaError_t launch_paged_decode_fp8(const Fp8DecodeMaps& maps, const Fp8DecodeParams& p, cudaStream_t s);
 
 // Causal attention of packed tokens; keys and values packed (cu gives their
 // rows too) or in the pages.

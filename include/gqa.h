@@ -102,6 +102,11 @@ int gqa_rope_table(float* rope, int rows, double theta, int scaled, double facto
                    double low_freq_factor, double high_freq_factor,
                    double original_context, void* stream);
 
+/* The same for heads of which the first rotary_dim dims (even, 2 to 128) are
+ * turned: [rows, rotary_dim / 2, 2], f_i = theta^(-2i/rotary_dim). */
+int gqa_rope_table_dim(float* rope, int rows, int rotary_dim, double theta, int scaled, double factor,
+                       double low_freq_factor, double high_freq_factor, double original_context, void* stream);
+
 /* The block for one batch with a common start position (the pages'
  * forward(x, start_pos, freqs_cis, mask)).
  *   x        [B, T, 4096] bf16, the (normalised) block input
@@ -420,6 +425,60 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
                      const float* rope, int rope_rows, const gqa_pages* pages, gqa_bf16* q_out, void* workspace,
                      size_t workspace_bytes, void* stream);
 
+/* gqa_paged_append for other rotary layouts. The first rotary_dim of the 128
+ * dims of a head are turned (a multiple of 16, 16 to 128), the others are kept:
+ * dims (2i, 2i + 1) by row pair i, or with `halves` non-zero dims (i, i +
+ * rotary_dim / 2).
+ *   rope  [rope_rows, rotary_dim / 2, 2], 16-byte aligned (gqa_rope_table_dim)
+ * Products and sums of the rotation are rounded to fp32 one by one, the result
+ * once to bf16. */
+int gqa_paged_append_rotary(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                            int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
+                            const int32_t* start_pos, const float* rope, int rope_rows, int rotary_dim, int halves,
+                            const gqa_pages* pages, gqa_bf16* q_out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* A paged cache in 8 bits. Row r of page p for KV head g is 128 e4m3 bytes at
+ * p * page_stride + r * row_stride + g * head_stride of k and of v (16-byte
+ * aligned, strides multiples of 16), and one byte at p * scale_page_stride + r *
+ * scale_row_stride + g * scale_head_stride of k_scale and of v_scale (strides
+ * of 1 at least): the row's exponent + 127. A value is its e4m3 times
+ * 2^exponent. The exponent is the least integer in [-100, 120] with |x| <= 448 *
+ * 2^exponent for all finite x of the row, so that the one rounding is that to
+ * e4m3 (ties to even), and reading back is exact. What is not finite is held
+ * as NaN. The rest as in gqa_pages. Values and scales lie in memory of their
+ * own (k and v may interleave, and k_scale and v_scale). */
+typedef struct gqa_fp8_pages {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t page_stride, row_stride, head_stride;
+  int64_t scale_page_stride, scale_row_stride, scale_head_stride;
+  const int32_t* block_table;
+  int num_pages, page_size, n_kv_heads;
+  int table_stride, columns;
+} gqa_fp8_pages;
+
+/* gqa_paged_append_rotary into 8-bit pages: keys are quantised from their
+ * rotation in fp32, values from their bf16. */
+int gqa_paged_append_fp8(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int64_t k_stride, const gqa_bf16* v,
+                         int64_t v_stride, int N, int n_heads, const int32_t* cu_tokens, int B,
+                         const int32_t* start_pos, const float* rope, int rope_rows, int rotary_dim, int halves,
+                         const gqa_fp8_pages* pages, gqa_bf16* q_out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Reads cache rows 0..rows[b]-1 of every sequence (rows: device int32 [B]; 0 or
+ * -1: none) from 8-bit pages into bf16 pages, exactly; the two caches have the
+ * same KV heads, and page sizes and tables of their own. Other rows of `to`
+ * are left as they were. No two rows may share a row of `to`. More rows than
+ * either table holds, and counts below -1, are reported as
+ * GQA_DEV_BAD_POSITION. For gqa_paged_prefill after a quantised prefix, for
+ * instance. At most GQA_PAGED_MAX_SEQS sequences; the smaller table's
+ * positions / 16 * B must stay below 2^31. */
+int gqa_paged_read_fp8(const int32_t* rows, int B, const gqa_fp8_pages* from, const gqa_pages* to, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Attention of one new token per sequence over the paged cache: for every
  * query head, softmax(scale q K^T) V over cache rows 0..start_pos[b] (row
  * start_pos[b] is the token's own, appended before). start_pos[b] = -1: the
@@ -434,6 +493,15 @@ int gqa_paged_append(const gqa_bf16* q, int64_t q_stride, const gqa_bf16* k, int
 int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
                      const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes,
                      void* stream);
+
+/* gqa_paged_decode over 8-bit pages. (columns * page_size / 32 + 1) * B *
+ * n_kv_heads must stay below 2^31, else GQA_EINVAL.
+ * Queries enter the products as f16 times a power of two per head (their 8 bits
+ * kept down to 2^-28 of the head's largest), probabilities times the value
+ * rows' scales as f16 (11 bits down to 2^-29 of the largest such term). */
+int gqa_paged_decode_fp8(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                         const gqa_fp8_pages* pages, float scale, gqa_bf16* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /* Causal attention of packed new tokens over the paged cache, which already
  * holds them: token i of sequence b reads rows 0..start_pos[b] + i. Whole
