@@ -12,7 +12,9 @@ entries ``block_forward_host`` / ``decode_host`` (with ``make_host_stage``,
 ``host_stage_wait``, ``release_host_stage``), ``decode_static``,
 ``rope_table``, ``workspace_bytes``, ``device_status``, ``last_launch_count``;
 and the serving operators over a paged cache ``paged_append`` /
-``paged_decode`` / ``paged_prefill`` / ``packed_prefill`` (with
+``paged_decode`` / ``paged_prefill`` / ``packed_prefill``, over one in 8 bits
+``paged_append_fp8`` / ``paged_decode_fp8`` / ``paged_read_fp8``, and
+``paged_decode_shared`` for sequences with shared rows (with
 ``make_paged_workspace``, ``default_paged_workspace``), whose argument checks are compiled
 (``csrc/binding.cpp``).
 If the library has not been built every call raises ``ImportError``; there is
@@ -38,7 +40,7 @@ __all__ = [
     "decode_host",
     "block_forward_host", "PAGED_WORKSPACE_BYTES", "make_paged_workspace", "default_paged_workspace",
     "paged_append", "paged_decode", "paged_prefill", "packed_prefill", "paged_append_fp8", "paged_read_fp8",
-    "paged_decode_fp8",
+    "paged_decode_fp8", "paged_decode_shared",
 ]
 
 D_MODEL, N_HEADS, N_KV_HEADS, HEAD_DIM = 4096, 32, 8, 128
@@ -82,6 +84,7 @@ _SIGNATURES = {
                                   _sz, _vp]),
     "gqa_paged_read_fp8": (_i, [_vp, _i, _vp, _vp, _vp, _sz, _vp]),
     "gqa_paged_decode_fp8": (_i, [_vp, _ll, _i, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
+    "gqa_paged_decode_shared": (_i, [_vp, _ll, _i, _i, _vp, _vp, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_paged_decode": (_i, [_vp, _ll, _i, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_paged_prefill": (_i, [_vp, _ll, _i, _i, _vp, _i, _vp, _vp, _f, _vp, _vp, _sz, _vp]),
     "gqa_packed_prefill": (_i, [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i, _vp, _i, _f, _vp, _vp, _sz, _vp]),
@@ -676,6 +679,25 @@ def paged_decode(q, start_pos, k_pages, v_pages, block_table, scale: float = HEA
                                             None if stream is None else stream.cuda_stream)
     if r:
         raise GQAError(r, "gqa_paged_decode")
+    return out
+
+
+def paged_decode_shared(q, start_pos, cu_groups, prefix_rows, k_pages, v_pages, block_table,
+                        scale: float = HEAD_DIM ** -0.5, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """``paged_decode`` for a batch whose sequences share their first rows in
+    groups (a system prompt, samples of one prompt): the same function, with
+    the shared rows read once for a group. Sequences cu_groups[g] ..
+    cu_groups[g+1]-1 (device int32 [G+1], non-decreasing; sequences outside are
+    in no group) have cache rows 0..prefix_rows[g]-1 (device int32 [G]) in
+    common, on the same pages or on copies. A sequence that does not see its
+    group's whole prefix is attended by itself."""
+    if out is None or workspace is None:
+        out, workspace = _defaults(q, "q", out, workspace, stream)
+    r = (_paged or _binding()).paged_decode_shared(q, start_pos, cu_groups, prefix_rows, k_pages, v_pages, block_table,
+                                                   scale, out, workspace,
+                                                   None if stream is None else stream.cuda_stream)
+    if r:
+        raise GQAError(r, "gqa_paged_decode_shared")
     return out
 
 

@@ -27,6 +27,15 @@ constexpr size_t PART_O_OFFSET = (PART_ML_OFFSET + PART_ML_BYTES + 255) / 256 * 
 constexpr size_t PART_O_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP * HEAD_DIM * 4;
 static_assert(REF_SMS * 2 * 4 <= JOINS_OFFSET - TICKETS_OFFSET, "tickets");
 static_assert(PART_O_OFFSET + PART_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
+// of a decode attention with shared rows: its plan, the parts of own rows, the parts of prefixes
+constexpr size_t SHARED_PLAN_OFFSET = (PART_O_OFFSET + PART_O_BYTES + 255) / 256 * 256;
+constexpr size_t SHARED_ROWS_OFFSET = SHARED_PLAN_OFFSET + 256;
+constexpr size_t OWN_ML_OFFSET = SHARED_ROWS_OFFSET + PAGED_MAX_SEQS * sizeof(SharedRow);
+constexpr size_t OWN_O_OFFSET = OWN_ML_OFFSET + SHARED_MAX_ROWS * static_cast<size_t>(8);
+constexpr int PREFIX_ROWS = SHARED_MAX_ROWS + REF_SMS * 256;
+constexpr size_t PREFIX_ML_OFFSET = OWN_O_OFFSET + SHARED_MAX_ROWS * static_cast<size_t>(HEAD_DIM * 4);
+constexpr size_t PREFIX_O_OFFSET = PREFIX_ML_OFFSET + PREFIX_ROWS * static_cast<size_t>(8);
+static_assert(PREFIX_O_OFFSET + PREFIX_ROWS * static_cast<size_t>(HEAD_DIM * 4) <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 static_assert(GQA_PAGED_MAX_SEQS == PAGED_MAX_SEQS && GQA_PAGED_MAX_REP == PAGED_MAX_REP, "limits");
 
 constexpr long long MAX_POSITIONS = 1LL << 30;  // positions a block table row can address
@@ -438,10 +447,10 @@ int gqa_paged_decode_fp8(const gqa_bf16* q, int64_t q_stride, int B, int n_heads
   return one_launch(stream, [&](cudaStream_t s) { return launch_paged_decode_fp8(maps, p, s); });
 }
 
-int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
-                     const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes,
-                     void* stream) {
-  PagedDecodeParams p{};
+// What the decode attentions over bf16 pages check and share.
+static int decode_args(PagedDecodeParams& p, const gqa_bf16* q, int64_t q_stride, int B, int n_heads,
+                       const int32_t* start_pos, const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace,
+                       size_t workspace_bytes) {
   if (!q || !start_pos || !out || B <= 0 || B > PAGED_MAX_SEQS) return GQA_EINVAL;
   int r = check_pages(pages, &p.pages);
   if (r == GQA_OK) r = check_heads(n_heads, pages->n_kv_heads);
@@ -471,12 +480,100 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
   p.part_o = reinterpret_cast<float*>(ws + PART_O_OFFSET);
   p.status = reinterpret_cast<int*>(ws);
   p.ctas = launch_sms();
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return GQA_OK;
+}
+
+int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                     const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  PagedDecodeParams p{};
+  const int r = decode_args(p, q, q_stride, B, n_heads, start_pos, pages, scale, out, workspace, workspace_bytes);
+  if (r != GQA_OK) return r;
   begin_call();
+  return one_launch(stream, [&](cudaStream_t s) { return launch_paged_decode(p, s); });
+}
+
+// The maps of packed queries and of keys and values for the attentions on the
+// tensor cores.
+static bool attention_maps(PackedPrefillMaps& maps, const gqa_bf16* q, int64_t q_stride, int N, int n_heads, int n_kv,
+                           const PagedCache& c, long long v_row, int kv_rows, int kv_pages, int box_rows) {
+  const int n_rep = n_heads / n_kv;
+  const cuuint64_t dims[3] = {HEAD_DIM, static_cast<cuuint64_t>(n_heads), static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[2] = {HEAD_DIM * 2, static_cast<cuuint64_t>(q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(n_rep), static_cast<cuuint32_t>(128 / n_rep)};
+  return encode_bf16(&maps.q, 3, q, dims, strides, box) &&
+         map_kv(&maps.k, c.k, n_kv, kv_rows, kv_pages, c.head_stride, c.row_stride, c.page_stride, box_rows) &&
+         map_kv(&maps.v, c.v, n_kv, kv_rows, kv_pages, c.head_stride, v_row, c.page_stride, box_rows);
+}
+
+int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                            const int32_t* cu_groups, int G, const int32_t* prefix_rows, const gqa_pages* pages,
+                            float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream) {
+  PagedDecodeParams p{};
+  if (!cu_groups || !prefix_rows || G <= 0 || G > PAGED_MAX_SEQS) return GQA_EINVAL;
+  const int r = decode_args(p, q, q_stride, B, n_heads, start_pos, pages, scale, out, workspace, workspace_bytes);
+  if (r != GQA_OK) return r;
+  if (!aligned4(cu_groups) || !aligned4(prefix_rows)) return GQA_EALIGN;
+  const int64_t row = static_cast<int64_t>(n_heads) * HEAD_DIM;
+  const Span o = span_of(out, B, row, row);
+  if (o.meets(span_of(cu_groups, static_cast<__int128>(G) + 1)) || o.meets(span_of(prefix_rows, G))) return GQA_EINVAL;
+  begin_call();
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The same function without sharing: where the batch cannot save enough, and
+  // where it passes what the plan and the workspace hold.
+  const int n_rep = n_heads / p.n_kv;
+  const long long keys = static_cast<long long>(pages->columns) * pages->page_size;
+  if (static_cast<unsigned long long>(keys) * (B - 1) * p.n_kv < SHARED_LEAST_ROWS || G > SHARED_MAX_GROUPS ||
+      B * n_heads > SHARED_MAX_ROWS || shared_most_units(B, n_rep, p.n_kv, keys) > 0x7fffffffLL)
+    return one_launch(stream, [&](cudaStream_t) { return launch_paged_decode(p, s); });
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SharedPrefixParams a{};
+  a.q = p.q;
+  a.B = B;
+  a.G = G;
+  a.n_heads = n_heads;
+  a.n_kv = p.n_kv;
+  a.start = start_pos;
+  a.cu = cu_groups;
+  a.prefix = prefix_rows;
+  a.pages = p.pages;
+  a.scale_log2 = p.scale_log2;
+  a.part_o = reinterpret_cast<float*>(ws + PREFIX_O_OFFSET);
+  a.part_ml = reinterpret_cast<float*>(ws + PREFIX_ML_OFFSET);
+  a.rows = reinterpret_cast<SharedRow*>(ws + SHARED_ROWS_OFFSET);
+  a.plan = reinterpret_cast<SharedPlan*>(ws + SHARED_PLAN_OFFSET);
+  a.status = p.status;
+  a.wait_ns = wait_limit_ns();
+  a.ctas = p.ctas;
+  p.shared = a.rows;
+  p.own_o = reinterpret_cast<float*>(ws + OWN_O_OFFSET);
+  p.own_ml = reinterpret_cast<float*>(ws + OWN_ML_OFFSET);
+  SharedJoinParams j{};
+  j.B = B;
+  j.n_heads = n_heads;
+  j.n_kv = p.n_kv;
+  j.start = start_pos;
+  j.rows = a.rows;
+  j.plan = a.plan;
+  j.part_o = a.part_o;
+  j.part_ml = a.part_ml;
+  j.part_rows = PREFIX_ROWS;
+  j.own_o = p.own_o;
+  j.own_ml = p.own_ml;
+  j.out = p.out;
+  PackedPrefillMaps maps;
+  if (!attention_maps(maps, q, q_stride, B, n_heads, p.n_kv, p.pages, p.pages.row_stride, pages->page_size,
+                      pages->num_pages, prefill_box_rows(pages->page_size)))
+    return fail_cuda(cudaErrorInvalidValue);
   prof_mark(0, s);
-  r = launched(launch_paged_decode(p, s));
+  int e = launched(launch_shared_prefix(maps, a, s));
   prof_mark(1, s);
-  return r;
+  if (e == GQA_OK) e = launched(launch_paged_decode(p, s));
+  prof_mark(2, s);
+  if (e == GQA_OK) e = launched(launch_shared_join(j, s));
+  prof_mark(3, s);
+  return e;
 }
 
 static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads, int n_kv, const int32_t* cu_tokens,
@@ -518,12 +615,7 @@ static int prefill_call(const gqa_bf16* q, int64_t q_stride, int N, int n_heads,
   if (packed_prefill_may_join(N, n_rep, most_keys)) p.joins = ws + JOINS_OFFSET;
   if (packed_prefill_join_bytes(p.ctas) > JOINS_BYTES) return fail_cuda(cudaErrorInvalidConfiguration);
   PackedPrefillMaps maps;
-  const cuuint64_t dims[3] = {HEAD_DIM, static_cast<cuuint64_t>(n_heads), static_cast<cuuint64_t>(N)};
-  const cuuint64_t strides[2] = {HEAD_DIM * 2, static_cast<cuuint64_t>(q_stride) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(n_rep), static_cast<cuuint32_t>(128 / n_rep)};
-  if (!encode_bf16(&maps.q, 3, q, dims, strides, box) ||
-      !map_kv(&maps.k, c.k, n_kv, kv_rows, kv_pages, c.head_stride, c.row_stride, c.page_stride, box_rows) ||
-      !map_kv(&maps.v, c.v, n_kv, kv_rows, kv_pages, c.head_stride, v_row, c.page_stride, box_rows))
+  if (!attention_maps(maps, q, q_stride, N, n_heads, n_kv, c, v_row, kv_rows, kv_pages, box_rows))
     return fail_cuda(cudaErrorInvalidValue);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_mark(0, s);

@@ -339,6 +339,29 @@ int paged_read_fp8(PyObject* const* a) {
   return gqa_paged_read_fp8(n, static_cast<int>(B), &from, &to, w.p, w.bytes, stream(a[10], d));
 }
 
+// q, start_pos, cu_groups, prefix_rows, k_pages, v_pages, block_table, scale, out, workspace, stream
+int paged_decode_shared(PyObject* const* a) {
+  const at::Tensor& qt = tensor(a[0], "q", at::kBFloat16);
+  const Device d{qt.device()};
+  const Rows q = rows(qt, "q");
+  const int32_t* start = ints(a[1], "start_pos", q.n, d);
+  int64_t G = 0;
+  const int32_t* prefix = ints(a[3], "prefix_rows", -1, d, &G);
+  const int32_t* cu = ints(a[2], "cu_groups", G + 1, d);
+  const gqa_pages g = pages(a[4], a[5], a[6], q.n, d);
+  const float scale = number(a[7]);
+  gqa_bf16* out = output(a[8], "out", q.n, q.heads, d);
+  d.cuda("q");
+  const Workspace w = workspace(a[9], d);
+  if (q.n == 0) return GQA_OK;
+  const c10::cuda::CUDAGuard guard(d.d);
+  if (G == 0)
+    return gqa_paged_decode(q.p, q.stride, static_cast<int>(q.n), static_cast<int>(q.heads), start, &g, scale, out, w.p,
+                            w.bytes, stream(a[10], d));
+  return gqa_paged_decode_shared(q.p, q.stride, static_cast<int>(q.n), static_cast<int>(q.heads), start, cu,
+                                 static_cast<int>(G), prefix, &g, scale, out, w.p, w.bytes, stream(a[10], d));
+}
+
 // q, start_pos, k_pages, v_pages, k_scales, v_scales, block_table, scale, out, workspace, stream
 int paged_decode_fp8(PyObject* const* a) {
   const at::Tensor& qt = tensor(a[0], "q", at::kBFloat16);
@@ -428,6 +451,7 @@ PyMethodDef methods[] = {
     {"paged_append_fp8", fast<16, paged_append_fp8>(), METH_FASTCALL, nullptr},
     {"paged_read_fp8", fast<11, paged_read_fp8>(), METH_FASTCALL, nullptr},
     {"paged_decode_fp8", fast<11, paged_decode_fp8>(), METH_FASTCALL, nullptr},
+    {"paged_decode_shared", fast<11, paged_decode_shared>(), METH_FASTCALL, nullptr},
     {"paged_decode", fast<9, paged_decode>(), METH_FASTCALL, nullptr},
     {"paged_prefill", fast<10, paged_prefill>(), METH_FASTCALL, nullptr},
     {"packed_prefill", fast<8, packed_prefill>(), METH_FASTCALL, nullptr},

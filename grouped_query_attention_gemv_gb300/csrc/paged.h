@@ -112,6 +112,22 @@ struct Fp8ReadParams {
 };
 cudaError_t launch_fp8_read(const Fp8ReadParams& p, cudaStream_t s);
 
+// The rows of a sequence that shares its first ones with others: `first` of
+// them; the parts of theirs (shared_prefix.cu): of KV head g at rows base + g
+// kv_rows + 256 x CTA, `span` of them, its own from `at` on, by the CTAs that
+// hold the units behind unit0 + g kv_units + ITEM_UNITS, before unit0 + g
+// kv_units + w. w 0: it shares none, first is 0.
+struct SharedRow {
+  int first, w, kv_units, unit0, kv_rows, base, span, at;
+};
+struct SharedPlan {
+  int units, parts;
+};
+constexpr int SHARED_MAX_GROUPS = 1024;  // groups that are looked at
+constexpr int SHARED_MAX_ROWS = 32768;   // query rows of a batch that shares (the workspace's room)
+// Cache rows (of one KV head) that sharing has to save, or it is not done.
+constexpr unsigned long long SHARED_LEAST_ROWS = 100000;
+
 // One new token per sequence over the pages.
 struct PagedDecodeParams {
   const __nv_bfloat16* q;
@@ -126,8 +142,38 @@ struct PagedDecodeParams {
   int* tickets;             // [ctas], zero-filled, left zero-filled
   int* status;
   int ctas;
+  // sequences that share their first rows: the rows that are read begin behind
+  // those, and what comes out is a part (own_o, own_ml); null: none shares
+  const SharedRow* shared;
+  float *own_o, *own_ml;
 };
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s);
+
+// The first part of an attention with shared rows: plan and prefixes.
+struct SharedPrefixParams {
+  const __nv_bfloat16* q;
+  int B, G, n_heads, n_kv;
+  const int *start, *cu, *prefix;
+  PagedCache pages;
+  float scale_log2;
+  float *part_o, *part_ml;  // rows of parts: O [32 column groups][span][4], (max in log2 units, sum)
+  SharedRow* rows;          // [B]
+  SharedPlan* plan;
+  int* status;
+  unsigned long long wait_ns;
+  int ctas;
+};
+// The last part: the join.
+struct SharedJoinParams {
+  int B, n_heads, n_kv;
+  const int* start;
+  const SharedRow* rows;
+  const SharedPlan* plan;
+  const float *part_o, *part_ml;
+  int part_rows;
+  const float *own_o, *own_ml;  // of each query row: O [128], (max in log2 units, sum)
+  __nv_bfloat16* out;
+};
 
 // The same over 8-bit pages. k, v: (dim, KV head, row, page), boxes of 128 dims
 // x 1 head x fp8_decode_box_rows(page) rows.
@@ -185,6 +231,9 @@ __host__ __device__ constexpr int prefill_box_rows(int page_size) { return page_
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& p, cudaStream_t s);
 // With p.joins set, the join follows.
 cudaError_t launch_packed_prefill_join(const PackedPrefillParams& p, cudaStream_t s);
+cudaError_t launch_shared_prefix(const PackedPrefillMaps& maps, const SharedPrefixParams& p, cudaStream_t s);
+cudaError_t launch_shared_join(const SharedJoinParams& p, cudaStream_t s);
+long long shared_most_units(int B, int n_rep, int n_kv, long long keys);
 bool packed_prefill_may_join(int N, int n_rep, long long most_keys);
 size_t packed_prefill_join_bytes(int ctas);
 

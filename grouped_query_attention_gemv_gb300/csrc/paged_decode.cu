@@ -64,8 +64,10 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
   return static_cast<uint32_t>(r * ROW_BYTES + ((c ^ (r & 7)) << 4));
 }
 
-// NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16).
-template <int NT>
+// NT: 8-wide tiles of query heads (1: n_rep <= 8, 2: n_rep <= 16). SHARED:
+// sequences may share their first rows (p.shared); the others' are read here,
+// and of such a sequence a part is left instead of its output rows.
+template <int NT, bool SHARED>
 __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int W = WARPS;
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
   float* stash = reinterpret_cast<float*>(smem + W * (STAGES * STAGE_BYTES));
   int* pre = reinterpret_cast<int*>(stash + W * n_rep * PART);
   int* last = pre + p.B + 1;  // last row of each sequence
+  int* begin = last + p.B;    // SHARED: its first row that is read
   __shared__ Shared sh;
 
   // nothing is read or written before the previous kernel of the stream is done
@@ -88,12 +91,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     const bool ok = s >= 0 && s < p.pages.capacity();
     if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
     last[b] = s;
+    if (SHARED) {
+      const int f = ok ? p.shared[b].first : 0;
+      begin[b] = f;
+      return ok && s >= f ? s / KEYS - f / KEYS + 1 : 0;
+    }
     return ok ? s / KEYS + 1 : 0;
   });
   // rows of sequences without keys
 #pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (pre[b + 1] == pre[b])
+    if (pre[b + 1] == pre[b] && (!SHARED || begin[b] == 0))
 #pragma unroll 1
       for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
         reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
@@ -114,8 +122,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
     Cursor iss = locate(a0, pre, p.B, p.n_kv), cur = iss;
     // element offset of row lane % 16 of the chunk at `iss`, -1 for a row past the sequence
     auto row_offset = [&]() -> long long {
-      const int pos = iss.j * KEYS + piece;
-      if (pos > last[iss.b]) return -1;
+      const int f = SHARED ? begin[iss.b] : 0;
+      const int pos = (iss.j + f / KEYS) * KEYS + piece;
+      if (pos > last[iss.b] || (SHARED && pos < f)) return -1;
       const int page = p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)];
       if (page < 0 || page >= p.pages.num_pages) {
         report(p.status, DEV_BAD_PAGE);
@@ -186,17 +195,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         for (int nt = 0; nt < NT; ++nt) mma16816((s & 1) ? sd[nt] : sc[nt], k0, k1, k2, k3, qb[nt][s][0], qb[nt][s][1]);
       }
       // rows gr and gr + 8 of the chunk
-      const int left = last[cur.b] - cur.j * KEYS;
+      const int from = SHARED ? begin[cur.b] : 0;
+      const int left = last[cur.b] - (cur.j + from / KEYS) * KEYS;
+      const int before = SHARED ? cur.j ? 0 : from % KEYS : 0;  // rows of the chunk that are shared
       uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float(&x)[4] = sc[nt];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += sd[nt][e];
-        x[0] = gr <= left ? x[0] * p.scale_log2 : -INFINITY;
-        x[1] = gr <= left ? x[1] * p.scale_log2 : -INFINITY;
-        x[2] = gr + 8 <= left ? x[2] * p.scale_log2 : -INFINITY;
-        x[3] = gr + 8 <= left ? x[3] * p.scale_log2 : -INFINITY;
+        const bool sees0 = gr <= left && (!SHARED || gr >= before), sees1 = gr + 8 <= left && (!SHARED || gr + 8 >= before);
+        x[0] = sees0 ? x[0] * p.scale_log2 : -INFINITY;
+        x[1] = sees0 ? x[1] * p.scale_log2 : -INFINITY;
+        x[2] = sees1 ? x[2] * p.scale_log2 : -INFINITY;
+        x[3] = sees1 ? x[3] * p.scale_log2 : -INFINITY;
         float pr[4], al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -258,7 +270,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
-      if (seg.first >= a0 && seg.end <= a1) {
+      if (SHARED && seg.first >= a0 && seg.end <= a1 && begin[here.b] > 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = nt * 8 + 2 * t + e;
+            if (h >= n_rep) continue;
+            float* row = p.own_o + static_cast<long long>(seg.row + h) * HEAD_DIM;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              __stcg(row + 16 * d + gr, oacc[nt][d][e]);
+              __stcg(row + 16 * d + gr + 8, oacc[nt][d][e + 2]);
+            }
+            if (gr == 0) __stcg(reinterpret_cast<float2*>(p.own_ml) + seg.row + h, make_float2(m_run[nt][e], l_run[nt][e]));
+          }
+      } else if (seg.first >= a0 && seg.end <= a1) {
         __nv_bfloat16* out = p.out + static_cast<long long>(seg.row) * HEAD_DIM;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -313,10 +340,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) paged_decode_kernel(PagedDecode
         return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
                        : stash + (e >> 1) * n_rep * PART;
       },
-      [&](int row, float4 o, float m, float l) { store_row(p.out, row, o, 1.f / l); });
+      [&](int row, float4 o, float m, float l) {
+        if (SHARED && begin[row / p.n_heads] > 0) {
+          __stcg(reinterpret_cast<float4*>(p.own_o) + static_cast<long long>(row) * (HEAD_DIM / 4) + lane, o);
+          if (lane == 0) __stcg(reinterpret_cast<float2*>(p.own_ml) + row, make_float2(m, l));
+        } else {
+          store_row(p.out, row, o, 1.f / l);
+        }
+      });
 }
 
-template <int NT>
+template <int NT, bool SHARED>
 cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t s) {
   static bool attr_set[64] = {};
   int dev = 0;
@@ -324,13 +358,14 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    e = cudaFuncSetAttribute(paged_decode_kernel<NT, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
   const int n_rep = p.n_heads / p.n_kv;
-  const size_t smem = static_cast<size_t>(WARPS) * (STAGES * STAGE_BYTES + n_rep * PART * 4) + (2 * p.B + 1) * 4;
-  return launch_behind(paged_decode_kernel<NT>, static_cast<unsigned>(p.ctas), WARPS * 32, smem, s, p);
+  const size_t smem =
+      static_cast<size_t>(WARPS) * (STAGES * STAGE_BYTES + n_rep * PART * 4) + ((SHARED ? 3 : 2) * p.B + 1) * 4;
+  return launch_behind(paged_decode_kernel<NT, SHARED>, static_cast<unsigned>(p.ctas), WARPS * 32, smem, s, p);
 }
 
 }  // namespace
@@ -339,7 +374,8 @@ cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s) {
   if (p.B <= 0 || p.B > PAGED_MAX_SEQS || p.ctas <= 0) return cudaErrorInvalidValue;
   const int n_rep = p.n_heads / p.n_kv;
   if (n_rep < 1 || n_rep > PAGED_MAX_REP) return cudaErrorInvalidValue;
-  return n_rep <= 8 ? launch_nt<1>(p, s) : launch_nt<2>(p, s);
+  if (p.shared) return n_rep <= 8 ? launch_nt<1, true>(p, s) : launch_nt<2, true>(p, s);
+  return n_rep <= 8 ? launch_nt<1, false>(p, s) : launch_nt<2, false>(p, s);
 }
 
 }  // namespace gqa

@@ -1,0 +1,795 @@
+// Attention of one new token per sequence for groups of sequences that share
+// their first rows ("Llama 3.1 8B · Grouped-query attention", mode decode): the
+// shared rows are read once for a group instead of once for each of its
+// sequences, the rows of its own are streamed for each (paged_decode.cu), and
+// the parts, each an O, a max and a sum, are joined by the log-sum-exp rule.
+// Three launches: the prefix kernel, which also plans, the streaming of own
+// rows, the join.
+//
+// The prefix part is matrix-shaped: members x n_rep query rows of a KV head
+// against the prefix's keys, 4 x 128 flops a pair, so it runs on the
+// 5th-generation tensor cores as the prefill attention does
+// (packed_prefill.cu, whose tiles and turns these are), without a causal mask:
+//   * An item is two 128-row Q tiles (128 / n_rep sequences x n_rep heads each)
+//     of one KV head and the whole prefix. S = Q K^T goes to TMEM, P as bf16 over
+//     its first half, O += P V; 128-key tiles, staged once for both Q tiles, whose
+//     issuers take turns so that one's softmax runs beside the other's products.
+//   * The key tiles of all items, ITEM_UNITS more for each, are cut into one equal
+//     range per CTA. A CTA's piece of an item leaves a part in the workspace,
+//     at (rows of the items before) + 256 x CTA: from one piece to the next
+//     either grows by what the last one took, so that no two meet.
+//   * All rows of a Q tile see all keys, so only the last tile is masked, and
+//     value rows behind the prefix are cleared in shared memory.
+// Which sequences share: those of a group that see all of its prefix
+// (start_pos + 1 >= prefix_rows), if there are two at least and sharing saves
+// enough bytes. The others are streamed from their row 0 on, in rows of the Q
+// tiles that nobody reads.
+//
+//   warp 8        TMA producer: 128 / min(page, 128) boxes a tile, one lane each
+//   warps 9, 10   MMA issuers, one per Q tile
+//   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
+// P is rounded to bf16 (the product takes no wider operand); sums are fp32 of
+// the unrounded values. Every wait is bounded (gqa_set_wait_limit_ns); one that
+// gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
+// frees TMEM before the CTA exits.
+#include <math.h>
+
+#include "decode_parts.cuh"
+#include "paged.h"
+
+namespace gqa {
+
+namespace {
+
+constexpr int ROWS = 128;                 // rows of a Q tile = MMA M
+constexpr int NQ = 2;                     // Q tiles per CTA
+constexpr int KT = PACKED_TILE;           // keys per tile
+constexpr int HALF = KT / 2;
+constexpr int STAGES = 2;                 // K tiles and V tiles in shared memory
+constexpr int Q_HALF = ROWS * 128;        // 128 rows x 64 dims
+constexpr int Q_TILE = 2 * Q_HALF;
+constexpr int KV_HALF = KT * 128;         // 128 keys x 64 dims
+constexpr int KV_TILE = 2 * KV_HALF;
+constexpr int K_OFF = NQ * Q_TILE;
+constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
+constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
+constexpr int BARS_BYTES = 1024;
+constexpr int PLAN_OFF = BAR_OFF + BARS_BYTES;
+constexpr int PLAN_ARRAY = SHARED_MAX_GROUPS + 1;
+constexpr int SMEM_BYTES = PLAN_OFF + 4 * PLAN_ARRAY * 4 + 1024;
+constexpr int THREADS = 352;
+constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
+constexpr int SLOTS = 2;                        // items handed from the producer to the other warps
+constexpr uint32_t TMEM_COLS = 512;
+// TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
+constexpr uint32_t S_COLS = 128, O_COL = 256, O_COLS = 128;
+constexpr float RESCALE_LOG2 = 8.f;
+
+// A CTA's piece of an item: KV head g, sequences seq0 .. seq0 + nseq - 1, key
+// tiles j0 .. j0 + n - 1 of the prefix's `end` keys, read by sequence lead's
+// table; its part's first row in the workspace.
+struct Item {
+  int g, seq0, nseq, lead, end, j0, n;
+  int base;
+};
+
+struct Bars {
+  uint64_t q_full[NQ];
+  uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
+  uint64_t s_full[NQ], p_full[NQ][2];  // p_full: the first and the second half of the keys
+  uint64_t turn[NQ];                   // the issuer of Q tile t has issued a step
+  uint64_t o_done[NQ], mma_done[NQ];
+  uint64_t item_full[SLOTS], item_empty[SLOTS];
+  uint32_t tmem_slot;
+  int abort;
+  unsigned long long wait_ns;  // limit of the waits
+  int q_issued[NQ], k_issued, v_issued;
+  int warp_sum[THREADS / 32][2];
+  unsigned long long saved;    // rows that sharing saves
+  Item item[SLOTS];            // g < 0: no more
+};
+static_assert(sizeof(Bars) <= BARS_BYTES, "barrier block");
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ bool aborted(const Bars& bs) { return *reinterpret_cast<const volatile int*>(&bs.abort) != 0; }
+
+// Wait of a whole warp for phase `parity` of a barrier; false when it gave up.
+__device__ __noinline__ bool wait_longer(const Bars& bs, uint32_t bar, unsigned parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, bs.wait_ns));
+}
+__device__ __forceinline__ bool wait_bar(const Bars& bs, uint64_t& bar, unsigned parity) {
+  const uint32_t at = smem_u32(&bar);
+  return __all_sync(0xffffffffu, mbar_try_wait(at, parity)) || wait_longer(bs, at, parity);
+}
+
+// The items of this CTA in order, as the other warps take them from the
+// producer's slots.
+struct ItemWalk {
+  int k = 0;
+  bool ok = true;
+  __device__ __forceinline__ bool next(Bars& bs, Item& it) {
+    const int s = k % SLOTS;
+    ok = wait_bar(bs, bs.item_full[s], (k / SLOTS) & 1);
+    if (!ok) return false;
+    it = bs.item[s];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bs.item_empty[s]));
+    ++k;
+    return it.g >= 0;
+  }
+};
+
+// The groups in shared memory: sequences cu[g] .. cu[g+1]-1; of those that
+// share, the first that sees the whole prefix, and prefix sums of the units of
+// one KV head and of the query rows of one KV head (no step: does not share).
+struct Groups {
+  int *cu, *lead, *units, *rows;
+};
+
+__device__ __forceinline__ int tiles_of(int prefix) { return ceil_div(prefix, KT); }
+
+__global__ void __launch_bounds__(THREADS, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedPrefixParams a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bs = *reinterpret_cast<Bars*>(smem + BAR_OFF);
+  int* plan = reinterpret_cast<int*>(smem + PLAN_OFF);
+  const Groups gs{plan, plan + PLAN_ARRAY, plan + 2 * PLAN_ARRAY, plan + 3 * PLAN_ARRAY};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int nrep = a.n_heads / a.n_kv;
+  const int qp = ROWS / nrep;  // sequences per Q tile
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&bs.k_full[s]), 1);
+      mbar_init(smem_u32(&bs.k_empty[s]), NQ);  // one arrival per MMA issuer
+      mbar_init(smem_u32(&bs.v_full[s]), 1);
+      mbar_init(smem_u32(&bs.v_empty[s]), NQ);
+    }
+    for (int t = 0; t < NQ; ++t) {
+      mbar_init(smem_u32(&bs.q_full[t]), 1);
+      mbar_init(smem_u32(&bs.s_full[t]), 1);
+      mbar_init(smem_u32(&bs.turn[t]), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&bs.p_full[t][h]), 4);
+      mbar_init(smem_u32(&bs.o_done[t]), 1);
+      mbar_init(smem_u32(&bs.mma_done[t]), 1);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(smem_u32(&bs.item_full[s]), 1);
+      mbar_init(smem_u32(&bs.item_empty[s]), 10);  // issuers, softmax warps
+    }
+    bs.abort = 0;
+    bs.wait_ns = a.wait_ns;
+    bs.q_issued[0] = bs.q_issued[1] = 0;
+    bs.k_issued = bs.v_issued = 0;
+    bs.saved = 0;
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&bs.tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  // nothing in global memory is read or written before the previous kernel of
+  // the stream is done
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- the plan. Members of each group (counted where K tiles will lie) and
+  // the first of them.
+  int* members = reinterpret_cast<int*>(smem + K_OFF);
+  bool bad = false;
+  for (int g = tid; g <= a.G; g += THREADS) {
+    const int c = a.cu[g];
+    gs.cu[g] = c;
+    bad |= c < 0 || c > a.B || (g > 0 && a.cu[g - 1] > c);
+    if (g < a.G) {
+      members[g] = 0;
+      gs.lead[g] = a.B;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && blockIdx.x == 0 && tid == 0) report(a.status, DEV_BAD_POSITION);
+  // the group of sequence b whose prefix it sees whole, or -1
+  auto group_of = [&](int b) {
+    if (bad || b < gs.cu[0] || b >= gs.cu[a.G]) return -1;
+    int lo = 0, hi = a.G;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (gs.cu[mid] <= b) lo = mid; else hi = mid;
+    }
+    const int s = a.start[b], p = a.prefix[lo];
+    return p > 0 && s >= p - 1 && s < a.pages.capacity() ? lo : -1;
+  };
+  for (int b = tid; b < a.B; b += THREADS) {
+    const int g = group_of(b);
+    if (g >= 0) {
+      atomicAdd(&members[g], 1);
+      atomicMin(&gs.lead[g], b);
+    }
+  }
+  __syncthreads();
+  {
+    const int per = ceil_div(a.G, THREADS);
+    const int g0 = min(tid * per, a.G), g1 = min(g0 + per, a.G);
+    unsigned long long saved = 0;
+    for (int g = g0; g < g1; ++g)
+      if (members[g] > 1) saved += static_cast<unsigned long long>(members[g] - 1) * a.prefix[g];
+    if (saved) atomicAdd(&bs.saved, saved);
+    __syncthreads();
+    const bool shares = bs.saved * a.n_kv >= SHARED_LEAST_ROWS;
+    int sum[2] = {0, 0};
+    for (int g = g0; g < g1; ++g) {
+      const int size = gs.cu[g + 1] - gs.cu[g];
+      const bool on = shares && members[g] > 1;
+      gs.units[g + 1] = on ? ceil_div(size, NQ * qp) * (tiles_of(a.prefix[g]) + ITEM_UNITS) : 0;
+      gs.rows[g + 1] = on ? size * nrep : 0;
+      sum[0] += gs.units[g + 1];
+      sum[1] += gs.rows[g + 1];
+    }
+    int run[2] = {sum[0], sum[1]};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, run[k], o);
+        if (lane >= o) run[k] += x;
+      }
+      if (lane == 31) bs.warp_sum[warp][k] = run[k];
+    }
+    if (tid == 0) gs.units[0] = gs.rows[0] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      run[k] -= sum[k];
+      for (int w = 0; w < warp; ++w) run[k] += bs.warp_sum[w][k];
+    }
+    for (int g = g0; g < g1; ++g) {
+      run[0] += gs.units[g + 1];
+      run[1] += gs.rows[g + 1];
+      gs.units[g + 1] = run[0];
+      gs.rows[g + 1] = run[1];
+    }
+  }
+  fence_proxy_async_smem();  // K tiles come where the members were counted
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int units = gs.units[a.G] * a.n_kv;
+  const int parts = units ? range_count(units, mean_range(units, gridDim.x), gridDim.x) : 1;
+  // what the own rows' kernel and the join need of it
+  if (blockIdx.x == 0 && tid == 0) {
+    a.plan->units = units;
+    a.plan->parts = parts;
+  }
+  for (int b = tid; b < a.B; b += THREADS) {
+    if (static_cast<int>(blockIdx.x) != (b >> 5) % static_cast<int>(gridDim.x)) continue;
+    SharedRow r = {};
+    const int g = group_of(b);
+    if (g >= 0 && gs.units[g + 1] > gs.units[g]) {
+      const int i = b - gs.cu[g], e = i / (NQ * qp), size = gs.cu[g + 1] - gs.cu[g];
+      r.first = a.prefix[g];
+      r.w = tiles_of(r.first) + ITEM_UNITS;
+      r.kv_units = gs.units[g + 1] - gs.units[g];
+      r.unit0 = gs.units[g] * a.n_kv + e * r.w;
+      r.kv_rows = size * nrep;
+      r.base = gs.rows[g] * a.n_kv + e * NQ * qp * nrep;
+      r.span = min(NQ * qp, size - e * NQ * qp) * nrep;
+      r.at = (i - e * NQ * qp) * nrep;
+    }
+    a.rows[b] = r;
+  }
+  const uint32_t tmem = bs.tmem_slot;
+  const uint32_t sbase = smem_u32(smem);
+  ItemWalk walk;
+  Item it = {};
+
+  if (warp == PRODUCER_WARP) {
+    const Split split(units, parts);
+    const bool ranged = static_cast<int>(blockIdx.x) < parts;
+    int ru = ranged ? split.start(blockIdx.x) : 0;
+    const int rend = ranged ? split.start(blockIdx.x + 1) : 0;
+    // units in (group, KV head, pair of Q tiles, key tile) order; this CTA's range of them
+    auto next_item = [&](Item& x) {
+      while (ru < rend) {
+        int lo = 0, hi = a.G;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (gs.units[mid] * a.n_kv <= ru) lo = mid; else hi = mid;
+        }
+        const int size = gs.cu[lo + 1] - gs.cu[lo], w = tiles_of(a.prefix[lo]) + ITEM_UNITS;
+        const int pairs = ceil_div(size, NQ * qp), in_group = ru - gs.units[lo] * a.n_kv;
+        const int item = in_group / w, in = in_group - item * w, base = ru - in, end = min(rend, base + w);
+        const int e = item % pairs;
+        x.g = item / pairs;
+        x.seq0 = gs.cu[lo] + e * NQ * qp;
+        x.nseq = min(NQ * qp, size - e * NQ * qp);
+        x.lead = gs.lead[lo];
+        x.end = a.prefix[lo];
+        x.j0 = max(0, in - ITEM_UNITS);
+        x.n = max(0, end - base - ITEM_UNITS - x.j0);
+        x.base = gs.rows[lo] * a.n_kv + (x.g * size + e * NQ * qp) * nrep + NQ * ROWS * static_cast<int>(blockIdx.x);
+        ru = end;
+        if (x.n > 0) return true;
+      }
+      return false;
+    };
+    int puts = 0;
+    auto put = [&](const Item& x) {
+      const int s = puts % SLOTS;
+      if (puts >= SLOTS && !wait_bar(bs, bs.item_empty[s], (puts / SLOTS - 1) & 1)) return false;
+      if (lane == 0) {
+        bs.item[s] = x;
+        mbar_arrive(smem_u32(&bs.item_full[s]));
+      }
+      __syncwarp();
+      ++puts;
+      return true;
+    };
+    if (lane == 0) {
+      tma_prefetch_desc(&mq);
+      tma_prefetch_desc(&mk);
+      tma_prefetch_desc(&mv);
+    }
+    // Lane x < boxes handles box x of every tile. u counts tiles over the
+    // CTA's items, ring slot u % STAGES.
+    const int box = prefill_box_rows(1 << a.pages.page_shift);
+    const int boxes = KT / box;
+    const uint32_t q_bytes = static_cast<uint32_t>(qp * nrep) * 128;
+    int u = 0, kn = 0, vn = 0, qn[NQ] = {};
+    int cs[NQ] = {};  // score tiles of each Q tile so far (as its issuer counts them)
+    bool ok = true, stop = false;
+    auto go_on = [&](uint64_t& bar, int parity) {
+      ok = wait_bar(bs, bar, parity);
+      return ok && !__any_sync(0xffffffffu, aborted(bs));
+    };
+    auto copy = [&](const CUtensorMap* map, uint64_t& full, uint32_t dst, int held, int g, int row, int page) {
+      const uint32_t fb = smem_u32(&full);
+      if (lane == 0) mbar_expect_tx(fb, static_cast<uint32_t>(held * box) * 256);
+      __syncwarp();
+      if (lane < held) {
+        const uint32_t at = dst + static_cast<uint32_t>(lane * box) * 128;
+        tma_load_4d(at, map, fb, 0, g, row, page);
+        tma_load_4d(at + KV_HALF, map, fb, 64, g, row, page);
+      }
+      __syncwarp();
+    };
+    while (!stop && next_item(it)) {
+      if (!put(it)) {
+        ok = false;
+        break;
+      }
+      for (int j = 0; j < it.n && !stop; ++j, ++u) {
+        const int s = u % STAGES;
+        // boxes of the tile that hold keys of the prefix; this lane's
+        const int held = min(boxes, (it.end - (it.j0 + j) * KT + box - 1) / box);
+        const int key = (it.j0 + j) * KT + lane * box;
+        const int row = key & ((1 << a.pages.page_shift) - 1);
+        int page = 0;
+        if (lane < held)
+          page = a.pages.table[static_cast<long long>(it.lead) * a.pages.table_stride + (key >> a.pages.page_shift)];
+        if (u >= STAGES && !go_on(bs.k_empty[s], (u / STAGES - 1) & 1)) {
+          stop = true;
+          break;
+        }
+        if (page < 0 || page >= a.pages.num_pages) {
+          report(a.status, DEV_BAD_PAGE);
+          page = 0;
+        }
+        copy(&mk, bs.k_full[s], sbase + K_OFF + s * KV_TILE, held, it.g, row, page);
+        kn = u + 1;
+        if (j == 0) {
+          // Q tile t is free once the last score product of the previous item
+          // that read it has completed
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) {
+            if (stop || it.nseq <= t * qp) continue;
+            if (cs[t] > 0 && !go_on(bs.s_full[t], (cs[t] - 1) & 1)) {
+              stop = true;
+              continue;
+            }
+            if (lane == 0) {
+              const uint32_t qb = smem_u32(&bs.q_full[t]);
+              mbar_expect_tx(qb, 2 * q_bytes);
+              // boxes may reach past the group, or past B (zeros): rows that are never stored
+              tma_load_3d(sbase + t * Q_TILE, &mq, qb, 0, it.g * nrep, it.seq0 + t * qp);
+              tma_load_3d(sbase + t * Q_TILE + Q_HALF, &mq, qb, 64, it.g * nrep, it.seq0 + t * qp);
+            }
+            __syncwarp();
+            ++qn[t];
+          }
+          if (stop) break;
+        }
+        if (u >= STAGES && !go_on(bs.v_empty[s], (u / STAGES - 1) & 1)) {
+          stop = true;
+          break;
+        }
+        copy(&mv, bs.v_full[s], sbase + V_OFF + s * KV_TILE, held, it.g, row, page);
+        vn = u + 1;
+      }
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) cs[t] += it.nseq > t * qp ? it.n : 0;
+    }
+    if (ok && !stop) {
+      it.g = -1;
+      ok = put(it);
+    }
+    if (lane == 0) {
+      if (!ok) atomicExch(&bs.abort, 1);
+      bs.q_issued[0] = qn[0];
+      bs.q_issued[1] = qn[1];
+      bs.k_issued = kn;
+      bs.v_issued = vn;
+    }
+  } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
+    // issuer of Q tile t (the whole warp runs the loop; one elected lane
+    // issues). Step j: P_{j-1} V_{j-1}, then S_j into the columns P_{j-1} lay
+    // in (products of one thread complete in order); the two issuers take turns
+    // step by step. They wait on every K and V tile of the item, so that their
+    // arrivals on the empty barriers stay in step. cs counts this Q tile's score
+    // tiles over the items, qi its items, step the steps of all items.
+    const int t = warp - MMA_WARP;
+    const uint32_t idesc_s = umma_idesc_bf16(ROWS, KT), idesc_sh = umma_idesc_bf16(ROWS, HALF);
+    const uint32_t idesc_o = umma_idesc_bf16(ROWS, HEAD_DIM) | (1u << 16);  // B (V) MN-major
+    const uint32_t qt = sbase + t * Q_TILE;
+    const uint32_t s_at = tmem + t * S_COLS, o_at = tmem + O_COL + t * O_COLS;
+    unsigned u0 = 0, cs = 0, qi = 0, step = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t& bar, unsigned parity) {
+      return ok = wait_bar(bs, bar, parity);
+    };
+    // the stage is free once this issuer's products on it are done (a commit
+    // covers every product the thread issued before it)
+    auto release = [&](uint64_t& bar, bool used) {
+      if (elect_one()) {
+        if (used) umma_commit(smem_u32(&bar));
+        else mbar_arrive(smem_u32(&bar));
+      }
+      __syncwarp();
+    };
+    while (ok && walk.next(bs, it)) {
+      const int n_t = it.nseq > t * qp ? it.n : 0;
+      for (int j = 0; j <= it.n; ++j, ++step) {
+        // everything S_j needs but its turn, so that it follows P_{j-1} V_{j-1} at once
+        const unsigned uk = u0 + j, sk = uk % STAGES;
+        if (j < it.n && !wait(bs.k_full[sk], (uk / STAGES) & 1)) break;
+        if (j == 0 && n_t > 0 && !wait(bs.q_full[t], qi & 1)) break;
+        const uint32_t kt = sbase + K_OFF + sk * KV_TILE;
+        const uint32_t idesc = it.end - (it.j0 + j) * KT > HALF ? idesc_s : idesc_sh;
+        if (j >= 1) {
+          const int i = j - 1, tile = it.j0 + i;
+          const unsigned u = u0 + i, s = u % STAGES;
+          if (!wait(bs.v_full[s], (u / STAGES) & 1)) break;
+          const uint32_t vt = sbase + V_OFF + s * KV_TILE;
+          const int left = it.end - tile * KT, read = left > HALF ? KT : HALF;
+          if (n_t > 0) {
+            if (left < read) {
+              // clear the value rows behind the prefix (both issuers write the same zeros)
+              for (int w = lane; w < (read - left) * 16; w += 32) {
+                const int row = left + (w >> 4);
+                st_shared_v4(vt + ((w >> 3) & 1) * KV_HALF + row * 128 + (w & 7) * 16, make_uint4(0, 0, 0, 0));
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            // P of the item's first key tile also tells that the softmax
+            // warps have read the previous item's O (their epilogue comes
+            // first), so that the first product may overwrite it
+            if (!wait(bs.p_full[t][0], (cs + i) & 1)) break;
+          }
+          if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) break;
+          if (n_t > 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !wait(bs.p_full[t][1], (cs + i) & 1)) break;
+              tc_fence_after();
+              if (h == 1 && read == HALF) break;  // no keys in the second half
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < HALF / 16; ++ks)
+                  umma_bf16_ts(o_at, s_at + h * (HALF / 2) + ks * 8,
+                               umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF), idesc_o,
+                               (i > 0 || h > 0 || ks > 0) ? 1u : 0u);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          }
+        } else if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) {
+          break;
+        }
+        if (j < n_t) {
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < HEAD_DIM / 16; ++ks) {
+              const uint32_t off = (ks & 3) * 32;
+              umma_bf16(s_at, umma_desc_sw128(qt + (ks >> 2) * Q_HALF + off),
+                        umma_desc_sw128(kt + (ks >> 2) * KV_HALF + off), idesc, ks > 0 ? 1u : 0u);
+            }
+            umma_commit(smem_u32(&bs.s_full[t]));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(smem_u32(&bs.turn[t]));
+        if (j >= 1) {
+          if (j == n_t) {
+            if (elect_one()) umma_commit(smem_u32(&bs.o_done[t]));
+            __syncwarp();
+          }
+          release(bs.v_empty[(u0 + j - 1) % STAGES], n_t > 0);
+        }
+        if (j < it.n) release(bs.k_empty[sk], n_t > 0);
+      }
+      if (!ok) break;
+      u0 += it.n;
+      cs += n_t;
+      qi += n_t > 0;
+    }
+    if ((!ok || !walk.ok) && lane == 0) atomicExch(&bs.abort, 1);
+    if (elect_one()) umma_commit(smem_u32(&bs.mma_done[t]));
+    __syncwarp();
+    mbar_wait(smem_u32(&bs.mma_done[t]), 0);
+  } else {
+    // softmax / epilogue: warpgroup t, thread r owns row r = TMEM lane r of Q tile t
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + t * S_COLS + lanes, o_at = tmem + O_COL + t * O_COLS + lanes;
+    const float scale = a.scale_log2;
+    unsigned cs = 0;     // score tiles of this Q tile over the items (as the issuer counts them)
+    unsigned items = 0;  // items of this Q tile
+    bool ok = true;
+    while (ok && walk.next(bs, it)) {
+      const int n_t = it.nseq > t * qp ? it.n : 0;
+      const int rows = min(qp, it.nseq - t * qp) * nrep;  // of this Q tile
+      const bool real = r < rows;
+      const bool works = (warp & 3) * 32 < rows;          // some row of this warp is real
+      float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
+      float l = 0.f;
+      float m_limit = -INFINITY, neg = 0.f;  // max that P is still taken against m_ref with; -m_ref in log2 units
+      for (int j = 0; j < n_t; ++j) {
+        // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
+        if (!wait_bar(bs, bs.s_full[t], (cs + j) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int vis = it.end - 1 - (it.j0 + j) * KT;  // columns 0..vis are keys
+        const bool second = vis >= HALF;
+        // columns of half h, what is behind the prefix at -inf; the second
+        // half is read for the max first and again for its P (registers)
+        uint32_t sr[HALF];
+        auto load = [&](int h) {
+          tmem_ld32(s_at + h * HALF, sr);
+          tmem_ld32(s_at + h * HALF + 32, sr + 32);
+          tmem_ld_wait();
+          if (vis < h * HALF + HALF - 1) {
+#pragma unroll
+            for (int cc = 0; cc < HALF; ++cc)
+              if (h * HALF + cc > vis) sr[cc] = __float_as_uint(-INFINITY);
+          }
+          __syncwarp();  // the TMEM accesses want the warp converged
+        };
+        if (works) {
+          float mx = -INFINITY, m1 = mx, m2 = mx, m3 = mx;
+#pragma unroll
+          for (int h = 1; h >= 0; --h) {
+            if (h == 1 && !second) continue;
+            load(h);
+#pragma unroll
+            for (int cc = 0; cc < HALF; cc += 8) {
+              mx = max3(mx, __uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1]));
+              m1 = max3(m1, __uint_as_float(sr[cc + 2]), __uint_as_float(sr[cc + 3]));
+              m2 = max3(m2, __uint_as_float(sr[cc + 4]), __uint_as_float(sr[cc + 5]));
+              m3 = max3(m3, __uint_as_float(sr[cc + 6]), __uint_as_float(sr[cc + 7]));
+            }
+          }
+          mx = fmaxf(max3(mx, m1, m2), m3);
+          // the max outgrew the reference (always at a row's first keys)
+          if (__any_sync(0xffffffffu, mx > m_limit)) {
+            float alpha = 1.f;
+            if (mx > m_limit) {
+              alpha = m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - mx) * scale);
+              m_ref = mx;
+              m_limit = mx + RESCALE_LOG2 / scale;
+              neg = -mx * scale;
+              l *= alpha;
+            }
+            if (j > 0) {
+#pragma unroll 1
+              for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(o_at + cc, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(o_at + cc, o);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        // exponent arguments and the row sum two columns per instruction
+        const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
+        float2 sum2 = make_float2(0.f, 0.f), sum3 = sum2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (works && (h == 0 || second)) {
+            if (h == 1) load(1);
+            uint32_t pk[HALF / 2];
+#pragma unroll
+            for (int cc = 0; cc < HALF; cc += 4) {
+              const float2 e = fma2(make_float2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, ng2);
+              const float2 f =
+                  fma2(make_float2(__uint_as_float(sr[cc + 2]), __uint_as_float(sr[cc + 3])), sc2, ng2);
+              const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              const float2 q = make_float2(ex2_approx(f.x), ex2_approx(f.y));
+              sum2 = add2(sum2, p);
+              sum3 = add2(sum3, q);
+              pk[cc >> 1] = pack_bf16(p.x, p.y);
+              pk[(cc >> 1) + 1] = pack_bf16(q.x, q.y);
+            }
+            tmem_st32(s_at + h * (HALF / 2), pk);
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bs.p_full[t][h]));
+          __syncwarp();
+        }
+        sum2 = add2(sum2, sum3);
+        l += sum2.x + sum2.y;
+      }
+      if (!ok) break;
+      if (n_t > 0) {
+        if (!wait_bar(bs, bs.o_done[t], items & 1)) {
+          ok = false;
+          break;
+        }
+        ++items;
+        tc_fence_after();
+        // the part: [32 column groups][rows of the item][4] and (max in log2 units, sum)
+        if (works) {
+          const int span = it.nseq * nrep, row = t * qp * nrep + r;
+          const float m2 = l > 0.f || l != l ? m_ref * scale : -INFINITY;
+          if (real) __stcg(reinterpret_cast<float2*>(a.part_ml) + it.base + row, make_float2(m2, l));
+          float4* o4 = reinterpret_cast<float4*>(a.part_o) + static_cast<size_t>(it.base) * (HEAD_DIM / 4) + row;
+          __syncwarp();
+#pragma unroll 1
+          for (int cc = 0; cc < HEAD_DIM; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_at + cc, o);
+            tmem_ld_wait();
+            if (real) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(o4 + static_cast<size_t>(cc / 4 + e) * span,
+                       make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+            }
+            __syncwarp();
+          }
+        }
+      }
+      cs += n_t;
+    }
+    if ((!ok || !walk.ok) && lane == 0) atomicExch(&bs.abort, 1);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (aborted(bs)) {
+    if (tid == 0) report(a.status, DEV_WAIT_TIMEOUT);
+    if (warp == PRODUCER_WARP && lane == 0) {
+      // the last copy into each buffer may still be in flight
+      for (int t = 0; t < NQ; ++t)
+        if (bs.q_issued[t] > 0) mbar_wait(smem_u32(&bs.q_full[t]), (bs.q_issued[t] - 1) & 1);
+      for (int u = max(0, bs.k_issued - STAGES); u < bs.k_issued; ++u)
+        mbar_wait(smem_u32(&bs.k_full[u % STAGES]), (u / STAGES) & 1);
+      for (int u = max(0, bs.v_issued - STAGES); u < bs.v_issued; ++u)
+        mbar_wait(smem_u32(&bs.v_full[u % STAGES]), (u / STAGES) & 1);
+    }
+    __syncthreads();
+  }
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---- the join: a warp a query row. The parts of its prefix, one per CTA that
+// holds a piece of its item, in CTA order, then its own rows' part.
+constexpr int JOIN_WARPS = 8, JOIN_BATCH = 8;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const __grid_constant__ SharedJoinParams a) {
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+  // nothing is read or written before the previous kernel of the stream is done
+  pdl_trigger();
+  pdl_wait();
+  if (row >= a.B * a.n_heads) return;
+  const int nrep = a.n_heads / a.n_kv, b = row / a.n_heads, h = row - b * a.n_heads, g = h / nrep;
+  const SharedRow s = a.rows[b];
+  if (s.w == 0) return;
+  const Split split(a.plan->units, a.plan->parts);
+  const int unit = s.unit0 + g * s.kv_units;
+  const int first = split.holder(unit + ITEM_UNITS), last = split.holder(unit + s.w - 1);
+  const int base = s.base + g * s.kv_rows, r = s.at + h - g * nrep;
+  // of another call (a workspace that two calls use at once): nothing of it is read
+  if (first < 0 || base < 0 || s.span <= 0 || r < 0 || r >= s.span || base + NQ * ROWS * last + s.span > a.part_rows) return;
+  const float2* mls = reinterpret_cast<const float2*>(a.part_ml) + base + r;
+  const float4* os = reinterpret_cast<const float4*>(a.part_o) + static_cast<size_t>(base) * (HEAD_DIM / 4) +
+                     static_cast<size_t>(lane) * s.span + r;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // the rows of its own
+  if (a.start[b] >= s.first) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.own_ml) + row);
+    m = ml.x;
+    l = ml.y;
+    o = __ldcg(reinterpret_cast<const float4*>(a.own_o) + static_cast<size_t>(row) * (HEAD_DIM / 4) + lane);
+  }
+#pragma unroll 1
+  for (int c0 = first; c0 <= last; c0 += JOIN_BATCH) {
+    float2 ml[JOIN_BATCH];
+    float4 x[JOIN_BATCH];
+#pragma unroll
+    for (int k = 0; k < JOIN_BATCH; ++k) {
+      const int c = c0 + k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c <= last) {
+        ml[k] = mls[c * (NQ * ROWS)];
+        x[k] = os[static_cast<size_t>(c) * (NQ * ROWS * (HEAD_DIM / 4))];
+      }
+    }
+    float mx = m;
+#pragma unroll
+    for (int k = 0; k < JOIN_BATCH; ++k) mx = fmaxf(mx, ml[k].x);
+    decode::rescale(m, mx, l, o);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int k = 0; k < JOIN_BATCH; ++k) {
+      const float w = ex2_approx(ml[k].x - ref);
+      l += w * ml[k].y;
+      o.x += w * x[k].x;
+      o.y += w * x[k].y;
+      o.z += w * x[k].z;
+      o.w += w * x[k].w;
+    }
+  }
+  decode::store_row(a.out, row, o, 1.f / l);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefix(const PackedPrefillMaps& maps, const SharedPrefixParams& a, cudaStream_t s) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_set[dev]) {
+    e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  if (a.B <= 0 || a.B > PAGED_MAX_SEQS || a.G <= 0 || a.G > SHARED_MAX_GROUPS || a.ctas <= 0) return cudaErrorInvalidValue;
+  // one CTA per SM (shared memory and TMEM admit no second)
+  return launch_behind(shared_prefix_kernel, static_cast<unsigned>(a.ctas), THREADS, SMEM_BYTES, s, maps.q, maps.k, maps.v, a);
+}
+
+cudaError_t launch_shared_join(const SharedJoinParams& a, cudaStream_t s) {
+  const long long rows = static_cast<long long>(a.B) * a.n_heads;
+  return launch_behind(shared_join_kernel, static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS), JOIN_WARPS * 32, 0, s, a);
+}
+
+// Units of a batch at most: of groups of two sequences at least, with `keys` in
+// common, and their pairs of Q tiles.
+long long shared_most_units(int B, int n_rep, int n_kv, long long keys) {
+  const int qp = ROWS / n_rep;
+  return (B / 2 + B / (NQ * qp) + 1) * ((keys + KT - 1) / KT + ITEM_UNITS) * n_kv;
+}
+
+}  // namespace gqa

@@ -252,7 +252,8 @@ int gqa_set_decode_fusion(int enable);
 int gqa_set_decode_attention_split(int mode);
 
 /* Limit, for calls made on the calling thread, of the waits of the packed
- * prefill attention (gqa_paged_prefill, gqa_packed_prefill; GQA_DEV_WAIT_TIMEOUT
+ * prefill attention (gqa_paged_prefill, gqa_packed_prefill) and of
+ * gqa_paged_decode_shared's prefixes (GQA_DEV_WAIT_TIMEOUT
  * then, rows unspecified, and the workspace to be zero-filled) and of the
  * grid-wide waits of the block's decode kernels: the one-kernel step's two gates (every CTA's Q|K|V rows
  * published; every attention output published) and the attention's meeting
@@ -355,7 +356,9 @@ int gqa_host_stage_release(void* stage);
  * gqa_paged_append, then gqa_paged_decode (one new token per sequence) or
  * gqa_paged_prefill (any number of new tokens per sequence), between the
  * caller's own projections. gqa_packed_prefill attends over keys and values
- * packed beside the queries instead of a cache.
+ * packed beside the queries instead of a cache. The cache may be held in 8 bits
+ * (gqa_paged_append_fp8, gqa_paged_decode_fp8, gqa_paged_read_fp8), and
+ * sequences may share their first rows (gqa_paged_decode_shared).
  *
  * Head size 128, n_heads a multiple of n_kv_heads with at most 16 query heads
  * per KV head; query head h reads KV head h / (n_heads / n_kv_heads).
@@ -382,7 +385,7 @@ int gqa_host_stage_release(void* stage);
  * and can be captured into a graph; no length is read by the host, so a
  * captured step replays with other lengths, tables and contents. One launch
  * each; two for the prefill attention where a sequence may have more than
- * 2,048 keys. The workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled
+ * 2,048 keys, three for the decode attention of groups. The workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled
  * before its first use, serves one call at a time and no other entries than
  * these; its status word is read with gqa_device_status. After
  * GQA_DEV_WAIT_TIMEOUT zero-fill it again (gqa_workspace_init). */
@@ -493,6 +496,28 @@ int gqa_paged_read_fp8(const int32_t* rows, int B, const gqa_fp8_pages* from, co
 int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
                      const gqa_pages* pages, float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes,
                      void* stream);
+
+/* gqa_paged_decode for batches whose sequences share their first rows in
+ * groups (a system prompt, samples of one prompt): the same function, the shared
+ * rows read once for a group.
+ *   cu_groups    device int32 [G+1], non-decreasing, within 0..B: sequences
+ *                cu_groups[g] .. cu_groups[g+1]-1 are group g, others are in none
+ *   prefix_rows  device int32 [G]: the first rows that a group's sequences have
+ *                in common (0 or less: none). They hold the same keys and values,
+ *                on the same pages or on copies; which of the sequences' tables
+ *                they are read by is not specified.
+ * A sequence that does not see the whole prefix (start_pos + 1 < prefix_rows,
+ * or an unused slot) is attended by itself, and so are all where sharing would
+ * not pay: where it saves fewer cache rows than a threshold, with more than
+ * 1,024 groups, with more than 32,768 query rows (B * n_heads). Probabilities
+ * enter the value product of shared rows as in gqa_paged_prefill, of the others
+ * as in gqa_paged_decode. cu_groups out of order or range, where it is looked
+ * at, is reported as GQA_DEV_BAD_POSITION, and nothing is shared. G at most
+ * GQA_PAGED_MAX_SEQS. Three launches, or one where the host can tell that
+ * nothing will be shared. */
+int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
+                            const int32_t* cu_groups, int G, const int32_t* prefix_rows, const gqa_pages* pages,
+                            float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* gqa_paged_decode over 8-bit pages. (columns * page_size / 32 + 1) * B *
  * n_kv_heads must stay below 2^31, else GQA_EINVAL.
