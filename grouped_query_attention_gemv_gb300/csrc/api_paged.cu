@@ -28,14 +28,15 @@ constexpr size_t PART_O_BYTES = static_cast<size_t>(2) * REF_SMS * PAGED_MAX_REP
 static_assert(REF_SMS * 2 * 4 <= JOINS_OFFSET - TICKETS_OFFSET, "tickets");
 static_assert(PART_O_OFFSET + PART_O_BYTES <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 // of a decode attention with shared rows: its plan, the parts of own rows, the parts of prefixes
-constexpr size_t SHARED_PLAN_OFFSET = (PART_O_OFFSET + PART_O_BYTES + 255) / 256 * 256;
-constexpr size_t SHARED_ROWS_OFFSET = SHARED_PLAN_OFFSET + 256;
-constexpr size_t OWN_ML_OFFSET = SHARED_ROWS_OFFSET + PAGED_MAX_SEQS * sizeof(SharedRow);
-constexpr size_t OWN_O_OFFSET = OWN_ML_OFFSET + SHARED_MAX_ROWS * static_cast<size_t>(8);
+constexpr size_t SHARED_PARTS_OFFSET = (PART_O_OFFSET + PART_O_BYTES + 255) / 256 * 256;
+constexpr size_t OWN_ML_OFFSET = SHARED_PARTS_OFFSET + SHARED_MAX_ROWS * sizeof(SharedParts);
+// one part more per warp, and per CTA with prefixes, than there are (sequence, KV head) pairs
+constexpr int OWN_ROWS = SHARED_MAX_ROWS + REF_SMS * 8 * PAGED_MAX_REP;
 constexpr int PREFIX_ROWS = SHARED_MAX_ROWS + REF_SMS * 256;
-constexpr size_t PREFIX_ML_OFFSET = OWN_O_OFFSET + SHARED_MAX_ROWS * static_cast<size_t>(HEAD_DIM * 4);
+constexpr size_t PREFIX_ML_OFFSET = OWN_ML_OFFSET + OWN_ROWS * static_cast<size_t>(8);
 constexpr size_t PREFIX_O_OFFSET = PREFIX_ML_OFFSET + PREFIX_ROWS * static_cast<size_t>(8);
-static_assert(PREFIX_O_OFFSET + PREFIX_ROWS * static_cast<size_t>(HEAD_DIM * 4) <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
+constexpr size_t OWN_O_OFFSET = PREFIX_O_OFFSET + PREFIX_ROWS * static_cast<size_t>(HEAD_DIM * 4);
+static_assert(OWN_O_OFFSET + OWN_ROWS * static_cast<size_t>(HEAD_DIM * 4) <= GQA_PAGED_WORKSPACE_BYTES, "workspace");
 static_assert(GQA_PAGED_MAX_SEQS == PAGED_MAX_SEQS && GQA_PAGED_MAX_REP == PAGED_MAX_REP, "limits");
 
 constexpr long long MAX_POSITIONS = 1LL << 30;  // positions a block table row can address
@@ -528,51 +529,37 @@ int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_he
     return one_launch(stream, [&](cudaStream_t) { return launch_paged_decode(p, s); });
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  SharedPrefixParams a{};
-  a.q = p.q;
-  a.B = B;
-  a.G = G;
-  a.n_heads = n_heads;
-  a.n_kv = p.n_kv;
-  a.start = start_pos;
-  a.cu = cu_groups;
-  a.prefix = prefix_rows;
-  a.pages = p.pages;
-  a.scale_log2 = p.scale_log2;
-  a.part_o = reinterpret_cast<float*>(ws + PREFIX_O_OFFSET);
-  a.part_ml = reinterpret_cast<float*>(ws + PREFIX_ML_OFFSET);
-  a.rows = reinterpret_cast<SharedRow*>(ws + SHARED_ROWS_OFFSET);
-  a.plan = reinterpret_cast<SharedPlan*>(ws + SHARED_PLAN_OFFSET);
-  a.status = p.status;
-  a.wait_ns = wait_limit_ns();
-  a.ctas = p.ctas;
-  p.shared = a.rows;
   p.own_o = reinterpret_cast<float*>(ws + OWN_O_OFFSET);
   p.own_ml = reinterpret_cast<float*>(ws + OWN_ML_OFFSET);
+  SharedDecodeParams a{};
+  a.own = p;
+  a.G = G;
+  a.cu = cu_groups;
+  a.prefix = prefix_rows;
+  a.part_o = reinterpret_cast<float*>(ws + PREFIX_O_OFFSET);
+  a.part_ml = reinterpret_cast<float*>(ws + PREFIX_ML_OFFSET);
+  a.rows = reinterpret_cast<SharedParts*>(ws + SHARED_PARTS_OFFSET);
+  a.wait_ns = wait_limit_ns();
   SharedJoinParams j{};
-  j.B = B;
-  j.n_heads = n_heads;
-  j.n_kv = p.n_kv;
-  j.start = start_pos;
+  j.pairs = B * p.n_kv;
+  j.n_rep = n_rep;
   j.rows = a.rows;
-  j.plan = a.plan;
-  j.part_o = a.part_o;
+  j.parts = a.part_o;
   j.part_ml = a.part_ml;
   j.part_rows = PREFIX_ROWS;
-  j.own_o = p.own_o;
+  j.own_rows = OWN_ROWS;
   j.own_ml = p.own_ml;
+  j.own_at = static_cast<int>((OWN_O_OFFSET - PREFIX_O_OFFSET) / 16);
   j.out = p.out;
   PackedPrefillMaps maps;
   if (!attention_maps(maps, q, q_stride, B, n_heads, p.n_kv, p.pages, p.pages.row_stride, pages->page_size,
                       pages->num_pages, prefill_box_rows(pages->page_size)))
     return fail_cuda(cudaErrorInvalidValue);
   prof_mark(0, s);
-  int e = launched(launch_shared_prefix(maps, a, s));
+  int e = launched(launch_shared_decode(maps, a, s));
   prof_mark(1, s);
-  if (e == GQA_OK) e = launched(launch_paged_decode(p, s));
-  prof_mark(2, s);
   if (e == GQA_OK) e = launched(launch_shared_join(j, s));
-  prof_mark(3, s);
+  prof_mark(2, s);
   return e;
 }
 

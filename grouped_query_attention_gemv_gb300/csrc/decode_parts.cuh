@@ -82,20 +82,28 @@ __device__ __forceinline__ void rescale(float& m, float mx, float& l, float4& o)
   o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
 }
 
+// Zeros for all heads of sequence b, by the whole CTA.
+__device__ __forceinline__ void zero_rows(__nv_bfloat16* out, int b, int n_heads) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n_heads * (HEAD_DIM / 8); i += blockDim.x)
+    reinterpret_cast<uint4*>(out + static_cast<long long>(b) * n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // Static shared memory of a CTA.
+constexpr int MAX_WARPS = 11;
 struct Shared {
   Part parts[2 * WARPS];  // each warp's two, first = -1: none
-  int warp_sum[WARPS], warp_max[WARPS];
+  int warp_sum[MAX_WARPS], warp_max[MAX_WARPS];
   int is_last[2];
   Part joint[2];  // of the shared segments: first and last CTA, first output row
 };
 
 // Chunks of the batch per KV head, and of its longest sequence; pre[0..B] gets
-// their prefix sums. chunks(b): those of sequence b.
+// their prefix sums. chunks(b): those of sequence b. By a CTA of W warps.
 struct Count {
   int total, longest;
 };
-template <class Chunks>
+template <int W, class Chunks>
 __device__ __forceinline__ Count count_chunks(Shared& sh, int* pre, int B, Chunks chunks) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (B + blockDim.x - 1) / blockDim.x;
@@ -122,7 +130,7 @@ __device__ __forceinline__ Count count_chunks(Shared& sh, int* pre, int B, Chunk
   __syncthreads();
   run -= sum;
   Count c{0, 0};
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w == warp) run += c.total;
     c.total += sh.warp_sum[w];
     c.longest = max(c.longest, sh.warp_max[w]);
@@ -136,24 +144,24 @@ __device__ __forceinline__ Count count_chunks(Shared& sh, int* pre, int B, Chunk
   return c;
 }
 
-// Chunks [c0, c1) of this CTA (total: of the batch, KV heads included); false:
-// it has none. One CTA per (sequence, KV head) instead of equal ranges where
+// Chunks [c0, c1) of CTA `cta` of `grid` (total: of the batch, KV heads
+// included; ctas: with a range, of equal ones); false: it has none. One CTA per (sequence, KV head) instead of equal ranges where
 // that costs less than joining parts across CTAs.
-__device__ __forceinline__ bool cta_range(int total, int longest, const Split& split, int ctas, const int* pre, int B,
-                                          int n_kv, int& c0, int& c1) {
+__device__ __forceinline__ bool cta_range(int total, int longest, const Split& split, int ctas, int cta, int grid,
+                                          const int* pre, int B, int n_kv, int& c0, int& c1) {
   const float memory = static_cast<float>(total);
-  const bool own = B * n_kv <= static_cast<int>(gridDim.x) &&
+  const bool own = B * n_kv <= grid &&
                    fmaxf(static_cast<float>(longest) * ALONE, memory) <=
                        fmaxf(static_cast<float>(split.each) * ALONE, memory) + JOIN_COST;
   if (own) {
-    if (static_cast<int>(blockIdx.x) >= B * n_kv) return false;
-    const int b = blockIdx.x / n_kv, h = blockIdx.x - b * n_kv, n = pre[b + 1] - pre[b];
+    if (cta >= B * n_kv) return false;
+    const int b = cta / n_kv, h = cta - b * n_kv, n = pre[b + 1] - pre[b];
     c0 = pre[b] * n_kv + h * n;
     c1 = c0 + n;
   } else {
-    if (static_cast<int>(blockIdx.x) >= ctas) return false;
-    c0 = split.start(blockIdx.x);
-    c1 = split.start(blockIdx.x + 1);
+    if (cta >= ctas) return false;
+    c0 = split.start(cta);
+    c1 = split.start(cta + 1);
   }
   return true;
 }
@@ -166,7 +174,7 @@ __device__ __forceinline__ bool cta_range(int total, int longest, const Split& s
 // floats of it are used once the parts are read; finish(row, o, m, l): takes a
 // finished row's 4 dims of each lane, by a whole warp.
 template <class PartAt, class Finish>
-__device__ __forceinline__ void join_parts(Shared& sh, float* work, const Split& split, int c0, int c1, int n_rep,
+__device__ __forceinline__ void join_parts(Shared& sh, float* work, const Split& split, int cta, int c0, int c1, int n_rep,
                                            float* part_o, float* part_ml, int* tickets, PartAt part_at, Finish finish) {
   constexpr int W = WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,7 +224,7 @@ __device__ __forceinline__ void join_parts(Shared& sh, float* work, const Split&
         if (side == 2) {
           finish(seg.row + r, o, m, l);
         } else {
-          const long long at = (2LL * blockIdx.x + side) * n_rep + r;
+          const long long at = (2LL * cta + side) * n_rep + r;
           __stcg(reinterpret_cast<float4*>(part_o + at * HEAD_DIM) + lane, o);
           if (lane == 0) __stcg(reinterpret_cast<float2*>(part_ml) + at, make_float2(m, l));
         }

@@ -112,21 +112,21 @@ struct Fp8ReadParams {
 };
 cudaError_t launch_fp8_read(const Fp8ReadParams& p, cudaStream_t s);
 
-// The rows of a sequence that shares its first ones with others: `first` of
-// them; the parts of theirs (shared_prefix.cu): of KV head g at rows base + g
-// kv_rows + 256 x CTA, `span` of them, its own from `at` on, by the CTAs that
-// hold the units behind unit0 + g kv_units + ITEM_UNITS, before unit0 + g
-// kv_units + w. w 0: it shares none, first is 0.
-struct SharedRow {
-  int first, w, kv_units, unit0, kv_rows, base, span, at;
-};
-struct SharedPlan {
-  int units, parts;
+// The parts (paged_decode_shared.cu) of a sequence's KV head in a batch with
+// shared rows: `prefixes` of those that it shares, 256 rows apart from row
+// `prefix` on, `span` rows in each and its own from `at` on; `owns` of its own
+// rows, n_rep rows apart from row `own` on.
+struct SharedParts {
+  int prefix, prefixes, span, at, own, owns, unused[2];
 };
 constexpr int SHARED_MAX_GROUPS = 1024;  // groups that are looked at
-constexpr int SHARED_MAX_ROWS = 32768;   // query rows of a batch that shares (the workspace's room)
-// Cache rows (of one KV head) that sharing has to save, or it is not done.
-constexpr unsigned long long SHARED_LEAST_ROWS = 100000;
+constexpr int SHARED_MAX_ROWS = 28672;   // query rows of a batch that shares (the workspace's room)
+// Cache rows (of one KV head) that sharing has to save, or it is not done. It
+// takes 15 us at least, of which 5 to plan and 5 to join. Measured, plain and
+// shared, own rows 64: 122,880 rows saved (16 sequences under 1,024 rows, 8 KV
+// heads) 12.9 and 18.2 us, 131,072 (2 under 16,384) 21.2 and 26.1, 393,216 (4
+// under 16,384) 33.3 and 26.0, 491,520 (16 under 4,096) 34.2 and 19.8.
+constexpr unsigned long long SHARED_LEAST_ROWS = 200000;
 
 // One new token per sequence over the pages.
 struct PagedDecodeParams {
@@ -142,36 +142,26 @@ struct PagedDecodeParams {
   int* tickets;             // [ctas], zero-filled, left zero-filled
   int* status;
   int ctas;
-  // sequences that share their first rows: the rows that are read begin behind
-  // those, and what comes out is a part (own_o, own_ml); null: none shares
-  const SharedRow* shared;
-  float *own_o, *own_ml;
+  float *own_o, *own_ml;  // of rows that are part of a whole (SharedDecodeParams)
 };
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, cudaStream_t s);
 
-// The first part of an attention with shared rows: plan and prefixes.
-struct SharedPrefixParams {
-  const __nv_bfloat16* q;
-  int B, G, n_heads, n_kv;
-  const int *start, *cu, *prefix;
-  PagedCache pages;
-  float scale_log2;
-  float *part_o, *part_ml;  // rows of parts: O [32 column groups][span][4], (max in log2 units, sum)
-  SharedRow* rows;          // [B]
-  SharedPlan* plan;
-  int* status;
+// An attention with shared rows: prefixes and own rows. own: pages, queries and
+// what streams the own rows; own_o, own_ml: their parts.
+struct SharedDecodeParams {
+  PagedDecodeParams own;
+  int G;
+  const int *cu, *prefix;
+  float *part_o, *part_ml;  // rows of the prefixes' parts: O [32 column groups][span][4], (max in log2 units, sum)
+  SharedParts* rows;        // [B][n_kv]
   unsigned long long wait_ns;
-  int ctas;
 };
-// The last part: the join.
+// Its join.
 struct SharedJoinParams {
-  int B, n_heads, n_kv;
-  const int* start;
-  const SharedRow* rows;
-  const SharedPlan* plan;
-  const float *part_o, *part_ml;
-  int part_rows;
-  const float *own_o, *own_ml;  // of each query row: O [128], (max in log2 units, sum)
+  int pairs, n_rep, sets;  // (sequence, KV head) pairs; sets: of rows in a pair
+  const SharedParts* rows;
+  const float *parts, *part_ml, *own_ml;  // parts: the prefixes' O, and own_at groups of 4 floats behind, the own rows'
+  int part_rows, own_rows, own_at;
   __nv_bfloat16* out;
 };
 
@@ -231,7 +221,7 @@ __host__ __device__ constexpr int prefill_box_rows(int page_size) { return page_
 cudaError_t launch_packed_prefill(const PackedPrefillMaps& maps, const PackedPrefillParams& p, cudaStream_t s);
 // With p.joins set, the join follows.
 cudaError_t launch_packed_prefill_join(const PackedPrefillParams& p, cudaStream_t s);
-cudaError_t launch_shared_prefix(const PackedPrefillMaps& maps, const SharedPrefixParams& p, cudaStream_t s);
+cudaError_t launch_shared_decode(const PackedPrefillMaps& maps, const SharedDecodeParams& p, cudaStream_t s);
 cudaError_t launch_shared_join(const SharedJoinParams& p, cudaStream_t s);
 long long shared_most_units(int B, int n_rep, int n_kv, long long keys);
 bool packed_prefill_may_join(int N, int n_rep, long long most_keys);

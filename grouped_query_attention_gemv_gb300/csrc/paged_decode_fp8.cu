@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   pdl_trigger();
   pdl_wait();
   // chunks per sequence, prefix-summed; unused slots and bad positions have none
-  const Count count = count_chunks(sh, pre, p.B, [&](int b) {
+  const Count count = count_chunks<WARPS>(sh, pre, p.B, [&](int b) {
     const int s = p.start[b];
     const bool ok = s >= 0 && s < p.pages.capacity();
     if (!ok && s != -1 && blockIdx.x == 0) report(p.status, DEV_BAD_POSITION);
@@ -89,17 +89,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   // rows of sequences without keys
 #pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (pre[b + 1] == pre[b])
-#pragma unroll 1
-      for (int i = threadIdx.x; i < p.n_heads * (HEAD_DIM / 8); i += blockDim.x)
-        reinterpret_cast<uint4*>(p.out + static_cast<long long>(b) * p.n_heads * HEAD_DIM)[i] = make_uint4(0, 0, 0, 0);
+    if (pre[b + 1] == pre[b]) zero_rows(p.out, b, p.n_heads);
 
   const int total = count.total * p.n_kv;
   if (total == 0) return;
   const int ctas = decode_ctas(total, gridDim.x, W);
   const Split split(total, ctas);
   int c0, c1;
-  if (!cta_range(total, count.longest, split, ctas, pre, p.B, p.n_kv, c0, c1)) return;
+  if (!cta_range(total, count.longest, split, ctas, blockIdx.x, gridDim.x, pre, p.B, p.n_kv, c0, c1)) return;
   const int a0 = warp_start(c0, c1, warp, W), a1 = warp_start(c0, c1, warp + 1, W);
   const int n = a1 - a0;
 
@@ -365,7 +362,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   }
   __syncthreads();
   join_parts(
-      sh, reinterpret_cast<float*>(smem), split, c0, c1, n_rep, p.part_o, p.part_ml, p.tickets,
+      sh, reinterpret_cast<float*>(smem), split, blockIdx.x, c0, c1, n_rep, p.part_o, p.part_ml, p.tickets,
       [&](int e) -> const float* {
         return (e & 1) ? reinterpret_cast<const float*>(smem + (e >> 1) * (STAGES * STAGE_BYTES))
                        : stash + (e >> 1) * n_rep * PART;

@@ -1,10 +1,8 @@
 // Attention of one new token per sequence for groups of sequences that share
 // their first rows ("Llama 3.1 8B · Grouped-query attention", mode decode): the
 // shared rows are read once for a group instead of once for each of its
-// sequences, the rows of its own are streamed for each (paged_decode.cu), and
-// the parts, each an O, a max and a sum, are joined by the log-sum-exp rule.
-// Three launches: the prefix kernel, which also plans, the streaming of own
-// rows, the join.
+// sequences, the rows of its own are streamed for each, and the parts, each an
+// O, a max and a sum, are joined by the log-sum-exp rule.
 //
 // The prefix part is matrix-shaped: members x n_rep query rows of a KV head
 // against the prefix's keys, 4 x 128 flops a pair, so it runs on the
@@ -20,11 +18,16 @@
 //     either grows by what the last one took, so that no two meet.
 //   * All rows of a Q tile see all keys, so only the last tile is masked, and
 //     value rows behind the prefix are cleared in shared memory.
+// The own rows are bound by memory and streamed as in paged_decode.cu
+// (decode_stream.cuh). One kernel does both: some of its CTAs, one per SM, take
+// the prefixes, the others the own rows, as many each as makes both end
+// together by measured costs; every CTA plans alike. A second kernel joins.
 // Which sequences share: those of a group that see all of its prefix
 // (start_pos + 1 >= prefix_rows), if there are two at least and sharing saves
 // enough bytes. The others are streamed from their row 0 on, in rows of the Q
 // tiles that nobody reads.
 //
+// Warps of a CTA with prefixes:
 //   warp 8        TMA producer: 128 / min(page, 128) boxes a tile, one lane each
 //   warps 9, 10   MMA issuers, one per Q tile
 //   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
@@ -34,8 +37,7 @@
 // frees TMEM before the CTA exits.
 #include <math.h>
 
-#include "decode_parts.cuh"
-#include "paged.h"
+#include "decode_stream.cuh"
 
 namespace gqa {
 
@@ -56,9 +58,21 @@ constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
 constexpr int BARS_BYTES = 1024;
 constexpr int PLAN_OFF = BAR_OFF + BARS_BYTES;
 constexpr int PLAN_ARRAY = SHARED_MAX_GROUPS + 1;
-constexpr int SMEM_BYTES = PLAN_OFF + 4 * PLAN_ARRAY * 4 + 1024;
+constexpr int SMEM_BYTES = PLAN_OFF + 5 * PLAN_ARRAY * 4 + 1024;
 constexpr int THREADS = 352;
+// Shared memory of a CTA with own rows: four numbers of each sequence, then the
+// warps' rings.
+__host__ __device__ constexpr int own_ints(int B) { return ((4 * B + 1) * 4 + 127) / 128 * 128; }
+static_assert(own_ints(PAGED_MAX_SEQS) <= K_OFF &&
+              own_ints(PAGED_MAX_SEQS) + decode::WARPS * decode::RING_BYTES <= BAR_OFF, "the plan is not in the way");
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+// Costs in us: a key tile (or unit) of an item with one and with two Q tiles,
+// a chunk of own rows by a CTA alone and by the whole memory, and what a CTA of
+// either kind takes beside.
+constexpr float ONE_TILE = 2.f, TWO_TILES = 1.6f, CHUNK = 0.15f, CHUNK_MEMORY = 1.f / 750, PREFIX_MORE = 9.f,
+                OWN_MORE = 5.f;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
+constexpr int AHEAD = 16;                       // key tiles that are asked for ahead of their copies at most
 constexpr int SLOTS = 2;                        // items handed from the producer to the other warps
 constexpr uint32_t TMEM_COLS = 512;
 // TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
@@ -71,6 +85,8 @@ constexpr float RESCALE_LOG2 = 8.f;
 struct Item {
   int g, seq0, nseq, lead, end, j0, n;
   int base;
+  // key tiles of Q tile t (qp: sequences per Q tile)
+  __device__ __forceinline__ int tiles(int t, int qp) const { return nseq > t * qp ? n : 0; }
 };
 
 struct Bars {
@@ -86,10 +102,11 @@ struct Bars {
   int q_issued[NQ], k_issued, v_issued;
   int warp_sum[THREADS / 32][2];
   unsigned long long saved;    // rows that sharing saves
+  unsigned long long tiles[2]; // units of items with one and with two Q tiles
+  unsigned long long best;     // least cost (float bits) << 32 | CTAs with prefixes
   Item item[SLOTS];            // g < 0: no more
 };
 static_assert(sizeof(Bars) <= BARS_BYTES, "barrier block");
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool aborted(const Bars& bs) { return *reinterpret_cast<const volatile int*>(&bs.abort) != 0; }
 
@@ -119,23 +136,31 @@ struct ItemWalk {
   }
 };
 
-// The groups in shared memory: sequences cu[g] .. cu[g+1]-1; of those that
-// share, the first that sees the whole prefix, and prefix sums of the units of
-// one KV head and of the query rows of one KV head (no step: does not share).
+// The groups in shared memory: sequences cu[g] .. cu[g+1]-1, the rows that they
+// share; of those that do, the first that sees them all, and prefix sums of
+// the units of one KV head and of the query rows of one KV head (no step: does
+// not share).
 struct Groups {
-  int *cu, *lead, *units, *rows;
+  int *cu, *prefix, *lead, *units, *rows;
 };
 
 __device__ __forceinline__ int tiles_of(int prefix) { return ceil_div(prefix, KT); }
 
+template <int NT>
 __global__ void __launch_bounds__(THREADS, 1)
-    shared_prefix_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                         const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedPrefixParams a) {
+    shared_decode_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mv, const __grid_constant__ SharedDecodeParams sp) {
+  const PagedDecodeParams& a = sp.own;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bs = *reinterpret_cast<Bars*>(smem + BAR_OFF);
+  __shared__ decode::Shared sh;
   int* plan = reinterpret_cast<int*>(smem + PLAN_OFF);
-  const Groups gs{plan, plan + PLAN_ARRAY, plan + 2 * PLAN_ARRAY, plan + 3 * PLAN_ARRAY};
+  const Groups gs{plan, plan + PLAN_ARRAY, plan + 2 * PLAN_ARRAY, plan + 3 * PLAN_ARRAY, plan + 4 * PLAN_ARRAY};
+  // of each sequence: chunks of own rows before it, its last row, its first own
+  // one, its group (-1: it does not share)
+  int* pre = reinterpret_cast<int*>(smem);
+  int *last = pre + a.B + 1, *begin = last + a.B, *group = begin + a.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int nrep = a.n_heads / a.n_kv;
   const int qp = ROWS / nrep;  // sequences per Q tile
@@ -160,72 +185,79 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(smem_u32(&bs.item_empty[s]), 10);  // issuers, softmax warps
     }
     bs.abort = 0;
-    bs.wait_ns = a.wait_ns;
+    bs.wait_ns = sp.wait_ns;
     bs.q_issued[0] = bs.q_issued[1] = 0;
     bs.k_issued = bs.v_issued = 0;
-    bs.saved = 0;
+    bs.saved = bs.tiles[0] = bs.tiles[1] = 0;
+    bs.best = ~0ull;
     fence_barrier_init();
-  }
-  if (warp == MMA_WARP) {
-    tmem_alloc(smem_u32(&bs.tmem_slot), TMEM_COLS);
-    tmem_relinquish();
   }
   // nothing in global memory is read or written before the previous kernel of
   // the stream is done
   pdl_trigger();
   pdl_wait();
 
-  // ---- the plan. Members of each group (counted where K tiles will lie) and
-  // the first of them.
+  // ---- the plan, from one look at what it takes. Members of each group
+  // (counted where K tiles will lie) and the first of them.
   int* members = reinterpret_cast<int*>(smem + K_OFF);
+#pragma unroll 1
+  for (int b = tid; b < a.B; b += THREADS) last[b] = a.start[b];
   bool bad = false;
-  for (int g = tid; g <= a.G; g += THREADS) {
-    const int c = a.cu[g];
+#pragma unroll 1
+  for (int g = tid; g <= sp.G; g += THREADS) {
+    const int c = sp.cu[g];
     gs.cu[g] = c;
-    bad |= c < 0 || c > a.B || (g > 0 && a.cu[g - 1] > c);
-    if (g < a.G) {
+    bad |= c < 0 || c > a.B || (g < sp.G && c > sp.cu[g + 1]);
+    if (g < sp.G) {
+      gs.prefix[g] = sp.prefix[g];
       members[g] = 0;
       gs.lead[g] = a.B;
     }
   }
   bad = __syncthreads_or(bad);
   if (bad && blockIdx.x == 0 && tid == 0) report(a.status, DEV_BAD_POSITION);
-  // the group of sequence b whose prefix it sees whole, or -1
-  auto group_of = [&](int b) {
-    if (bad || b < gs.cu[0] || b >= gs.cu[a.G]) return -1;
-    int lo = 0, hi = a.G;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (gs.cu[mid] <= b) lo = mid; else hi = mid;
-    }
-    const int s = a.start[b], p = a.prefix[lo];
-    return p > 0 && s >= p - 1 && s < a.pages.capacity() ? lo : -1;
-  };
+  // the group of a sequence whose prefix it sees whole, or -1
+#pragma unroll 1
   for (int b = tid; b < a.B; b += THREADS) {
-    const int g = group_of(b);
-    if (g >= 0) {
-      atomicAdd(&members[g], 1);
-      atomicMin(&gs.lead[g], b);
+    int g = -1;
+    if (!bad && b >= gs.cu[0] && b < gs.cu[sp.G]) {
+      int lo = 0, hi = sp.G;
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (gs.cu[mid] <= b) lo = mid; else hi = mid;
+      }
+      const int p = gs.prefix[lo];
+      if (p > 0 && last[b] >= p - 1 && last[b] < a.pages.capacity()) {
+        g = lo;
+        atomicAdd(&members[g], 1);
+        atomicMin(&gs.lead[g], b);
+      }
     }
+    group[b] = g;
   }
   __syncthreads();
   {
-    const int per = ceil_div(a.G, THREADS);
-    const int g0 = min(tid * per, a.G), g1 = min(g0 + per, a.G);
+    const int per = ceil_div(sp.G, THREADS);
+    const int g0 = min(tid * per, sp.G), g1 = min(g0 + per, sp.G);
     unsigned long long saved = 0;
+#pragma unroll 1
     for (int g = g0; g < g1; ++g)
-      if (members[g] > 1) saved += static_cast<unsigned long long>(members[g] - 1) * a.prefix[g];
+      if (members[g] > 1) saved += static_cast<unsigned long long>(members[g] - 1) * gs.prefix[g];
     if (saved) atomicAdd(&bs.saved, saved);
     __syncthreads();
     const bool shares = bs.saved * a.n_kv >= SHARED_LEAST_ROWS;
     int sum[2] = {0, 0};
+#pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       const int size = gs.cu[g + 1] - gs.cu[g];
       const bool on = shares && members[g] > 1;
-      gs.units[g + 1] = on ? ceil_div(size, NQ * qp) * (tiles_of(a.prefix[g]) + ITEM_UNITS) : 0;
+      const int units = on ? ceil_div(size, NQ * qp) * (tiles_of(gs.prefix[g]) + ITEM_UNITS) : 0;
+      gs.units[g + 1] = units;
       gs.rows[g + 1] = on ? size * nrep : 0;
-      sum[0] += gs.units[g + 1];
+      sum[0] += units;
       sum[1] += gs.rows[g + 1];
+      if (on) atomicAdd(&bs.tiles[size > qp], static_cast<unsigned long long>(units));
     }
     int run[2] = {sum[0], sum[1]};
 #pragma unroll
@@ -242,8 +274,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       run[k] -= sum[k];
+#pragma unroll 1
       for (int w = 0; w < warp; ++w) run[k] += bs.warp_sum[w][k];
     }
+#pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       run[0] += gs.units[g + 1];
       run[1] += gs.rows[g + 1];
@@ -251,34 +285,96 @@ __global__ void __launch_bounds__(THREADS, 1)
       gs.rows[g + 1] = run[1];
     }
   }
-  fence_proxy_async_smem();  // K tiles come where the members were counted
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const int units = gs.units[a.G] * a.n_kv;
-  const int parts = units ? range_count(units, mean_range(units, gridDim.x), gridDim.x) : 1;
-  // what the own rows' kernel and the join need of it
-  if (blockIdx.x == 0 && tid == 0) {
-    a.plan->units = units;
-    a.plan->parts = parts;
+  const int units = gs.units[sp.G] * a.n_kv;
+  // the own rows' chunks
+  const decode::Count count = decode::count_chunks<THREADS / 32>(sh, pre, a.B, [&](int b) {
+    const int s = last[b], g = group[b];
+    const bool ok = s >= 0 && s < a.pages.capacity();
+    if (!ok && s != -1 && blockIdx.x == 0) report(a.status, DEV_BAD_POSITION);
+    const bool shares = g >= 0 && gs.units[g + 1] > gs.units[g];
+    const int first = shares ? gs.prefix[g] : 0;
+    if (!shares) group[b] = -1;
+    begin[b] = first;
+    return ok && s >= first ? s / decode::KEYS - first / decode::KEYS + 1 : 0;
+  });
+  // rows of sequences without keys
+#pragma unroll 1
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+    if (pre[b + 1] == pre[b] && begin[b] == 0) decode::zero_rows(a.out, b, a.n_heads);
+  // how many CTAs take prefixes: thread n looks at n of them
+  const int chunks = count.total * a.n_kv, grid = gridDim.x;
+  if (units > 0 && warp * 32 <= grid) {
+    const float tile = static_cast<float>(bs.tiles[0]) * ONE_TILE + static_cast<float>(bs.tiles[1]) * TWO_TILES;
+    float cost = INFINITY;
+    if (tid > 0 && tid <= grid && (tid < grid || chunks == 0)) {
+      const float own = chunks > 0 ? fmaxf(chunks * CHUNK / (grid - tid), chunks * CHUNK_MEMORY) + OWN_MORE : 0.f;
+      cost = fmaxf(tile * a.n_kv / tid + PREFIX_MORE, own);
+    }
+    const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
+    const unsigned who = __ballot_sync(0xffffffffu, __float_as_uint(cost) == least);
+    if (lane == 0) atomicMin(&bs.best, static_cast<unsigned long long>(least) << 32 | (tid + __ffs(who) - 1));
   }
-  for (int b = tid; b < a.B; b += THREADS) {
-    if (static_cast<int>(blockIdx.x) != (b >> 5) % static_cast<int>(gridDim.x)) continue;
-    SharedRow r = {};
-    const int g = group_of(b);
-    if (g >= 0 && gs.units[g + 1] > gs.units[g]) {
-      const int i = b - gs.cu[g], e = i / (NQ * qp), size = gs.cu[g + 1] - gs.cu[g];
-      r.first = a.prefix[g];
-      r.w = tiles_of(r.first) + ITEM_UNITS;
-      r.kv_units = gs.units[g + 1] - gs.units[g];
-      r.unit0 = gs.units[g] * a.n_kv + e * r.w;
-      r.kv_rows = size * nrep;
-      r.base = gs.rows[g] * a.n_kv + e * NQ * qp * nrep;
+  fence_proxy_async_smem();  // tiles come where the counts lie
+  __syncthreads();
+  const int most = units ? static_cast<int>(bs.best & 0xffffffffu) : 0;
+  const int parts = units ? range_count(units, mean_range(units, most), most) : 0;  // CTAs with prefixes
+  const int own_ctas = chunks ? full_ctas(chunks, grid - parts, decode::WARPS) : 0;
+  // where the parts of a sequence's KV head will lie, for the join
+  auto tell = [&](int pair) {
+    const int b = pair / a.n_kv, h = pair - b * a.n_kv, g = group[b];
+    SharedParts r = {};
+    if (g >= 0) {
+      const int i = b - gs.cu[g], size = gs.cu[g + 1] - gs.cu[g], e = i / (NQ * qp), w = tiles_of(gs.prefix[g]) + ITEM_UNITS;
+      const int unit = gs.units[g] * a.n_kv + h * (gs.units[g + 1] - gs.units[g]) + e * w;
+      const Split split(units, parts);
+      const int c0 = split.holder(unit + ITEM_UNITS);
+      r.prefixes = split.holder(unit + w - 1) - c0 + 1;
+      r.prefix = gs.rows[g] * a.n_kv + (h * size + e * NQ * qp) * nrep + NQ * ROWS * c0;
       r.span = min(NQ * qp, size - e * NQ * qp) * nrep;
       r.at = (i - e * NQ * qp) * nrep;
     }
-    a.rows[b] = r;
+    const int n = pre[b + 1] - pre[b];
+    if (n > 0) {
+      const int first = pre[b] * a.n_kv + h * n;
+      const WarpSpan w = warps_of(first, first + n, Split(chunks, own_ctas), least(decode::WARPS, chunks));
+      r.own = (pair + w.first) * nrep;
+      r.owns = w.last - w.first + 1;
+    }
+    sp.rows[pair] = r;
+  };
+  const int pairs = a.B * a.n_kv;
+  if (static_cast<int>(blockIdx.x) >= parts) {
+    // ---- own rows
+    const int cta = blockIdx.x - parts;
+    if (warp >= decode::WARPS) {
+      // the warps that stream nothing
+      constexpr int FREE = THREADS - decode::WARPS * 32;
+#pragma unroll 1
+      for (int p = cta * FREE + tid - decode::WARPS * 32; p < pairs; p += (grid - parts) * FREE) tell(p);
+      return;
+    }
+    if (cta >= own_ctas) return;
+    const Split split(chunks, own_ctas);
+    decode::stream_chunks<NT, true>(a, sh, smem + own_ints(a.B), nullptr, pre, last, begin, split, cta, split.start(cta),
+                                    split.start(cta + 1));
+    return;
   }
+  if (parts == grid) {
+#pragma unroll 1
+    for (int p = blockIdx.x * THREADS + tid; p < pairs; p += grid * THREADS) tell(p);
+    // tiles come where the numbers lie
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+  // ---- prefixes
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&bs.tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = bs.tmem_slot;
   const uint32_t sbase = smem_u32(smem);
   ItemWalk walk;
@@ -286,18 +382,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (warp == PRODUCER_WARP) {
     const Split split(units, parts);
-    const bool ranged = static_cast<int>(blockIdx.x) < parts;
-    int ru = ranged ? split.start(blockIdx.x) : 0;
-    const int rend = ranged ? split.start(blockIdx.x + 1) : 0;
+    int ru = split.start(blockIdx.x);
+    const int rend = split.start(blockIdx.x + 1);
     // units in (group, KV head, pair of Q tiles, key tile) order; this CTA's range of them
     auto next_item = [&](Item& x) {
       while (ru < rend) {
-        int lo = 0, hi = a.G;
+        int lo = 0, hi = sp.G;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (gs.units[mid] * a.n_kv <= ru) lo = mid; else hi = mid;
         }
-        const int size = gs.cu[lo + 1] - gs.cu[lo], w = tiles_of(a.prefix[lo]) + ITEM_UNITS;
+        const int size = gs.cu[lo + 1] - gs.cu[lo], w = tiles_of(gs.prefix[lo]) + ITEM_UNITS;
         const int pairs = ceil_div(size, NQ * qp), in_group = ru - gs.units[lo] * a.n_kv;
         const int item = in_group / w, in = in_group - item * w, base = ru - in, end = min(rend, base + w);
         const int e = item % pairs;
@@ -305,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         x.seq0 = gs.cu[lo] + e * NQ * qp;
         x.nseq = min(NQ * qp, size - e * NQ * qp);
         x.lead = gs.lead[lo];
-        x.end = a.prefix[lo];
+        x.end = gs.prefix[lo];
         x.j0 = max(0, in - ITEM_UNITS);
         x.n = max(0, end - base - ITEM_UNITS - x.j0);
         x.base = gs.rows[lo] * a.n_kv + (x.g * size + e * NQ * qp) * nrep + NQ * ROWS * static_cast<int>(blockIdx.x);
@@ -359,20 +454,42 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = false;
         break;
       }
+      // Pages of a window of 32 / boxes tiles, a box a lane, and of the next one.
+      const int window = 32 / boxes, ahead = min(AHEAD, window), my_tile = lane / boxes, my_box = lane - my_tile * boxes;
+      const int in_page = (1 << a.pages.page_shift) - 1;
+      const int* table = a.pages.table + static_cast<long long>(it.lead) * a.pages.table_stride;
+      const int keys = min(it.end, (it.j0 + it.n) * KT);  // behind the item's
+      auto first_key = [&](int j) { return (it.j0 + j) * KT + my_box * box; };
+      auto look_up = [&](int j) {  // the window that begins with tile j
+        const int key = first_key(j + my_tile);
+        return key < keys ? table[key >> a.pages.page_shift] : -1;
+      };
+      // The tiles are asked for well ahead of their copies: these have two stages
+      // to wait in, not enough for the memory's latency beside the own rows' stream.
+      auto ask = [&](int j, int page) {
+        const int row = first_key(j) & in_page;
+        if (first_key(j) >= keys || page < 0 || page >= a.pages.num_pages) return;
+        tma_prefetch_4d(&mk, 0, it.g, row, page);
+        tma_prefetch_4d(&mk, 64, it.g, row, page);
+        tma_prefetch_4d(&mv, 0, it.g, row, page);
+        tma_prefetch_4d(&mv, 64, it.g, row, page);
+      };
+      int pages = 0, next_pages = look_up(0);
       for (int j = 0; j < it.n && !stop; ++j, ++u) {
-        const int s = u % STAGES;
+        const int s = u % STAGES, in_window = j % window;
+        if (in_window == 0) {
+          pages = next_pages;
+          next_pages = look_up(j + window);
+        }
         // boxes of the tile that hold keys of the prefix; this lane's
         const int held = min(boxes, (it.end - (it.j0 + j) * KT + box - 1) / box);
-        const int key = (it.j0 + j) * KT + lane * box;
-        const int row = key & ((1 << a.pages.page_shift) - 1);
-        int page = 0;
-        if (lane < held)
-          page = a.pages.table[static_cast<long long>(it.lead) * a.pages.table_stride + (key >> a.pages.page_shift)];
+        const int row = ((it.j0 + j) * KT + lane * box) & in_page;
+        int page = __shfl_sync(0xffffffffu, pages, (in_window * boxes + lane) & 31);
         if (u >= STAGES && !go_on(bs.k_empty[s], (u / STAGES - 1) & 1)) {
           stop = true;
           break;
         }
-        if (page < 0 || page >= a.pages.num_pages) {
+        if (lane < held && (page < 0 || page >= a.pages.num_pages)) {
           report(a.status, DEV_BAD_PAGE);
           page = 0;
         }
@@ -383,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // that read it has completed
 #pragma unroll
           for (int t = 0; t < NQ; ++t) {
-            if (stop || it.nseq <= t * qp) continue;
+            if (stop || it.tiles(t, qp) == 0) continue;
             if (cs[t] > 0 && !go_on(bs.s_full[t], (cs[t] - 1) & 1)) {
               stop = true;
               continue;
@@ -406,9 +523,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         copy(&mv, bs.v_full[s], sbase + V_OFF + s * KV_TILE, held, it.g, row, page);
         vn = u + 1;
+        if (j == 0 && my_tile >= STAGES && my_tile < ahead) ask(my_tile, pages);
+        const int x = in_window + ahead;
+        if (x % window == my_tile) ask(j + ahead, x < window ? pages : next_pages);
+        __syncwarp();
       }
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) cs[t] += it.nseq > t * qp ? it.n : 0;
+      for (int t = 0; t < NQ; ++t) cs[t] += it.tiles(t, qp);
     }
     if (ok && !stop) {
       it.g = -1;
@@ -448,7 +569,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     };
     while (ok && walk.next(bs, it)) {
-      const int n_t = it.nseq > t * qp ? it.n : 0;
+      const int n_t = it.tiles(t, qp);
       for (int j = 0; j <= it.n; ++j, ++step) {
         // everything S_j needs but its turn, so that it follows P_{j-1} V_{j-1} at once
         const unsigned uk = u0 + j, sk = uk % STAGES;
@@ -456,12 +577,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (j == 0 && n_t > 0 && !wait(bs.q_full[t], qi & 1)) break;
         const uint32_t kt = sbase + K_OFF + sk * KV_TILE;
         const uint32_t idesc = it.end - (it.j0 + j) * KT > HALF ? idesc_s : idesc_sh;
+        const unsigned uv = u0 + j - 1, sv = uv % STAGES;
+        const uint32_t vt = sbase + V_OFF + sv * KV_TILE;
+        const int left = it.end - (it.j0 + j - 1) * KT, read = left > HALF ? KT : HALF;
         if (j >= 1) {
-          const int i = j - 1, tile = it.j0 + i;
-          const unsigned u = u0 + i, s = u % STAGES;
-          if (!wait(bs.v_full[s], (u / STAGES) & 1)) break;
-          const uint32_t vt = sbase + V_OFF + s * KV_TILE;
-          const int left = it.end - tile * KT, read = left > HALF ? KT : HALF;
+          if (!wait(bs.v_full[sv], (uv / STAGES) & 1)) break;
           if (n_t > 0) {
             if (left < read) {
               // clear the value rows behind the prefix (both issuers write the same zeros)
@@ -475,28 +595,26 @@ __global__ void __launch_bounds__(THREADS, 1)
             // P of the item's first key tile also tells that the softmax
             // warps have read the previous item's O (their epilogue comes
             // first), so that the first product may overwrite it
-            if (!wait(bs.p_full[t][0], (cs + i) & 1)) break;
+            if (!wait(bs.p_full[t][0], (cs + j - 1) & 1)) break;
           }
-          if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) break;
-          if (n_t > 0) {
+        }
+        if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) break;
+        if (j >= 1 && n_t > 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (h == 1 && !wait(bs.p_full[t][1], (cs + i) & 1)) break;
-              tc_fence_after();
-              if (h == 1 && read == HALF) break;  // no keys in the second half
-              if (elect_one()) {
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !wait(bs.p_full[t][1], (cs + j - 1) & 1)) break;
+            tc_fence_after();
+            if (h == 1 && read == HALF) break;  // no keys in the second half
+            if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < HALF / 16; ++ks)
-                  umma_bf16_ts(o_at, s_at + h * (HALF / 2) + ks * 8,
-                               umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF), idesc_o,
-                               (i > 0 || h > 0 || ks > 0) ? 1u : 0u);
-              }
-              __syncwarp();
+              for (int ks = 0; ks < HALF / 16; ++ks)
+                umma_bf16_ts(o_at, s_at + h * (HALF / 2) + ks * 8,
+                             umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF), idesc_o,
+                             (j > 1 || h > 0 || ks > 0) ? 1u : 0u);
             }
-            if (!ok) break;
+            __syncwarp();
           }
-        } else if (t == 0 ? step > 0 && !wait(bs.turn[1], (step - 1) & 1) : !wait(bs.turn[0], step & 1)) {
-          break;
+          if (!ok) break;
         }
         if (j < n_t) {
           tc_fence_after();
@@ -512,13 +630,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         if (lane == 0) mbar_arrive(smem_u32(&bs.turn[t]));
-        if (j >= 1) {
-          if (j == n_t) {
-            if (elect_one()) umma_commit(smem_u32(&bs.o_done[t]));
-            __syncwarp();
-          }
-          release(bs.v_empty[(u0 + j - 1) % STAGES], n_t > 0);
+        if (j >= 1 && j == n_t) {
+          if (elect_one()) umma_commit(smem_u32(&bs.o_done[t]));
+          __syncwarp();
         }
+        if (j >= 1) release(bs.v_empty[sv], n_t > 0);
         if (j < it.n) release(bs.k_empty[sk], n_t > 0);
       }
       if (!ok) break;
@@ -541,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned items = 0;  // items of this Q tile
     bool ok = true;
     while (ok && walk.next(bs, it)) {
-      const int n_t = it.nseq > t * qp ? it.n : 0;
+      const int n_t = it.tiles(t, qp);
       const int rows = min(qp, it.nseq - t * qp) * nrep;  // of this Q tile
       const bool real = r < rows;
       const bool works = (warp & 3) * 32 < rows;          // some row of this warp is real
@@ -654,8 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (works) {
           const int span = it.nseq * nrep, row = t * qp * nrep + r;
           const float m2 = l > 0.f || l != l ? m_ref * scale : -INFINITY;
-          if (real) __stcg(reinterpret_cast<float2*>(a.part_ml) + it.base + row, make_float2(m2, l));
-          float4* o4 = reinterpret_cast<float4*>(a.part_o) + static_cast<size_t>(it.base) * (HEAD_DIM / 4) + row;
+          if (real) __stcg(reinterpret_cast<float2*>(sp.part_ml) + it.base + row, make_float2(m2, l));
+          float4* o4 = reinterpret_cast<float4*>(sp.part_o) + static_cast<size_t>(it.base) * (HEAD_DIM / 4) + row;
           __syncwarp();
 #pragma unroll 1
           for (int cc = 0; cc < HEAD_DIM; cc += 32) {
@@ -699,90 +815,160 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// ---- the join: a warp a query row. The parts of its prefix, one per CTA that
-// holds a piece of its item, in CTA order, then its own rows' part.
-constexpr int JOIN_WARPS = 8, JOIN_BATCH = 8;
-__global__ void __launch_bounds__(JOIN_WARPS * 32) shared_join_kernel(const __grid_constant__ SharedJoinParams a) {
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5);
+// ---- the join: WAYS warps for R query rows of one (sequence, KV head), which
+// share their parts: those of the prefix, one per CTA that holds a piece of its
+// item, then those of the own rows, one per warp. 32 / R parts at a time: a lane
+// finds the max and sum of a row of one, then the warp adds the parts up in
+// order, R float4 of a row a lane. The R rows lie side by side in a prefix's
+// part, 16 bytes each. The kernel waits for its code more than for data, so that
+// it is short: where parts lie was found out beside the streaming.
+constexpr int JOIN_WARPS = 8;
+constexpr int MOST_PARTS = 152 * (1 + decode::WARPS);  // of a pair: one per CTA, one per warp
+template <int R, int WAYS>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 3) shared_join_kernel(const __grid_constant__ SharedJoinParams a) {
+  constexpr int PARTS = 32 / R, BATCH = R == 4 ? 3 : 8 / R;
+  __shared__ float4 others_o[JOIN_WARPS][R][32];
+  __shared__ float2 others_ml[JOIN_WARPS][R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = lane % R, cg = lane / R;
+  const int set = (blockIdx.x * JOIN_WARPS + warp) / WAYS, way = warp % WAYS;  // of R rows
+  const int pair = a.sets == 1 ? set : set / a.sets, h = a.sets == 1 ? rr : (set - pair * a.sets) * R + rr;
+  const bool real = pair < a.pairs && h < a.n_rep;
   // nothing is read or written before the previous kernel of the stream is done
   pdl_trigger();
   pdl_wait();
-  if (row >= a.B * a.n_heads) return;
-  const int nrep = a.n_heads / a.n_kv, b = row / a.n_heads, h = row - b * a.n_heads, g = h / nrep;
-  const SharedRow s = a.rows[b];
-  if (s.w == 0) return;
-  const Split split(a.plan->units, a.plan->parts);
-  const int unit = s.unit0 + g * s.kv_units;
-  const int first = split.holder(unit + ITEM_UNITS), last = split.holder(unit + s.w - 1);
-  const int base = s.base + g * s.kv_rows, r = s.at + h - g * nrep;
-  // of another call (a workspace that two calls use at once): nothing of it is read
-  if (first < 0 || base < 0 || s.span <= 0 || r < 0 || r >= s.span || base + NQ * ROWS * last + s.span > a.part_rows) return;
-  const float2* mls = reinterpret_cast<const float2*>(a.part_ml) + base + r;
-  const float4* os = reinterpret_cast<const float4*>(a.part_o) + static_cast<size_t>(base) * (HEAD_DIM / 4) +
-                     static_cast<size_t>(lane) * s.span + r;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // the rows of its own
-  if (a.start[b] >= s.first) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.own_ml) + row);
-    m = ml.x;
-    l = ml.y;
-    o = __ldcg(reinterpret_cast<const float4*>(a.own_o) + static_cast<size_t>(row) * (HEAD_DIM / 4) + lane);
-  }
-#pragma unroll 1
-  for (int c0 = first; c0 <= last; c0 += JOIN_BATCH) {
-    float2 ml[JOIN_BATCH];
-    float4 x[JOIN_BATCH];
+  SharedParts s = {};
+  if (real) s = a.rows[pair];
+  const int all = __shfl_sync(0xffffffffu, min(s.prefixes + s.owns, MOST_PARTS), 0);
+  float m = -INFINITY, l = 0.f;  // of row rr, the same in its lanes
+  float4 o[R];                   // of row rr, dims 4 (cg + PARTS i) ..
 #pragma unroll
-    for (int k = 0; k < JOIN_BATCH; ++k) {
-      const int c = c0 + k;
-      ml[k] = make_float2(-INFINITY, 0.f);
-      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c <= last) {
-        ml[k] = mls[c * (NQ * ROWS)];
-        x[k] = os[static_cast<size_t>(c) * (NQ * ROWS * (HEAD_DIM / 4))];
+  for (int i = 0; i < R; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k0 = way; k0 < all; k0 += PARTS * WAYS) {
+    // row rr of part k0 + WAYS cg: where its 4-dim groups lie, and how far apart.
+    // One of another call (a workspace that two calls use at once) is not read.
+    const int k = k0 + cg * WAYS;
+    int at = -1, apart = 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const bool own = k >= s.prefixes;
+    const int part = own ? s.own + (k - s.prefixes) * a.n_rep : s.prefix + k * (NQ * ROWS);
+    if (real && k < all && part >= 0 && (own ? part + h < a.own_rows : s.at + h >= 0 && s.at + h < s.span && part + s.span <= a.part_rows)) {
+      ml = reinterpret_cast<const float2*>(own ? a.own_ml : a.part_ml)[part + (own ? 0 : s.at) + h];
+      at = own ? a.own_at + (part + h) * (HEAD_DIM / 4) : part * (HEAD_DIM / 4) + s.at + h;
+      apart = own ? 1 : s.span;
+    }
+    const int n = min(PARTS, ceil_div(all - k0, WAYS));
+    float4 x[BATCH][R];
+    auto load = [&](int i, float4 (&y)[R]) {
+      const int from = __shfl_sync(0xffffffffu, at, (i * R + rr) & 31), step = __shfl_sync(0xffffffffu, apart, (i * R + rr) & 31);
+#pragma unroll
+      for (int e = 0; e < R; ++e)
+        y[e] = i < n && from != -1 ? reinterpret_cast<const float4*>(a.parts)[from + (cg + PARTS * e) * step]
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    // the first ones come beside the maxima
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) load(i, x[i]);
+    float mx = ml.x;
+#pragma unroll
+    for (int d = R; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    mx = fmaxf(mx, m);
+    const float ref = mx == -INFINITY ? 0.f : mx, f = ex2_approx(m - ref), weight = ex2_approx(ml.x - ref);
+    float sum = weight * ml.y;
+#pragma unroll
+    for (int d = R; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    m = mx;
+    l = l * f + sum;
+#pragma unroll
+    for (int e = 0; e < R; ++e) o[e] = make_float4(o[e].x * f, o[e].y * f, o[e].z * f, o[e].w * f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i)
+        if (i0 > 0) load(i0 + i, x[i]);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const float w = __shfl_sync(0xffffffffu, weight, ((i0 + i) * R + rr) & 31);
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+          o[e].x += w * x[i][e].x;
+          o[e].y += w * x[i][e].y;
+          o[e].z += w * x[i][e].z;
+          o[e].w += w * x[i][e].w;
+        }
       }
     }
-    float mx = m;
+  }
+  if (WAYS > 1) {
+    if (way) {
 #pragma unroll
-    for (int k = 0; k < JOIN_BATCH; ++k) mx = fmaxf(mx, ml[k].x);
-    decode::rescale(m, mx, l, o);
-    const float ref = mx == -INFINITY ? 0.f : mx;
+      for (int e = 0; e < R; ++e) others_o[warp][e][lane] = o[e];
+      if (cg == 0) others_ml[warp][rr] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (way) return;
+#pragma unroll 1
+    for (int w = warp + 1; w < warp + WAYS; ++w) {
+      const float2 ml = others_ml[w][rr];
+      const float mx = fmaxf(m, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+      const float f = ex2_approx(m - ref), y = ex2_approx(ml.x - ref);
+      m = mx;
+      l = l * f + y * ml.y;
 #pragma unroll
-    for (int k = 0; k < JOIN_BATCH; ++k) {
-      const float w = ex2_approx(ml[k].x - ref);
-      l += w * ml[k].y;
-      o.x += w * x[k].x;
-      o.y += w * x[k].y;
-      o.z += w * x[k].z;
-      o.w += w * x[k].w;
+      for (int e = 0; e < R; ++e) {
+        const float4 x = others_o[w][e][lane];
+        o[e].x = o[e].x * f + y * x.x;
+        o[e].y = o[e].y * f + y * x.y;
+        o[e].z = o[e].z * f + y * x.z;
+        o[e].w = o[e].w * f + y * x.w;
+      }
     }
   }
-  decode::store_row(a.out, row, o, 1.f / l);
+  // a sequence without keys has its zeros
+  if (!real || all == 0) return;
+  const float inv = 1.f / l;
+  uint2* out = reinterpret_cast<uint2*>(a.out + (static_cast<long long>(pair) * a.n_rep + h) * HEAD_DIM) + cg;
+#pragma unroll
+  for (int e = 0; e < R; ++e)
+    out[PARTS * e] = make_uint2(pack_bf16(o[e].x * inv, o[e].y * inv), pack_bf16(o[e].z * inv, o[e].w * inv));
 }
 
 }  // namespace
 
-cudaError_t launch_shared_prefix(const PackedPrefillMaps& maps, const SharedPrefixParams& a, cudaStream_t s) {
-  static bool attr_set[64] = {};
+cudaError_t launch_shared_decode(const PackedPrefillMaps& maps, const SharedDecodeParams& a, cudaStream_t s) {
+  const PagedDecodeParams& p = a.own;
+  const int n_rep = p.n_heads / p.n_kv;
+  if (p.B <= 0 || p.B > PAGED_MAX_SEQS || a.G <= 0 || a.G > SHARED_MAX_GROUPS || p.ctas < 2 || p.ctas >= THREADS ||
+      n_rep < 1 || n_rep > PAGED_MAX_REP)
+    return cudaErrorInvalidValue;
+  const auto kernel = n_rep <= 8 ? shared_decode_kernel<1> : shared_decode_kernel<2>;
+  static bool attr_set[64][2] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (!attr_set[dev][n_rep <= 8]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev][n_rep <= 8] = true;
   }
-  if (a.B <= 0 || a.B > PAGED_MAX_SEQS || a.G <= 0 || a.G > SHARED_MAX_GROUPS || a.ctas <= 0) return cudaErrorInvalidValue;
-  // one CTA per SM (shared memory and TMEM admit no second)
-  return launch_behind(shared_prefix_kernel, static_cast<unsigned>(a.ctas), THREADS, SMEM_BYTES, s, maps.q, maps.k, maps.v, a);
+  // one CTA per SM (shared memory admits no second)
+  return launch_behind(kernel, static_cast<unsigned>(p.ctas), THREADS, SMEM_BYTES, s, maps.q, maps.k, maps.v, a);
 }
 
+// R: 4 rows where a KV head has as many. Warps for them: as many as still run
+// at once (3 CTAs per SM).
+template <int R>
+static cudaError_t launch_join(SharedJoinParams a, cudaStream_t s) {
+  a.sets = (a.n_rep + R - 1) / R;
+  const int sets = a.pairs * a.sets;
+  const int ways = sets <= 448 ? 8 : sets <= 896 ? 4 : sets <= 1792 ? 2 : 1, each = JOIN_WARPS / ways;
+  const auto kernel = ways == 8 ? shared_join_kernel<R, 8> : ways == 4 ? shared_join_kernel<R, 4>
+                                                         : ways == 2 ? shared_join_kernel<R, 2> : shared_join_kernel<R, 1>;
+  return launch_behind(kernel, static_cast<unsigned>((sets + each - 1) / each), JOIN_WARPS * 32, 0, s, a);
+}
 cudaError_t launch_shared_join(const SharedJoinParams& a, cudaStream_t s) {
-  const long long rows = static_cast<long long>(a.B) * a.n_heads;
-  return launch_behind(shared_join_kernel, static_cast<unsigned>((rows + JOIN_WARPS - 1) / JOIN_WARPS), JOIN_WARPS * 32, 0, s, a);
+  return a.n_rep >= 3 ? launch_join<4>(a, s) : a.n_rep == 2 ? launch_join<2>(a, s) : launch_join<1>(a, s);
 }
 
 // Units of a batch at most: of groups of two sequences at least, with `keys` in

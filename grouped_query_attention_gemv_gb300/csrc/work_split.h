@@ -55,6 +55,22 @@ GQA_HD int decode_ctas(int total, int grid, int warps) { return least(grid, ceil
 // The first chunk of a warp's share of [c0, c1); warp = warps: c1.
 GQA_HD int warp_start(int c0, int c1, int warp, int warps) { return c0 + (c1 - c0) * warp / warps; }
 
+// CTAs with a range of `total` > 0 chunks, each of `warps` chunks at least (one
+// CTA with fewer where the total is fewer).
+GQA_HD int full_ctas(int total, int grid, int warps) { return most(1, least(grid, total / warps)); }
+// The warps that hold chunks [first, end) of equal ranges, `warps` to a CTA, each
+// with a chunk at least; counted 8 to a CTA.
+struct WarpSpan {
+  int first, last;
+};
+GQA_HD int holding_warp(int u, const Split& split, int warps) {
+  const int c = split.holder(u), c0 = split.start(c), n = split.start(c + 1) - c0;
+  return c * 8 + static_cast<int>((static_cast<long long>(u - c0 + 1) * warps - 1) / n);
+}
+GQA_HD WarpSpan warps_of(int first, int end, const Split& split, int warps) {
+  return {holding_warp(first, split, warps), holding_warp(end - 1, split, warps)};
+}
+
 // ---- packed prefill attention: items cut into equal ranges
 
 constexpr int ITEM_UNITS = 2;  // what an item takes beside its key tiles, in those (2.8 us)

@@ -385,7 +385,7 @@ int gqa_host_stage_release(void* stage);
  * and can be captured into a graph; no length is read by the host, so a
  * captured step replays with other lengths, tables and contents. One launch
  * each; two for the prefill attention where a sequence may have more than
- * 2,048 keys, three for the decode attention of groups. The workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled
+ * 2,048 keys, and for the decode attention of groups. The workspace holds GQA_PAGED_WORKSPACE_BYTES, zero-filled
  * before its first use, serves one call at a time and no other entries than
  * these; its status word is read with gqa_device_status. After
  * GQA_DEV_WAIT_TIMEOUT zero-fill it again (gqa_workspace_init). */
@@ -509,11 +509,11 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
  * A sequence that does not see the whole prefix (start_pos + 1 < prefix_rows,
  * or an unused slot) is attended by itself, and so are all where sharing would
  * not pay: where it saves fewer cache rows than a threshold, with more than
- * 1,024 groups, with more than 32,768 query rows (B * n_heads). Probabilities
+ * 1,024 groups, with more than 28,672 query rows (B * n_heads). Probabilities
  * enter the value product of shared rows as in gqa_paged_prefill, of the others
  * as in gqa_paged_decode. cu_groups out of order or range, where it is looked
  * at, is reported as GQA_DEV_BAD_POSITION, and nothing is shared. G at most
- * GQA_PAGED_MAX_SEQS. Three launches, or one where the host can tell that
+ * GQA_PAGED_MAX_SEQS. Two launches, or one where the host can tell that
  * nothing will be shared. */
 int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
                             const int32_t* cu_groups, int G, const int32_t* prefix_rows, const gqa_pages* pages,
