@@ -57,7 +57,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 // Paired fp32 arithmetic (two lanes of fp32 in one 64-bit register pair; one
-// instruction for both): d = a * b + c and d = a + b, round to nearest.
+// instruction for both): d = a * b + c, d = a + b and d = a * b, round to nearest.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   unsigned long long ra, rb, rc, rd;
   asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
@@ -73,6 +73,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
   asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
   float2 d;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
   return d;

@@ -9,11 +9,21 @@
 // fp8.cuh. Values that are not finite take no part in a row's scale and are
 // held as e4m3's NaN.
 //
-// Every row is read once and written once, so the bound is memory. As in
-// paged_append.cu one warp takes 8 of a token's n_heads + 2 n_kv head rows, two
-// at a time (16 lanes x 8 dims each), the rows' loads first, and the (cos, sin)
-// of a token once for its 8 rows. A pair of halves lies in two lanes: they
-// swap their dims. The largest |x| of a row is four exchanges of its 16 lanes.
+// Every row is read once and written once, so the bound is memory, and as near
+// to it the instructions a value: 40 bytes a lane and row pass some 90 of them.
+// As in paged_append.cu a warp takes 8 of a token's n_heads + 2 n_kv head rows,
+// two at a time (16 lanes x 8 dims each), the rows' loads first, and the (cos,
+// sin) of a token once. A batch of 8 is of queries, keys or values alone, so
+// that addresses and what is done with it are found once (7 prompts, 356 MB:
+// 80 us row by row, 69 so). A pair of halves lies in two lanes: they swap their
+// dims. The largest |x| of a row is four exchanges of its 16 lanes. With many
+// tokens a warp takes several batches, so that the chain to the token's place
+// is walked less often.
+// Measured (GB300, 6.8 TB/s copied), 32 and 8 heads: 59.2 us for 7 prompts into
+// 8 bits (356 MB), 38.9 for 5 prompts into bf16, 64 dims turned (244 MB), 2.7
+// for one token, 2.8 for 64.
+#include <math.h>
+
 #include "fp8.cuh"
 #include "paged.h"
 
@@ -22,51 +32,52 @@ namespace gqa {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int ROWS = 8;  // head rows per warp
+constexpr int ROWS = 8;  // head rows of a warp at a time
 
-__device__ __forceinline__ void unpack(uint4 x, float (&f)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
+__device__ __forceinline__ void unpack(uint4 x, float2 (&f)[4]) {
+  f[0] = make_float2(bf16_lo(x.x), bf16_hi(x.x));
+  f[1] = make_float2(bf16_lo(x.y), bf16_hi(x.y));
+  f[2] = make_float2(bf16_lo(x.z), bf16_hi(x.z));
+  f[3] = make_float2(bf16_lo(x.w), bf16_hi(x.w));
 }
-// a c - b s and a s + b c
-__device__ __forceinline__ float turned_first(float a, float b, float2 cs) {
-  return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-}
-__device__ __forceinline__ float turned_second(float a, float b, float2 cs) {
-  return __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x));
+// own c + other s: dims of a pair (a, b) turned, a c - b s with s negated, b c + a s
+__device__ __forceinline__ float2 turned(float2 own, float2 other, float2 c, float2 s) {
+  return make_float2(__fadd_rn(__fmul_rn(own.x, c.x), __fmul_rn(other.x, s.x)),
+                     __fadd_rn(__fmul_rn(own.y, c.y), __fmul_rn(other.y, s.y)));
 }
 
 template <bool HALVES, bool FP8>
-__global__ void __launch_bounds__(WARPS * 32) rotary_append_kernel(const __grid_constant__ RotaryAppendParams rp, int groups) {
+__global__ void __launch_bounds__(WARPS * 32) rotary_append_kernel(const __grid_constant__ RotaryAppendParams rp, int shares, int each) {
   const PagedAppendParams& p = rp.a;
   // nothing is read or written before the previous kernel of the stream is done
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, half = lane >> 4, piece = lane & 15;
-  const long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
-  const int m = static_cast<int>(item / groups);
+  // the warps of a token follow each other
+  const unsigned long long item = static_cast<unsigned long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  const int m = static_cast<int>(item >> 32 ? item / shares : static_cast<unsigned>(item) / static_cast<unsigned>(shares));
   if (m >= p.N) return;
-  const int row0 = static_cast<int>(item - static_cast<long long>(m) * groups) * ROWS;
-  const int rows = p.n_heads + 2 * p.n_kv;
-
+  int row0 = static_cast<int>(item - static_cast<unsigned long long>(m) * shares) * each * ROWS;
+  const int row_end = min(p.n_heads + 2 * p.n_kv, row0 + each * ROWS);
+  // A batch is rows row0 .. row0 + n - 1 of the queries, the keys or the values:
+  // addresses are found once a batch, and a batch does one thing.
+  int n = 0;
+  enum { QUERY, KEY, VALUE } kind = QUERY;
   uint4 x[ROWS / 2];
+  auto load = [&]() {
+    kind = row0 < p.n_heads ? QUERY : row0 < p.n_heads + p.n_kv ? KEY : VALUE;
+    const int first = kind == QUERY ? 0 : kind == KEY ? p.n_heads : p.n_heads + p.n_kv;
+    n = min(ROWS, min(row_end, first + (kind == QUERY ? p.n_heads : p.n_kv)) - row0);
+    const __nv_bfloat16* src = (kind == QUERY ? p.q + m * p.q_stride : kind == KEY ? p.k + m * p.k_stride : p.v + m * p.v_stride) +
+                               (row0 - first + half) * HEAD_DIM + piece * 8;
 #pragma unroll
-  for (int i = 0; i < ROWS / 2; ++i) {
-    const int r = row0 + 2 * i + half;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const __nv_bfloat16* src = r < p.n_heads ? p.q + m * p.q_stride + r * HEAD_DIM
-                                 : r < p.n_heads + p.n_kv
-                                     ? p.k + m * p.k_stride + (r - p.n_heads) * HEAD_DIM
-                                     : p.v + m * p.v_stride + (r - p.n_heads - p.n_kv) * HEAD_DIM;
+    for (int i = 0; i < ROWS / 2; ++i) {
+      x[i] = make_uint4(0, 0, 0, 0);
       // q may be rotated in place: not the read-only path
-      x[i] = *(reinterpret_cast<const uint4*>(src) + piece);
+      if (2 * i + half < n) x[i] = *reinterpret_cast<const uint4*>(src + 2 * i * HEAD_DIM);
     }
-  }
+  };
+  load();
 
   int b = m, t = 0;
   if (p.cu) {
@@ -95,26 +106,30 @@ __global__ void __launch_bounds__(WARPS * 32) rotary_append_kernel(const __grid_
   // has one dim of; lanes past the turned dims have none
   const int pieces = rp.rotary_dim / 8, across = pieces / 2;
   const bool turns = piece < pieces, second = HALVES && piece >= across;
-  constexpr int CS = HALVES ? 8 : 4;
-  float2 cs[CS];
+  float2 cos2[4], sin2[4];  // of this lane's dims, two each; -sin for the first dim of a pair
   {
     const float4* src = reinterpret_cast<const float4*>(p.rope + pos * rp.rotary_dim) +
                         (HALVES ? (second ? piece - across : piece) * 4 : piece * 2);
+    const float sign = second ? 1.f : -1.f;
 #pragma unroll
-    for (int i = 0; i < CS / 2; ++i) {
+    for (int i = 0; i < (HALVES ? 4 : 2); ++i) {
       float4 c = make_float4(1.f, 0.f, 1.f, 0.f);
       if (turns) c = __ldg(src + i);
-      cs[2 * i] = make_float2(c.x, c.y);
-      cs[2 * i + 1] = make_float2(c.z, c.w);
+      if (HALVES) {
+        cos2[i] = make_float2(c.x, c.z);
+        sin2[i] = make_float2(c.y * sign, c.w * sign);
+      } else {
+        cos2[2 * i] = make_float2(c.x, c.x);
+        sin2[2 * i] = make_float2(-c.y, c.y);
+        cos2[2 * i + 1] = make_float2(c.z, c.z);
+        sin2[2 * i + 1] = make_float2(-c.w, c.w);
+      }
     }
   }
   const int other = (lane & 16) | (turns ? (second ? piece - across : piece + across) : piece);
 
-#pragma unroll
-  for (int i = 0; i < ROWS / 2; ++i) {
-    const int r = row0 + 2 * i + half;
-    const bool is_kv = r >= p.n_heads, is_v = r >= p.n_heads + p.n_kv;
-    float f[8];
+  // a lane's dims of its row of the i-th two, turned
+  auto turn = [&](int i, float2(&f)[4]) {
     unpack(x[i], f);
     if (HALVES) {
       uint4 y;
@@ -122,71 +137,117 @@ __global__ void __launch_bounds__(WARPS * 32) rotary_append_kernel(const __grid_
       y.y = __shfl_sync(0xffffffffu, x[i].y, other);
       y.z = __shfl_sync(0xffffffffu, x[i].z, other);
       y.w = __shfl_sync(0xffffffffu, x[i].w, other);
-      float g[8];
+      float2 g[4];
       unpack(y, g);
-      if (!is_v && turns) {
+      if (turns) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = second ? turned_second(g[e], f[e], cs[e % CS]) : turned_first(f[e], g[e], cs[e % CS]);
+        for (int e = 0; e < 4; ++e) f[e] = turned(f[e], g[e], cos2[e], sin2[e]);
       }
-    } else if (!is_v && turns) {
+    } else if (turns) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = f[2 * e], c = f[2 * e + 1];
-        f[2 * e] = turned_first(a, c, cs[e]);
-        f[2 * e + 1] = turned_second(a, c, cs[e]);
-      }
+      for (int e = 0; e < 4; ++e) f[e] = turned(f[e], make_float2(f[e].y, f[e].x), cos2[e], sin2[e]);
     }
-    if (!FP8 || !is_kv) {
-      const uint4 y = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-      if (r < rows) {
-        __nv_bfloat16* dst;
-        if (!is_kv) {
-          dst = p.q_out + (static_cast<long long>(m) * p.n_heads + r) * HEAD_DIM;
-        } else {
-          const long long at = page * p.pages.page_stride + in_page * p.pages.row_stride;
-          dst = is_v ? p.pages.v + at + (r - p.n_heads - p.n_kv) * p.pages.head_stride
-                     : p.pages.k + at + (r - p.n_heads) * p.pages.head_stride;
-        }
-        // what is not turned is stored as it came, a NaN's bits among it
-        *(reinterpret_cast<uint4*>(dst) + piece) = is_v || !turns ? x[i] : y;
+  };
+  // the row in bf16; what is not turned as it came, a NaN's bits among it
+  auto in_bf16 = [&](int i, const float2(&f)[4]) {
+    return turns ? make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y), pack_bf16(f[2].x, f[2].y),
+                              pack_bf16(f[3].x, f[3].y))
+                 : x[i];
+  };
+  // a row's values to 8 bits; its exponent
+  auto in_fp8 = [&](float2(&f)[4], int& e) {
+    // fmaxf passes over NaN, which stays one; infinities are rare
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) most = max3(most, fabsf(f[k].x), fabsf(f[k].y));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (__any_sync(0xffffffffu, most == INFINITY)) {
+      most = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (fabsf(f[k].x) == INFINITY) f[k].x = __uint_as_float(0x7fffffffu);
+        if (fabsf(f[k].y) == INFINITY) f[k].y = __uint_as_float(0x7fffffffu);
+        most = max3(most, fabsf(f[k].x), fabsf(f[k].y));
       }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
     }
-    if (FP8) {
-      uint32_t most = 0;
+    e = row_exponent(__float_as_uint(most));
+    const float2 s = make_float2(power_of_two(-e), power_of_two(-e));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = __float_as_uint(f[e]) & 0x7fffffffu;
-        if (u < 0x7f800000u) most = max(most, u);
-        else f[e] = __uint_as_float(0x7fffffffu);
+    for (int k = 0; k < 4; ++k) f[k] = mul2(f[k], s);
+    return make_uint2(to_e4m3x2(f[0].x, f[0].y) | to_e4m3x2(f[1].x, f[1].y) << 16,
+                      to_e4m3x2(f[2].x, f[2].y) | to_e4m3x2(f[3].x, f[3].y) << 16);
+  };
+
+#pragma unroll 1
+  for (;;) {
+    if (kind == QUERY) {
+      __nv_bfloat16* dst = p.q_out + (static_cast<long long>(m) * p.n_heads + row0 + half) * HEAD_DIM + piece * 8;
+#pragma unroll
+      for (int i = 0; i < ROWS / 2; ++i) {
+        float2 f[4];
+        turn(i, f);
+        if (2 * i + half < n) *reinterpret_cast<uint4*>(dst + 2 * i * HEAD_DIM) = in_bf16(i, f);
       }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-      const int e = row_exponent(most);
-      const float s = power_of_two(-e);
-      if (r < rows && is_kv) {
-        const int h = r - p.n_heads - (is_v ? p.n_kv : 0);
+    } else {
+      const bool key = kind == KEY;
+      const int h = row0 + half - p.n_heads - (key ? 0 : p.n_kv);
+      if (FP8) {
         const Fp8Cache& c = rp.pages8;
-        uint8_t* dst = (is_v ? c.v : c.k) + page * c.page_stride + in_page * c.row_stride + h * c.head_stride;
-        const uint2 y = make_uint2(to_e4m3x2(f[0] * s, f[1] * s) | to_e4m3x2(f[2] * s, f[3] * s) << 16,
-                                   to_e4m3x2(f[4] * s, f[5] * s) | to_e4m3x2(f[6] * s, f[7] * s) << 16);
-        *(reinterpret_cast<uint2*>(dst) + piece) = y;
-        if (piece == 0)
-          (is_v ? c.v_scale : c.k_scale)[page * c.scale_page + in_page * c.scale_row + h * c.scale_head] =
-              static_cast<uint8_t>(e + 127);
+        uint8_t* dst = (key ? c.k : c.v) + page * c.page_stride + in_page * c.row_stride + h * c.head_stride + piece * 8;
+        uint8_t* scale = (key ? c.k_scale : c.v_scale) + page * c.scale_page + in_page * c.scale_row + h * c.scale_head;
+#pragma unroll
+        for (int i = 0; i < ROWS / 2; ++i) {
+          float2 f[4];
+          if (key) turn(i, f);
+          else unpack(x[i], f);
+          int e;
+          const uint2 y = in_fp8(f, e);
+          if (2 * i + half < n) {
+            *reinterpret_cast<uint2*>(dst) = y;
+            if (piece == 0) *scale = static_cast<uint8_t>(e + 127);
+          }
+          dst += 2 * c.head_stride;
+          scale += 2 * c.scale_head;
+        }
+      } else {
+        __nv_bfloat16* dst = (key ? p.pages.k : p.pages.v) + page * p.pages.page_stride + in_page * p.pages.row_stride +
+                             h * p.pages.head_stride + piece * 8;
+#pragma unroll
+        for (int i = 0; i < ROWS / 2; ++i) {
+          uint4 y = x[i];
+          if (key) {
+            float2 f[4];
+            turn(i, f);
+            y = in_bf16(i, f);
+          }
+          if (2 * i + half < n) *reinterpret_cast<uint4*>(dst) = y;
+          dst += 2 * p.pages.head_stride;
+        }
       }
     }
+    row0 += n;
+    if (row0 >= row_end) break;
+    load();
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rotary_append(const RotaryAppendParams& p, cudaStream_t s) {
+  // Batches of a warp. Measured, 1 / 2 / all 6 of a token, halves, us: into 8
+  // bits 1,024 tokens 7.0 / 6.8 / 10.4, 2,048 13.1 / 13.5 / 14.3, 4,096 21.4 /
+  // 20.7 / 18.7, 8,192 37.7 / 35.4 / 32.7; into bf16 1,024 6.5 / 6.2 / 9.4, 2,048
+  // 12.6 / 12.2 / 12.9, 4,096 20.7 / 19.1 / 18.9, 8,192 36.6 / 33.7 / 34.0.
   const int groups = (p.a.n_heads + 2 * p.a.n_kv + ROWS - 1) / ROWS;
-  const long long blocks = (static_cast<long long>(p.a.N) * groups + WARPS - 1) / WARPS;
+  const int each = p.fp8 ? (p.a.N >= 4096 ? groups : 1) : p.a.N >= 2048 ? 2 : 1, shares = (groups + each - 1) / each;
+  const long long blocks = (static_cast<long long>(p.a.N) * shares + WARPS - 1) / WARPS;
   if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const auto kernel = p.halves ? (p.fp8 ? rotary_append_kernel<true, true> : rotary_append_kernel<true, false>)
                                : (p.fp8 ? rotary_append_kernel<false, true> : rotary_append_kernel<false, false>);
-  return launch_behind(kernel, static_cast<unsigned>(blocks), WARPS * 32, 0, s, p, groups);
+  return launch_behind(kernel, static_cast<unsigned>(blocks), WARPS * 32, 0, s, p, shares, each);
 }
 
 }  // namespace gqa
