@@ -107,30 +107,34 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     Cursor iss = locate(a0, pre, p.B, p.n_kv), cur = iss;
     const int in_page = (1 << p.pages.page_shift) - 1;
     const int box = min(KEYS, in_page + 1), boxes = KEYS / box;
-    const uint64_t policy = l2_evict_first();
-    // the page of this lane's position of the chunk at `iss`, -1 past the sequence
+    // The page of this lane's position of the chunk at `iss`, -1 past the
+    // sequence. What is loaded ahead (pages, scales) is not looked at before it
+    // is used: a look waits for it, 0.3 us each a chunk.
+    constexpr int NONE = -1;
+    bool in_seq;  // of `next`
     auto page_of = [&]() -> int {
       const int pos = iss.j * KEYS + lane;
-      if (pos > last[iss.b]) return -1;
-      const int page = p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)];
-      if (page < 0 || page >= p.pages.num_pages) {
-        report(p.status, DEV_BAD_PAGE);
-        return -1;
-      }
-      return page;
+      in_seq = pos <= last[iss.b];
+      return in_seq ? p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)] : NONE;
     };
     int issued = 0;
     int next = page_of();
     const uint32_t ring32 = smem_u32(ring);
-    // copies the chunk at `iss`; its scale bytes (key | value << 8) of this lane's position
-    auto issue = [&]() -> uint32_t {
-      uint32_t scales = 0x7f7f;
+    // copies the chunk at `iss`; its scale bytes of this lane's position
+    struct Scales {
+      uint32_t k, v;
+    };
+    auto issue = [&]() -> Scales {
+      Scales scales{127, 127};
       if (issued < n) {
         const uint32_t dst = ring32 + (issued % STAGES) * STAGE_BYTES, bar = smem_u32(&full[warp][issued % STAGES]);
-        const int page = next, row = (iss.j * KEYS + lane) & in_page, h = iss.h;
-        if (page >= 0) {
+        const int row = (iss.j * KEYS + lane) & in_page, h = iss.h;
+        const bool good = next >= 0 && next < p.pages.num_pages;
+        if (in_seq && !good) report(p.status, DEV_BAD_PAGE);
+        const int page = good ? next : NONE;
+        if (good) {
           const long long at = page * p.pages.scale_page + row * p.pages.scale_row + h * p.pages.scale_head;
-          scales = p.pages.k_scale[at] | static_cast<uint32_t>(p.pages.v_scale[at]) << 8;
+          scales = {p.pages.k_scale[at], p.pages.v_scale[at]};
         }
         // lane x < boxes: box x of K, the next ones of V
         const int x = lane % boxes;
@@ -141,8 +145,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         if (lane == 0) mbar_expect_tx(bar, held * box * HEAD_DIM);
         __syncwarp();
         if (copies)
-          tma_load_4d_stream(dst + (lane >= boxes ? TILE_BYTES : 0) + x * box * HEAD_DIM, lane >= boxes ? &mv : &mk, bar,
-                             0, h, first_row, first_page, policy);
+          tma_load_4d(dst + (lane >= boxes ? TILE_BYTES : 0) + x * box * HEAD_DIM, lane >= boxes ? &mv : &mk, bar,
+                             0, h, first_row, first_page);
         ++issued;
         if (issued < n) {
           advance(iss, pre, p.B, p.n_kv);
@@ -152,14 +156,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       return scales;
     };
     static_assert(STAGES == 2, "one chunk's scales in hand");
-    uint32_t ahead = issue();
+    Scales ahead = issue();
 
     uint32_t qb[NT][8][2];  // Q^T as B fragments: dims 16s + 4t (+1) | +2 (+3), query head 8 nt + gr
     float q_scale[NT][2];   // what takes the products of heads 8 nt + 2t (+1) to scores in log2 units
     float m_run[NT][2], l_run[NT][2], v_run[NT][2], oacc[NT][8][4];  // heads 8 nt + 2t (+1); O^T tile d: dims 16d + 2 gr (+1)
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const uint32_t scales = ahead;
+      const Scales scales = ahead;
       ahead = issue();
       if (i == 0 || cur.j == 0) {
         const __nv_bfloat16* q = p.q + cur.b * p.q_stride + cur.h * n_rep * HEAD_DIM + 4 * t;
@@ -207,30 +211,54 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         __syncwarp();
       }
 
-      float sc[NT][2][4];  // keys 16 m + gr (+8), heads 2t (+1)
+      float sc[NT][2][4], sd[NT][2][4];  // keys 16 m + gr (+8), heads 2t (+1): two sums, added up below
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) sc[nt][m][0] = sc[nt][m][1] = sc[nt][m][2] = sc[nt][m][3] = 0.f;
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[nt][m][e] = sd[nt][m][e] = 0.f;
+      uint32_t kr[4][2][4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          ldsm_x4(kt + m * 16 * HEAD_DIM + sw128(lane & 15, 2 * s + half), kr[s][m][0], kr[s][m][1], kr[s][m][2], kr[s][m][3]);
 #pragma unroll
       for (int s = 0; s < 8; s += 2)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          uint32_t r[4], lo[4], hi[4];
-          ldsm_x4(kt + m * 16 * HEAD_DIM + sw128(lane & 15, s + half), r[0], r[1], r[2], r[3]);
+          uint32_t lo[4], hi[4];
+          const uint32_t(&r)[4] = kr[s / 2][m];
 #pragma unroll
           for (int e = 0; e < 4; ++e) e4m3x4_to_f16(r[e], lo[e], hi[e]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16(sc[nt][m], lo[0], lo[1], hi[0], hi[1], qb[nt][s][0], qb[nt][s][1]);
-            mma_f16(sc[nt][m], lo[2], lo[3], hi[2], hi[3], qb[nt][s + 1][0], qb[nt][s + 1][1]);
+            mma_f16(sd[nt][m], lo[2], lo[3], hi[2], hi[3], qb[nt][s + 1][0], qb[nt][s + 1][1]);
           }
         }
+      // One tile of heads: the values are converted here, beside the softmax's long
+      // chain of dependent steps, two while it leaves no registers for that.
+      uint32_t even[4][2][4], odd[4][2][4];
+      auto values = [&](int d, int m) {
+        uint32_t r[4];
+        ldsm_x4_t(vt + m * 16 * HEAD_DIM + sw128(lane & 15, 2 * d + half), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4m3x4_to_f16(__byte_perm(r[e], 0, 0x3120), even[d][m][e], odd[d][m][e]);
+      };
+      if (NT == 1) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) values(d, m);
+      }
       // the scales of keys gr, gr + 8, gr + 16, gr + 24
       float ks[4], ve[4];
+      const uint32_t both = scales.k | scales.v << 8;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t x = __shfl_sync(0xffffffffu, scales, gr + 8 * e);
+        const uint32_t x = __shfl_sync(0xffffffffu, both, gr + 8 * e);
         ks[e] = scale_value(x & 0xffu);
         ve[e] = static_cast<float>(static_cast<int>(x >> 8) - 127);
       }
@@ -243,7 +271,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
           float x[4], y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            x[k] = gr + 8 * k <= left ? sc[nt][k >> 1][(k & 1) * 2 + e] * (ks[k] * q_scale[nt][e]) : -INFINITY;
+            x[k] = gr + 8 * k <= left ? (sc[nt][k >> 1][(k & 1) * 2 + e] + sd[nt][k >> 1][(k & 1) * 2 + e]) * (ks[k] * q_scale[nt][e])
+                                      : -INFINITY;
             y[k] = x[k] + ve[k];
           }
           float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), my = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
@@ -284,17 +313,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
       }
 #pragma unroll
-      for (int d = 0; d < 8; d += 2)
+      for (int d = 0; d < 4; ++d)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          uint32_t r[4], even[4], odd[4];
-          ldsm_x4_t(vt + m * 16 * HEAD_DIM + sw128(lane & 15, d + half), r[0], r[1], r[2], r[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4m3x4_to_f16(__byte_perm(r[e], 0, 0x3120), even[e], odd[e]);
+          if (NT > 1) values(d, m);
+          const uint32_t(&x)[4] = even[d][m], (&y)[4] = odd[d][m];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(oacc[nt][d], even[0], odd[0], even[1], odd[1], pb[nt][m][0], pb[nt][m][1]);
-            mma_f16(oacc[nt][d + 1], even[2], odd[2], even[3], odd[3], pb[nt][m][0], pb[nt][m][1]);
+            mma_f16(oacc[nt][2 * d], x[0], y[0], x[1], y[1], pb[nt][m][0], pb[nt][m][1]);
+            mma_f16(oacc[nt][2 * d + 1], x[2], y[2], x[3], y[3], pb[nt][m][0], pb[nt][m][1]);
           }
         }
       __syncwarp();  // the chunk's rows are read before its slot is filled again
