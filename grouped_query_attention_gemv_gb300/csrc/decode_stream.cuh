@@ -49,30 +49,30 @@ __device__ __forceinline__ void stream_chunks(const PagedDecodeParams& p, Shared
 
   if (n > 0) {
     Cursor iss = locate(a0, pre, p.B, p.n_kv), cur = iss;
-    // element offset of row lane % 16 of the chunk at `iss`, -1 for a row past the sequence
-    auto row_offset = [&]() -> long long {
+    // The page of row lane % 16 of the chunk at `iss`, if it is one that is read.
+    // It is loaded a chunk ahead and not looked at before its use: a look waits.
+    int row = 0;          // within the page
+    bool reads = false;
+    auto page_of = [&]() -> int {
       const int f = SHARED ? begin[iss.b] : 0;
       const int pos = (iss.j + f / KEYS) * KEYS + piece;
-      if (pos > last[iss.b] || (SHARED && pos < f)) return -1;
-      const int page = p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)];
-      if (page < 0 || page >= p.pages.num_pages) {
-        report(p.status, DEV_BAD_PAGE);
-        return -1;
-      }
-      return page * p.pages.page_stride + (pos & ((1 << p.pages.page_shift) - 1)) * p.pages.row_stride +
-             iss.h * p.pages.head_stride;
+      reads = pos <= last[iss.b] && (!SHARED || pos >= f);
+      row = pos & ((1 << p.pages.page_shift) - 1);
+      return reads ? p.pages.table[static_cast<long long>(iss.b) * p.pages.table_stride + (pos >> p.pages.page_shift)] : 0;
     };
     int issued = 0;
-    long long next = row_offset();
+    int page = page_of();
     const uint32_t ring32 = smem_u32(ring);
     auto issue = [&]() {
       if (issued < n) {
         const uint32_t dst = ring32 + (issued % STAGES) * STAGE_BYTES;
-        const long long off = next;
-        ++issued;
-        if (issued < n) {
-          advance(iss, pre, p.B, p.n_kv);
-          next = row_offset();
+        // element offset of the row, -1: zeros instead
+        long long off = -1;
+        if (reads) {
+          if (page < 0 || page >= p.pages.num_pages)
+            report(p.status, DEV_BAD_PAGE);
+          else
+            off = page * p.pages.page_stride + row * p.pages.row_stride + iss.h * p.pages.head_stride;
         }
 #pragma unroll
         for (int i = 0; i < KEYS / 2; ++i) {
@@ -82,6 +82,11 @@ __device__ __forceinline__ void stream_chunks(const PagedDecodeParams& p, Shared
           const uint32_t bytes = o < 0 ? 0u : 16u;
           cp_async16(dst + tile_at(r, piece), p.pages.k + e, bytes);
           cp_async16(dst + TILE_BYTES + tile_at(r, piece), p.pages.v + e, bytes);
+        }
+        ++issued;
+        if (issued < n) {
+          advance(iss, pre, p.B, p.n_kv);
+          page = page_of();
         }
       }
       cp_async_commit();
