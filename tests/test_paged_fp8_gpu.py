@@ -137,6 +137,13 @@ def test_append_one_token_each(gen, ws, bits, B):
                cu=False)
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("heads,n_kv,dim,halves", [(8, 2, 128, True), (28, 4, 96, False), (5, 1, 64, True)])
+def test_append_many_tokens(gen, ws, bits, heads, n_kv, dim, halves):
+    # a warp takes several batches of a token's rows
+    run_append(gen, ws, bits, heads, n_kv, 64, [3000, 0, 1500, 1, 620], [5, 7, 0, -1, 40], dim, halves, behind=3)
+
+
 def test_append_rounds_as_the_formula(gen, ws):
     """Value rows of every kind: ties, the least and the largest exponents, zero,
     one value at the border of a scale, what is not finite."""
