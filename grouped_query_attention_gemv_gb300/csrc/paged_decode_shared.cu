@@ -35,6 +35,18 @@
 // the unrounded values. Every wait is bounded (gqa_set_wait_limit_ns); one that
 // gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
 // frees TMEM before the CTA exits.
+//
+// Measured (GB300, 6.8 TB/s copied): 38.0 us for 64 sequences with up to 512
+// rows of their own under a prefix of 8,000 (103 MB), 51.8 for 96 under three
+// prefixes of up to 4,095 (210 MB), 24.4 for 32 under 8,000 with up to 8 rows of
+// their own. Of the first: 4.4 us to plan, then 3 to the first chunks and 4 to
+// the first scores, 15 to 20 of streaming and products at 4 to 5 TB/s together,
+// 1.2 for a part's way to memory, 2 from the last CTA's end to the join, 4 to 5
+// for that. Three launches (prefixes, own rows, join) took 68.5; own rows joined
+// in their CTAs 53. Slower were: one Q tile's key tiles shared out between the
+// two issuers (70 us for 60: two stages do not hide the memory for both), and L2
+// asked for tiles ahead, once pages are looked up ahead (54 us for 48.5, a
+// prefix of 32,000).
 #include <math.h>
 
 #include "decode_stream.cuh"
@@ -66,13 +78,13 @@ __host__ __device__ constexpr int own_ints(int B) { return ((4 * B + 1) * 4 + 12
 static_assert(own_ints(PAGED_MAX_SEQS) <= K_OFF &&
               own_ints(PAGED_MAX_SEQS) + decode::WARPS * decode::RING_BYTES <= BAR_OFF, "the plan is not in the way");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-// Costs in us: a key tile (or unit) of an item with one and with two Q tiles,
-// a chunk of own rows by a CTA alone and by the whole memory, and what a CTA of
-// either kind takes beside.
-constexpr float ONE_TILE = 2.f, TWO_TILES = 1.6f, CHUNK = 0.15f, CHUNK_MEMORY = 1.f / 750, PREFIX_MORE = 9.f,
+// Costs in us, measured with CTAs of both kinds running: a key tile (or unit) of
+// an item with one and with two Q tiles, a chunk of own rows by a CTA and by the
+// whole memory, and what a CTA of either kind takes beside. A tenth more or less
+// of them changes the time by 1 or 2%.
+constexpr float ONE_TILE = 2.f, TWO_TILES = 1.6f, CHUNK = 0.15f, CHUNK_MEMORY = 1.f / 750, PREFIX_MORE = 8.f,
                 OWN_MORE = 5.f;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
-constexpr int AHEAD = 16;                       // key tiles that are asked for ahead of their copies at most
 constexpr int SLOTS = 2;                        // items handed from the producer to the other warps
 constexpr uint32_t TMEM_COLS = 512;
 // TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
@@ -455,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         break;
       }
       // Pages of a window of 32 / boxes tiles, a box a lane, and of the next one.
-      const int window = 32 / boxes, ahead = min(AHEAD, window), my_tile = lane / boxes, my_box = lane - my_tile * boxes;
+      const int window = 32 / boxes, my_tile = lane / boxes, my_box = lane - my_tile * boxes;
       const int in_page = (1 << a.pages.page_shift) - 1;
       const int* table = a.pages.table + static_cast<long long>(it.lead) * a.pages.table_stride;
       const int keys = min(it.end, (it.j0 + it.n) * KT);  // behind the item's
@@ -463,16 +475,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto look_up = [&](int j) {  // the window that begins with tile j
         const int key = first_key(j + my_tile);
         return key < keys ? table[key >> a.pages.page_shift] : -1;
-      };
-      // The tiles are asked for well ahead of their copies: these have two stages
-      // to wait in, not enough for the memory's latency beside the own rows' stream.
-      auto ask = [&](int j, int page) {
-        const int row = first_key(j) & in_page;
-        if (first_key(j) >= keys || page < 0 || page >= a.pages.num_pages) return;
-        tma_prefetch_4d(&mk, 0, it.g, row, page);
-        tma_prefetch_4d(&mk, 64, it.g, row, page);
-        tma_prefetch_4d(&mv, 0, it.g, row, page);
-        tma_prefetch_4d(&mv, 64, it.g, row, page);
       };
       int pages = 0, next_pages = look_up(0);
       for (int j = 0; j < it.n && !stop; ++j, ++u) {
@@ -523,10 +525,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         copy(&mv, bs.v_full[s], sbase + V_OFF + s * KV_TILE, held, it.g, row, page);
         vn = u + 1;
-        if (j == 0 && my_tile >= STAGES && my_tile < ahead) ask(my_tile, pages);
-        const int x = in_window + ahead;
-        if (x % window == my_tile) ask(j + ahead, x < window ? pages : next_pages);
-        __syncwarp();
       }
 #pragma unroll
       for (int t = 0; t < NQ; ++t) cs[t] += it.tiles(t, qp);
