@@ -603,9 +603,10 @@ def paged_append(q, k, v, start_pos, rope, k_pages, v_pages, block_table, cu_tok
     columns]. Returns the rotated queries (q_out, which may be q), or None
     without q. rotary_dim: the first dims of a head that are turned (a multiple
     of 16; rope [rows, rotary_dim / 2, 2]), the others are kept; halves: dims i
-    and i + rotary_dim / 2 are a pair instead of 2i and 2i + 1. No other output of the paged operators, and here none of the
-    pages, may share memory with their inputs (a tensor counts from its first
-    byte to its last); key and value pages may interleave but not meet.
+    and i + rotary_dim / 2 are a pair instead of 2i and 2i + 1. But for q_out as
+    q, no output of the paged operators, and here none of the pages, may share
+    memory with their inputs (a tensor counts from its first byte to its last);
+    key and value pages may interleave but not meet.
     Bad positions and table entries are found on the device: ``device_status``
     of the workspace, or of ``default_paged_workspace()`` where none was given."""
     if q is None and q_out is not None:

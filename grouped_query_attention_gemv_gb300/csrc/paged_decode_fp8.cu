@@ -23,7 +23,7 @@
 //     of probabilities has its own running max of s.
 // Measured (GB300, 6.8 TB/s copied): 95 to 103 us for 559 MB (64 sequences of
 // up to 8,192 rows), 49.4 to 53 for 271 MB (one of 131,072), 30.4 for 133 MB
-// (16 of 1,001, 32 KV heads), 11.4 for 33 MB (8 KV heads), 4.2 for one sequence
+// (16 of 1,001, 32 KV heads), 11.2 for 33 MB (8 KV heads), 4.2 for one sequence
 // of 16 rows. What bounds the long ones is the memory at 128-byte rows 1 KB
 // apart: head-major pages ([page, KV head, row]) take 93.5 us where [page, row,
 // KV head] took 104. More in flight changes nothing (3 stages: 99.7 for 99.9) or
@@ -31,7 +31,8 @@
 // to evict first costs 5, 256-byte L2 promotion 20%. Eight KV heads side by side,
 // a warp each, so that neighbouring rows are read together, took 101 us where 96
 // (more parts to join, and the warps drift apart). With more than 8 query heads
-// per KV head the two tiles of heads bound it: 36 us for 88 MB.
+// per KV head the joins are longer and the two tiles of heads bound it: 34 us for
+// 88 MB.
 #include "decode_parts.cuh"
 #include "fp8.cuh"
 
@@ -177,16 +178,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       ahead = issue();
       if (i == 0 || cur.j == 0) {
         const __nv_bfloat16* q = p.q + cur.b * p.q_stride + cur.h * n_rep * HEAD_DIM + 4 * t;
+        uint2 all[NT][8];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int h = nt * 8 + gr;
-          uint2 x[8];
-          uint32_t most = 0;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
-            x[s] = make_uint2(0, 0);
-            if (h < n_rep) x[s] = __ldg(reinterpret_cast<const uint2*>(q + h * HEAD_DIM + 16 * s));
+            all[nt][s] = make_uint2(0, 0);
+            if (nt * 8 + gr < n_rep) all[nt][s] = __ldg(reinterpret_cast<const uint2*>(q + (nt * 8 + gr) * HEAD_DIM + 16 * s));
           }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2(&x)[8] = all[nt];
+          uint32_t most = 0;
 #pragma unroll
           for (int s = 0; s < 8; ++s)
             most = max(most, max(max(finite_bits(bf16_lo(x[s].x)), finite_bits(bf16_hi(x[s].x))),
