@@ -36,13 +36,13 @@
 // gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
 // frees TMEM before the CTA exits.
 //
-// Measured (GB300, 6.8 TB/s copied): 38.0 us for 64 sequences with up to 512
-// rows of their own under a prefix of 8,000 (103 MB), 51.8 for 96 under three
-// prefixes of up to 4,095 (210 MB), 24.4 for 32 under 8,000 with up to 8 rows of
-// their own. Of the first: 4.4 us to plan, then 3 to the first chunks and 4 to
-// the first scores, 15 to 20 of streaming and products at 4 to 5 TB/s together,
-// 1.2 for a part's way to memory, 2 from the last CTA's end to the join, 4 to 5
-// for that. Three launches (prefixes, own rows, join) took 68.5; own rows joined
+// Measured (GB300, 6.8 TB/s copied): 34.0 us for 64 sequences with up to 512
+// rows of their own under a prefix of 8,000 (103 MB), 49.2 to 49.9 for 96 under
+// three prefixes of up to 4,095 (210 MB), 21.0 for 32 under 8,000 with up to 8
+// rows of their own. Of the first: 4.4 us to plan, then 3 to the first chunks and
+// 4 to the first scores, 15 to 20 of streaming and products at 4 to 5 TB/s
+// together, 1.2 for a part's way to memory, 6 from the last CTA's end to that of
+// the join. Three launches (prefixes, own rows, join) took 68.5; own rows joined
 // in their CTAs 53. Slower were: one Q tile's key tiles shared out between the
 // two issuers (70 us for 60: two stages do not hide the memory for both), and L2
 // asked for tiles ahead, once pages are looked up ahead (54 us for 48.5, a
@@ -820,11 +820,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 // order, R float4 of a row a lane. The R rows lie side by side in a prefix's
 // part, 16 bytes each. The kernel waits for its code more than for data, so that
 // it is short: where parts lie was found out beside the streaming.
-constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_WARPS = 8, JOIN_CTAS = 2;  // CTAs per SM: with three, registers go to local memory, 3 us more
 constexpr int MOST_PARTS = 152 * (1 + decode::WARPS);  // of a pair: one per CTA, one per warp
 template <int R, int WAYS>
-__global__ void __launch_bounds__(JOIN_WARPS * 32, 3) shared_join_kernel(const __grid_constant__ SharedJoinParams a) {
-  constexpr int PARTS = 32 / R, BATCH = R == 4 ? 3 : 8 / R;
+__global__ void __launch_bounds__(JOIN_WARPS * 32, JOIN_CTAS) shared_join_kernel(const __grid_constant__ SharedJoinParams a) {
+  constexpr int PARTS = 32 / R, BATCH = 8 / R;
   __shared__ float4 others_o[JOIN_WARPS][R][32];
   __shared__ float2 others_ml[JOIN_WARPS][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rr = lane % R, cg = lane / R;
@@ -955,12 +955,14 @@ cudaError_t launch_shared_decode(const PackedPrefillMaps& maps, const SharedDeco
 }
 
 // R: 4 rows where a KV head has as many. Warps for them: as many as still run
-// at once (3 CTAs per SM).
+// at once. 64 sequences under 8,000 rows: 34.0 us with as many as here, 35.8
+// with half, 35.4 with twice as many.
 template <int R>
 static cudaError_t launch_join(SharedJoinParams a, cudaStream_t s) {
   a.sets = (a.n_rep + R - 1) / R;
   const int sets = a.pairs * a.sets;
-  const int ways = sets <= 448 ? 8 : sets <= 896 ? 4 : sets <= 1792 ? 2 : 1, each = JOIN_WARPS / ways;
+  constexpr int WARPS_AT_ONCE = 152 * JOIN_CTAS * JOIN_WARPS;
+  const int most = WARPS_AT_ONCE / sets, ways = most >= 8 ? 8 : most >= 4 ? 4 : most >= 2 ? 2 : 1, each = JOIN_WARPS / ways;
   const auto kernel = ways == 8 ? shared_join_kernel<R, 8> : ways == 4 ? shared_join_kernel<R, 4>
                                                          : ways == 2 ? shared_join_kernel<R, 2> : shared_join_kernel<R, 1>;
   return launch_behind(kernel, static_cast<unsigned>((sets + each - 1) / each), JOIN_WARPS * 32, 0, s, a);
