@@ -122,20 +122,20 @@ __device__ __forceinline__ Count count_chunks(Shared& sh, int* pre, int B, Chunk
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += x;
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
+  most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 31) sh.warp_sum[warp] = run;
   if (lane == 0) sh.warp_max[warp] = most;
   if (threadIdx.x < 2 * WARPS) sh.parts[threadIdx.x].first = -1;
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
-  run -= sum;
-  Count c{0, 0};
-  for (int w = 0; w < W; ++w) {
-    if (w == warp) run += c.total;
-    c.total += sh.warp_sum[w];
-    c.longest = max(c.longest, sh.warp_max[w]);
-  }
+  // a lane for each warp: short code, as it is fetched anew by every launch
+  static_assert(W <= 32, "a lane for each warp");
+  const int of_warp = lane < W ? sh.warp_sum[lane] : 0;
+  Count c;
+  c.total = __reduce_add_sync(0xffffffffu, of_warp);
+  c.longest = __reduce_max_sync(0xffffffffu, lane < W ? sh.warp_max[lane] : 0);
+  run += __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0) - sum;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     run += pre[b + 1];

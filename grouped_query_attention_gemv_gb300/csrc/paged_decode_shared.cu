@@ -284,11 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) gs.units[0] = gs.rows[0] = 0;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      run[k] -= sum[k];
-#pragma unroll 1
-      for (int w = 0; w < warp; ++w) run[k] += bs.warp_sum[w][k];
-    }
+    for (int k = 0; k < 2; ++k) run[k] += __reduce_add_sync(0xffffffffu, lane < warp ? bs.warp_sum[lane][k] : 0) - sum[k];
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       run[0] += gs.units[g + 1];
