@@ -19,7 +19,7 @@ constexpr int WARPS = 8;
 // across CTAs (2.5 us).
 constexpr float ALONE = 85.f, JOIN_COST = 2000.f;
 constexpr int BATCH = 5;             // partials a warp has in flight when it joins
-constexpr int TOGETHER = 4;          // parts of a CTA's warps that are read together (1: 1 us more, 8: 0.1 to 0.9)
+constexpr int TOGETHER = 2;          // parts of a CTA's warps that are read together (1: 1 us more, 4: 0.1, 8: 0.2 to 1)
 constexpr int PART = HEAD_DIM + 2;   // floats of a partial row: o, max, sum
 
 // A place in the chunk order.
@@ -81,6 +81,13 @@ __device__ __forceinline__ void rescale(float& m, float mx, float& l, float4& o)
   m = mx;
   l *= s;
   o = make_float4(o.x * s, o.y * s, o.z * s, o.w * s);
+}
+
+// The largest of a warp's values (NaN only where all are).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Zeros for all heads of sequence b, by the whole CTA.
@@ -203,9 +210,7 @@ __device__ __forceinline__ void join_parts(Shared& sh, float* work, const Split&
           m_e = ml.x;
           l_e = ml.y;
         }
-        float m = m_e;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float m = warp_max(m_e);
         const float w_e = ex2_approx(m_e - (m == -INFINITY ? 0.f : m));
         float l = w_e * l_e;
 #pragma unroll
