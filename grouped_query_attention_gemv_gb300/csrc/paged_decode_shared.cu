@@ -36,10 +36,10 @@
 // gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
 // frees TMEM before the CTA exits.
 //
-// Measured (GB300, 6.8 TB/s copied): 34.0 us for 64 sequences with up to 512
-// rows of their own under a prefix of 8,000 (103 MB), 49.2 to 49.9 for 96 under
-// three prefixes of up to 4,095 (210 MB), 21.0 for 32 under 8,000 with up to 8
-// rows of their own. Of the first: 4.4 us to plan, then 3 to the first chunks and
+// Measured (GB300, 6.8 TB/s copied): 33.7 us for 64 sequences with up to 512
+// rows of their own under a prefix of 8,000 (103 MB), 49.4 for 96 under
+// three prefixes of up to 4,095 (210 MB), 20.3 for 32 under 8,000 with up to 8
+// rows of their own. Of the first: 3.8 us to plan, then 3 to the first chunks and
 // 4 to the first scores, 15 to 20 of streaming and products at 4 to 5 TB/s
 // together, 1.2 for a part's way to memory, 6 from the last CTA's end to that of
 // the join. Three launches (prefixes, own rows, join) took 68.5; own rows joined

@@ -12,7 +12,7 @@ from tests.test_paged_gpu import LAYOUTS, fill_cache, ints
 
 pytestmark = pytest.mark.gpu
 
-LEAST = 200_000   # cache rows x KV heads that sharing has to save
+LEAST = 200_000   # saving as many cache rows x KV heads, a batch shares
 
 
 @pytest.fixture(scope="module")
