@@ -9,9 +9,13 @@
 // 5th-generation tensor cores as the prefill attention does
 // (packed_prefill.cu, whose tiles and turns these are), without a causal mask:
 //   * An item is two 128-row Q tiles (128 / n_rep sequences x n_rep heads each)
-//     of one KV head and the whole prefix. S = Q K^T goes to TMEM, P as bf16 over
-//     its first half, O += P V; 128-key tiles, staged once for both Q tiles, whose
-//     issuers take turns so that one's softmax runs beside the other's products.
+//     of one KV head and the whole prefix. S = Q K^T goes to TMEM, P over it, O +=
+//     P V; 128-key tiles, staged once for both Q tiles, whose issuers take turns
+//     so that one's softmax runs beside the other's products.
+//   * P enters the product as two bf16 terms, as in paged_decode.cu: the upper 16
+//     bits and the rest, each over half of the columns of the scores that it
+//     comes from, O += hi V + lo V. A sequence is then as exact in a batch that
+//     shares as in one that does not, for a product of three more a tile.
 //   * The key tiles of all items, ITEM_UNITS more for each, are cut into one equal
 //     range per CTA. A CTA's piece of an item leaves a part in the workspace,
 //     at (rows of the items before) + 256 x CTA: from one piece to the next
@@ -31,8 +35,7 @@
 //   warp 8        TMA producer: 128 / min(page, 128) boxes a tile, one lane each
 //   warps 9, 10   MMA issuers, one per Q tile
 //   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
-// P is rounded to bf16 (the product takes no wider operand); sums are fp32 of
-// the unrounded values. Every wait is bounded (gqa_set_wait_limit_ns); one that
+// Sums are fp32 of the probabilities before they are cut in two. Every wait is bounded (gqa_set_wait_limit_ns); one that
 // gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
 // frees TMEM before the CTA exits.
 //
@@ -87,7 +90,8 @@ constexpr float ONE_TILE = 2.f, TWO_TILES = 1.6f, CHUNK = 0.15f, CHUNK_MEMORY = 
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                        // items handed from the producer to the other warps
 constexpr uint32_t TMEM_COLS = 512;
-// TMEM columns: S (128, P over its first 64) of Q tiles 0 and 1, then O of both
+// TMEM columns: S (128; P over it, of each half of the keys its upper and its lower
+// terms) of Q tiles 0 and 1, then O of both
 constexpr uint32_t S_COLS = 128, O_COL = 256, O_COLS = 128;
 constexpr float RESCALE_LOG2 = 8.f;
 
@@ -155,6 +159,18 @@ struct ItemWalk {
 struct Groups {
   int *cu, *prefix, *lead, *units, *rows;
 };
+
+// Two probabilities as bf16 pairs: their upper 16 bits, and the rest. The rest is
+// above 0 where the probability is (a 2^-23 of it is added, far below its own
+// rounding of 2^-15, and 2^-133, the least bf16), so that an infinite value gives
+// an infinite sum and not a NaN.
+__device__ __forceinline__ void two_terms(float2 p, uint32_t& hi, uint32_t& lo) {
+  const uint32_t u0 = __float_as_uint(p.x), u1 = __float_as_uint(p.y);
+  hi = __byte_perm(u0, u1, 0x7632);
+  const float2 minus = make_float2(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u), __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u));
+  const float2 rest = add2(fma2(p, make_float2(1.f + 0x1p-23f, 1.f + 0x1p-23f), minus), make_float2(0x1p-133f, 0x1p-133f));
+  lo = pack_bf16(rest.x, rest.y);
+}
 
 __device__ __forceinline__ int tiles_of(int prefix) { return ceil_div(prefix, KT); }
 
@@ -601,10 +617,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (h == 1 && read == HALF) break;  // no keys in the second half
             if (elect_one()) {
 #pragma unroll
-              for (int ks = 0; ks < HALF / 16; ++ks)
-                umma_bf16_ts(o_at, s_at + h * (HALF / 2) + ks * 8,
-                             umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF), idesc_o,
-                             (j > 1 || h > 0 || ks > 0) ? 1u : 0u);
+              for (int ks = 0; ks < HALF / 16; ++ks) {
+                const uint64_t v = umma_desc_sw128_mn(vt + (h * HALF + ks * 16) * 128, KV_HALF);
+                umma_bf16_ts(o_at, s_at + h * HALF + ks * 8, v, idesc_o, (j > 1 || h > 0 || ks > 0) ? 1u : 0u);
+                umma_bf16_ts(o_at, s_at + h * HALF + HALF / 2 + ks * 8, v, idesc_o, 1u);
+              }
             }
             __syncwarp();
           }
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int h = 0; h < 2; ++h) {
           if (works && (h == 0 || second)) {
             if (h == 1) load(1);
-            uint32_t pk[HALF / 2];
+            uint32_t hi[HALF / 2], lo[HALF / 2];
 #pragma unroll
             for (int cc = 0; cc < HALF; cc += 4) {
               const float2 e = fma2(make_float2(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, ng2);
@@ -738,10 +755,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               const float2 q = make_float2(ex2_approx(f.x), ex2_approx(f.y));
               sum2 = add2(sum2, p);
               sum3 = add2(sum3, q);
-              pk[cc >> 1] = pack_bf16(p.x, p.y);
-              pk[(cc >> 1) + 1] = pack_bf16(q.x, q.y);
+              two_terms(p, hi[cc >> 1], lo[cc >> 1]);
+              two_terms(q, hi[(cc >> 1) + 1], lo[(cc >> 1) + 1]);
             }
-            tmem_st32(s_at + h * (HALF / 2), pk);
+            tmem_st32(s_at + h * HALF, hi);
+            tmem_st32(s_at + h * HALF + HALF / 2, lo);
             tmem_st_wait();
           }
           tc_fence_before();

@@ -510,11 +510,10 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
  * or an unused slot) is attended by itself, and so are all where sharing would
  * not pay: where it saves fewer cache rows than a threshold, with more than
  * 1,024 groups, with more than 28,672 query rows (B * n_heads). Probabilities
- * enter the value product of shared rows as in gqa_paged_prefill, of the others
- * as in gqa_paged_decode. cu_groups out of order or range, where it is looked
- * at, is reported as GQA_DEV_BAD_POSITION, and nothing is shared. G at most
- * GQA_PAGED_MAX_SEQS. Two launches, or one where the host can tell that
- * nothing will be shared. */
+ * enter the value product as in gqa_paged_decode, those of shared rows too.
+ * cu_groups out of order or range, where it is looked at, is reported as
+ * GQA_DEV_BAD_POSITION, and nothing is shared. G at most GQA_PAGED_MAX_SEQS.
+ * Two launches, or one where the host can tell that nothing will be shared. */
 int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
                             const int32_t* cu_groups, int G, const int32_t* prefix_rows, const gqa_pages* pages,
                             float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
