@@ -121,12 +121,13 @@ struct SharedParts {
 };
 constexpr int SHARED_MAX_GROUPS = 1024;  // groups that are looked at
 constexpr int SHARED_MAX_ROWS = 28672;   // query rows of a batch that shares (the workspace's room)
-// Cache rows (of one KV head) that sharing has to save, or it is not done. It
-// takes 14 us at least, of which 4 to plan and 4 to join. Measured, plain and
-// shared, 8 KV heads, own rows up to 50: 60,000 rows saved (16 sequences under
-// 500 rows) 8.9 and 14.1 us, 120,000 (16 under 1,000) 12.5 and 14.9, 144,000 (4
-// under 6,000) 17.4 and 17.4, 156,000 (16 under 1,300) 14.3 and 15.1, 173,600 (32
-// under 700) 16.1 and 14.3; up to 400: 156,000 16.8 and 16.3, 173,600 18.3 and 16.8.
+// Cache rows (of one KV head) that sharing has to save, or it is not done: those
+// that are really not read. It takes 14 us at least, of which 4 to plan and 4 to
+// join. Measured, plain and shared, 8 KV heads, 4 query heads each, own rows up to
+// 50: 60,000 rows saved (16 sequences under 500 rows) 8.9 and 14.1 us, 120,000 (16
+// under 1,000) 12.5 and 14.9, 144,000 (4 under 6,000) 17.4 and 17.4, 156,000 (16
+// under 1,300) 14.3 and 15.1, 173,600 (32 under 700) 16.1 and 14.3; up to 400:
+// 156,000 16.8 and 16.3, 173,600 18.3 and 16.8.
 constexpr unsigned long long SHARED_LEAST_ROWS = 150000;
 
 // One new token per sequence over the pages.

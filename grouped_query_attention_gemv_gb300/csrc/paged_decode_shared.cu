@@ -26,10 +26,12 @@
 // (decode_stream.cuh). One kernel does both: some of its CTAs, one per SM, take
 // the prefixes, the others the own rows, as many each as makes both end
 // together by measured costs; every CTA plans alike. A second kernel joins.
-// Which sequences share: those of a group that see all of its prefix
-// (start_pos + 1 >= prefix_rows), if there are two at least and sharing saves
-// enough bytes. The others are streamed from their row 0 on, in rows of the Q
-// tiles that nobody reads.
+// Which sequences share: the members of a group, those that see all of its
+// prefix (start_pos + 1 >= prefix_rows). Its items reach from the first of them to
+// the last, so the prefix is read once for each NQ Q tiles in between. It shares if
+// that is less often than for each member by itself, and if the batch saves
+// enough rows in all. The others are streamed from their row 0 on; where they lie
+// between members, in rows of the Q tiles that nobody reads.
 //
 // Warps of a CTA with prefixes:
 //   warp 8        TMA producer: 128 / min(page, 128) boxes a tile, one lane each
@@ -73,7 +75,7 @@ constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
 constexpr int BARS_BYTES = 1024;
 constexpr int PLAN_OFF = BAR_OFF + BARS_BYTES;
 constexpr int PLAN_ARRAY = SHARED_MAX_GROUPS + 1;
-constexpr int SMEM_BYTES = PLAN_OFF + 5 * PLAN_ARRAY * 4 + 1024;
+constexpr int SMEM_BYTES = PLAN_OFF + 6 * PLAN_ARRAY * 4 + 1024;
 constexpr int THREADS = 352;
 // Shared memory of a CTA with own rows: four numbers of each sequence, then the
 // warps' rings.
@@ -153,11 +155,12 @@ struct ItemWalk {
 };
 
 // The groups in shared memory: sequences cu[g] .. cu[g+1]-1, the rows that they
-// share; of those that do, the first that sees them all, and prefix sums of
-// the units of one KV head and of the query rows of one KV head (no step: does
-// not share).
+// share; lead and size: the first of those that see them all, and how many
+// sequences there are from it to the last (while members are counted: the last);
+// prefix sums of the units of one KV head and of the query rows of one KV head (no
+// step: does not share).
 struct Groups {
-  int *cu, *prefix, *lead, *units, *rows;
+  int *cu, *prefix, *lead, *size, *units, *rows;
 };
 
 // Two probabilities as bf16 pairs: their upper 16 bits, and the rest. The rest is
@@ -184,7 +187,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   Bars& bs = *reinterpret_cast<Bars*>(smem + BAR_OFF);
   __shared__ decode::Shared sh;
   int* plan = reinterpret_cast<int*>(smem + PLAN_OFF);
-  const Groups gs{plan, plan + PLAN_ARRAY, plan + 2 * PLAN_ARRAY, plan + 3 * PLAN_ARRAY, plan + 4 * PLAN_ARRAY};
+  const Groups gs{plan, plan + PLAN_ARRAY, plan + 2 * PLAN_ARRAY, plan + 3 * PLAN_ARRAY, plan + 4 * PLAN_ARRAY,
+                  plan + 5 * PLAN_ARRAY};
   // of each sequence: chunks of own rows before it, its last row, its first own
   // one, its group (-1: it does not share)
   int* pre = reinterpret_cast<int*>(smem);
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();
 
   // ---- the plan, from one look at what it takes. Members of each group
-  // (counted where K tiles will lie) and the first of them.
+  // (counted where K tiles will lie), the first and the last of them.
   int* members = reinterpret_cast<int*>(smem + K_OFF);
 #pragma unroll 1
   for (int b = tid; b < a.B; b += THREADS) last[b] = a.start[b];
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       gs.prefix[g] = sp.prefix[g];
       members[g] = 0;
       gs.lead[g] = a.B;
+      gs.size[g] = -1;
     }
   }
   bad = __syncthreads_or(bad);
@@ -260,6 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         g = lo;
         atomicAdd(&members[g], 1);
         atomicMin(&gs.lead[g], b);
+        atomicMax(&gs.size[g], b);
       }
     }
     group[b] = g;
@@ -270,16 +276,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int g0 = min(tid * per, sp.G), g1 = min(g0 + per, sp.G);
     unsigned long long saved = 0;
 #pragma unroll 1
-    for (int g = g0; g < g1; ++g)
-      if (members[g] > 1) saved += static_cast<unsigned long long>(members[g] - 1) * gs.prefix[g];
+    for (int g = g0; g < g1; ++g) {
+      gs.size[g] = members[g] ? gs.size[g] - gs.lead[g] + 1 : 0;
+      // reads that there are fewer
+      members[g] -= members[g] ? ceil_div(gs.size[g], NQ * qp) : 0;
+      if (members[g] > 0) saved += static_cast<unsigned long long>(members[g]) * gs.prefix[g];
+    }
     if (saved) atomicAdd(&bs.saved, saved);
     __syncthreads();
     const bool shares = bs.saved * a.n_kv >= SHARED_LEAST_ROWS;
     int sum[2] = {0, 0};
 #pragma unroll 1
     for (int g = g0; g < g1; ++g) {
-      const int size = gs.cu[g + 1] - gs.cu[g];
-      const bool on = shares && members[g] > 1;
+      const int size = gs.size[g];
+      const bool on = shares && members[g] > 0;
       const int units = on ? ceil_div(size, NQ * qp) * (tiles_of(gs.prefix[g]) + ITEM_UNITS) : 0;
       gs.units[g + 1] = units;
       gs.rows[g + 1] = on ? size * nrep : 0;
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int b = pair / a.n_kv, h = pair - b * a.n_kv, g = group[b];
     SharedParts r = {};
     if (g >= 0) {
-      const int i = b - gs.cu[g], size = gs.cu[g + 1] - gs.cu[g], e = i / (NQ * qp), w = tiles_of(gs.prefix[g]) + ITEM_UNITS;
+      const int i = b - gs.lead[g], size = gs.size[g], e = i / (NQ * qp), w = tiles_of(gs.prefix[g]) + ITEM_UNITS;
       const int unit = gs.units[g] * a.n_kv + h * (gs.units[g + 1] - gs.units[g]) + e * w;
       const Split split(units, parts);
       const int c0 = split.holder(unit + ITEM_UNITS);
@@ -416,12 +426,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int mid = (lo + hi) >> 1;
           if (gs.units[mid] * a.n_kv <= ru) lo = mid; else hi = mid;
         }
-        const int size = gs.cu[lo + 1] - gs.cu[lo], w = tiles_of(gs.prefix[lo]) + ITEM_UNITS;
+        const int size = gs.size[lo], w = tiles_of(gs.prefix[lo]) + ITEM_UNITS;
         const int pairs = ceil_div(size, NQ * qp), in_group = ru - gs.units[lo] * a.n_kv;
         const int item = in_group / w, in = in_group - item * w, base = ru - in, end = min(rend, base + w);
         const int e = item % pairs;
         x.g = item / pairs;
-        x.seq0 = gs.cu[lo] + e * NQ * qp;
+        x.seq0 = gs.lead[lo] + e * NQ * qp;
         x.nseq = min(NQ * qp, size - e * NQ * qp);
         x.lead = gs.lead[lo];
         x.end = gs.prefix[lo];

@@ -509,11 +509,14 @@ int gqa_paged_decode(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, co
  * A sequence that does not see the whole prefix (start_pos + 1 < prefix_rows,
  * or an unused slot) is attended by itself, and so are all where sharing would
  * not pay: where it saves fewer cache rows than a threshold, with more than
- * 1,024 groups, with more than 28,672 query rows (B * n_heads). Probabilities
- * enter the value product as in gqa_paged_decode, those of shared rows too.
- * cu_groups out of order or range, where it is looked at, is reported as
- * GQA_DEV_BAD_POSITION, and nothing is shared. G at most GQA_PAGED_MAX_SEQS.
- * Two launches, or one where the host can tell that nothing will be shared. */
+ * 1,024 groups, with more than 28,672 query rows (B * n_heads). The shared rows
+ * are read once for each 2 (128 / n_rep) sequences (128 / n_rep rounded down)
+ * from the first that sees them all to the last; a group in which that is no less
+ * often than for each such sequence does not share. Probabilities enter the value
+ * product as in gqa_paged_decode, those of shared rows too. cu_groups out of
+ * order or range, where it is looked at, is reported as GQA_DEV_BAD_POSITION, and
+ * nothing is shared. G at most GQA_PAGED_MAX_SEQS. Two launches, or one where the
+ * host can tell that nothing will be shared. */
 int gqa_paged_decode_shared(const gqa_bf16* q, int64_t q_stride, int B, int n_heads, const int32_t* start_pos,
                             const int32_t* cu_groups, int G, const int32_t* prefix_rows, const gqa_pages* pages,
                             float scale, gqa_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
