@@ -84,11 +84,12 @@ static_assert(own_ints(PAGED_MAX_SEQS) <= K_OFF &&
               own_ints(PAGED_MAX_SEQS) + decode::WARPS * decode::RING_BYTES <= BAR_OFF, "the plan is not in the way");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 // Costs in us, measured with CTAs of both kinds running: a key tile (or unit) of
-// an item with one and with two Q tiles, a chunk of own rows by a CTA and by the
-// whole memory, and what a CTA of either kind takes beside. A tenth more or less
-// of them changes the time by 1 or 2%.
-constexpr float ONE_TILE = 2.f, TWO_TILES = 1.6f, CHUNK = 0.15f, CHUNK_MEMORY = 1.f / 750, PREFIX_MORE = 8.f,
-                OWN_MORE = 5.f;
+// an item with one and with two Q tiles, a chunk of own rows by a CTA (with 8
+// query heads per KV head at most, and with more) and by the whole memory, and
+// what a CTA of either kind takes beside. A tenth more or less of them changes the
+// time by 1 or 2%.
+constexpr float ONE_TILE = 2.4f, TWO_TILES = 2.2f, CHUNK = 0.15f, WIDE_CHUNK = 0.2f, CHUNK_MEMORY = 1.f / 750,
+                PREFIX_MORE = 8.f, OWN_MORE = 5.f;
 constexpr int PRODUCER_WARP = 8, MMA_WARP = 9;  // MMA warps 9 (Q tile 0) and 10 (Q tile 1)
 constexpr int SLOTS = 2;                        // items handed from the producer to the other warps
 constexpr uint32_t TMEM_COLS = 512;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float tile = static_cast<float>(bs.tiles[0]) * ONE_TILE + static_cast<float>(bs.tiles[1]) * TWO_TILES;
     float cost = INFINITY;
     if (tid > 0 && tid <= grid && (tid < grid || chunks == 0)) {
-      const float own = chunks > 0 ? fmaxf(chunks * CHUNK / (grid - tid), chunks * CHUNK_MEMORY) + OWN_MORE : 0.f;
+      const float own = chunks > 0 ? fmaxf(chunks * (NT > 1 ? WIDE_CHUNK : CHUNK) / (grid - tid), chunks * CHUNK_MEMORY) + OWN_MORE : 0.f;
       cost = fmaxf(tile * a.n_kv / tid + PREFIX_MORE, own);
     }
     const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));
