@@ -436,6 +436,7 @@ int gqa_paged_decode_fp8(const gqa_bf16* q, int64_t q_stride, int B, int n_heads
   p.part_o = reinterpret_cast<float*>(ws + PART_O_OFFSET);
   p.status = reinterpret_cast<int*>(ws);
   p.ctas = launch_sms();
+  p.wait_ns = wait_limit_ns();
   Fp8DecodeMaps maps;
   const cuuint64_t dims[4] = {HEAD_DIM, static_cast<cuuint64_t>(p.n_kv), static_cast<cuuint64_t>(pages->page_size),
                               static_cast<cuuint64_t>(pages->num_pages)};

@@ -202,6 +202,26 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   return true;
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// mbar_wait that keeps short limits too: a try may be held up for some
+// microseconds, in which most copies land, and the timer counts in steps of about
+// one, so under a limit below 100 it looks instead, and counts two cycles a ns.
+__device__ __forceinline__ bool mbar_wait_within(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  if (limit_ns >= 100000) return mbar_wait(bar, parity, limit_ns);
+  const long long t0 = clock64();
+  while (!mbar_test_wait(bar, parity)) {
+    if (clock64() - t0 > 2 * static_cast<long long>(limit_ns)) return false;
+  }
+  return true;
+}
+
 // mbar_wait that also gives up (false) as soon as *abort, a shared-memory
 // flag a producer raises when it stops issuing, becomes non-zero: consumers
 // then leave a phase whose loads will not come without waiting out the limit.

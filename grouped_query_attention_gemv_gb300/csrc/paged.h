@@ -181,6 +181,7 @@ struct Fp8DecodeParams {
   int* tickets;
   int* status;
   int ctas;
+  unsigned long long wait_ns;  // limit of the waits
 };
 struct Fp8DecodeMaps {
   CUtensorMap k, v;

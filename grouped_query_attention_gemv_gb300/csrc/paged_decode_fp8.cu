@@ -21,6 +21,8 @@
 //     running max of s + e, so that the largest term has all bits whatever the
 //     scales, and 11 bits (f16) are left of each down to 2^-29 of it. The sum
 //     of probabilities has its own running max of s.
+//   * The waits on the copies are bounded (gqa_set_wait_limit_ns). One that gives up
+//     records DEV_WAIT_TIMEOUT; its CTA lets issued copies land and joins nothing.
 // Measured (GB300, 6.8 TB/s copied): 93 to 101 us for 559 MB (64 sequences of
 // up to 8,192 rows), 49.4 to 53 for 271 MB (one of 131,072), 30.4 for 133 MB
 // (16 of 1,001, 32 KV heads), 11.1 for 33 MB (8 KV heads), 4.1 for one sequence
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   const int gr = lane >> 2, t = lane & 3;
   const int half = lane >> 4;
 
+  bool ok = true;  // false: a wait gave up
   if (n > 0) {
     Cursor iss = locate(a0, pre, p.B, p.n_kv), cur = iss;
     const int in_page = (1 << p.pages.page_shift) - 1;
@@ -172,7 +175,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     uint32_t qb[NT][8][2];  // Q^T as B fragments: dims 16s + 4t (+1) | +2 (+3), query head 8 nt + gr
     float q_scale[NT][2];   // what takes the products of heads 8 nt + 2t (+1) to scores in log2 units
     float m_run[NT][2], l_run[NT][2], v_run[NT][2], oacc[NT][8][4];  // heads 8 nt + 2t (+1); O^T tile d: dims 16d + 2 gr (+1)
-    bool ok = true;
     for (int i = 0; i < n; ++i) {
       const Scales scales = ahead;
       ahead = issue();
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
           for (int d = 0; d < 8; ++d) oacc[nt][d][0] = oacc[nt][d][1] = oacc[nt][d][2] = oacc[nt][d][3] = 0.f;
         }
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][i % STAGES]), (i / STAGES) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait_within(smem_u32(&full[warp][i % STAGES]), (i / STAGES) & 1, p.wait_ns));
       if (!ok) break;
       const uint32_t kt = ring32 + (i % STAGES) * STAGE_BYTES, vt = kt + TILE_BYTES;
       const int left = last[cur.b] - cur.j * KEYS;
@@ -395,12 +397,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
       }
     }
     if (!ok) {
-      // the copies in flight may still land
+      // the copies in flight land in the ring: nothing else is done with it before
       if (lane == 0) report(p.status, DEV_WAIT_TIMEOUT);
       for (int u = max(0, issued - STAGES); u < issued; ++u) mbar_wait(smem_u32(&full[warp][u % STAGES]), (u / STAGES) & 1);
     }
   }
-  __syncthreads();
+  // A CTA that gave up joins nothing, and counts at no ticket.
+  if (__syncthreads_or(!ok)) return;
   join_parts(
       sh, reinterpret_cast<float*>(smem), split, blockIdx.x, c0, c1, n_rep, p.part_o, p.part_ml, p.tickets,
       [&](int e) -> const float* {

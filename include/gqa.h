@@ -252,18 +252,18 @@ int gqa_set_decode_fusion(int enable);
 int gqa_set_decode_attention_split(int mode);
 
 /* Limit, for calls made on the calling thread, of the waits of the packed
- * prefill attention (gqa_paged_prefill, gqa_packed_prefill) and of
- * gqa_paged_decode_shared's prefixes (GQA_DEV_WAIT_TIMEOUT
- * then, rows unspecified, and the workspace to be zero-filled) and of the
- * grid-wide waits of the block's decode kernels: the one-kernel step's two gates (every CTA's Q|K|V rows
- * published; every attention output published) and the attention's meeting
- * before its merges. A wait that runs out records GQA_DEV_WAIT_TIMEOUT in the
- * workspace status word; the kernel then skips the work that needed the
- * wait, lets its own loads land, leaves the grid counters reset and exits
- * (the call's output is unspecified). ns = 0 restores the default of 2 s
- * (2,000,000,000 ns). Returns the previous limit. Meant for tests and for
- * callers that prefer a fast error over a long stall; the waits on the block
- * kernels' own data loads keep their 2 s limit. */
+ * prefill attention (gqa_paged_prefill, gqa_packed_prefill), of
+ * gqa_paged_decode_shared's prefixes and of gqa_paged_decode_fp8's copies
+ * (GQA_DEV_WAIT_TIMEOUT then, rows unspecified, and the workspace to be
+ * zero-filled) and of the grid-wide waits of the block's decode kernels: the
+ * one-kernel step's two gates (every CTA's Q|K|V rows published; every attention
+ * output published) and the attention's meeting before its merges. A wait that
+ * runs out records GQA_DEV_WAIT_TIMEOUT in the workspace status word; the kernel
+ * then skips the work that needed the wait, lets its own loads land, leaves the
+ * grid counters reset and exits (the call's output is unspecified). ns = 0
+ * restores the default of 2 s (2,000,000,000 ns). Returns the previous limit.
+ * Meant for tests and for callers that prefer a fast error over a long stall; the
+ * waits on the block kernels' own data loads keep their 2 s limit. */
 unsigned long long gqa_set_wait_limit_ns(unsigned long long ns);
 
 /* Measurement hook; it changes nothing the block computes. While set, every
