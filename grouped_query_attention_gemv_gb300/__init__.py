@@ -634,8 +634,8 @@ def paged_append_fp8(q, k, v, start_pos, rope, k_pages, v_pages, k_scales, v_sca
     times 2^(s - 127), s the row's byte in k_scales, v_scales (torch.uint8
     [pages, page_size, n_kv], any strides, memory of their own). The exponent is
     the least in [-100, 120] for which the row's finite values fit, so a value
-    is off by 2^-4 of itself at most (by 2^-10 of the scale below 2^-6 of it);
-    what is not finite is held as NaN. The queries are rotated and returned as
+    is off by 2^-4 of itself at most (by 2^-10 of the scale below 2^-6 of it),
+    and none is read back past 240 x 2^120; what is not finite is held as NaN. The queries are rotated and returned as
     by ``paged_append``."""
     if q is None and q_out is not None:
         raise ValueError("q_out needs q")

@@ -4,7 +4,9 @@
 // with one is exact, so each value is rounded once, by half a step of 2^-3
 // relative at most, and the way back to bf16 is exact (4 significant bits); a
 // float format gains nothing from a finer scale. LEAST_E keeps the products of
-// the decode attention normal: rows below 2^-91 are held in steps of 2^-109.
+// the decode attention normal: rows below 2^-91 are held in steps of 2^-109. At
+// MOST_E, 248 and more would round to 256, and 256 x 2^120 is past the largest
+// float: what is past 240 is held as 240, by 2^-4 of itself off at most as well.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -14,6 +16,7 @@
 namespace gqa {
 
 constexpr int LEAST_E = -100, MOST_E = 120;
+constexpr float MOST_UNITS = 240.f;  // at MOST_E
 
 // e for the largest |x| of a row, given as its bits (finite).
 __device__ __forceinline__ int row_exponent(uint32_t bits) {
@@ -26,6 +29,8 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(st
 // 2^e of a scale byte
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// A value of a row at MOST_E, in units, within reach of what reads it (NaN stays).
+__device__ __forceinline__ float within_reach(float x) { return fabsf(x) > MOST_UNITS ? copysignf(MOST_UNITS, x) : x; }
 // Two values to e4m3 (ties to even, in range), x in the lower byte.
 __device__ __forceinline__ uint32_t to_e4m3x2(float x, float y) {
   uint16_t r;

@@ -177,6 +177,10 @@ __global__ void __launch_bounds__(WARPS * 32) rotary_append_kernel(const __grid_
     const float2 s = make_float2(power_of_two(-e), power_of_two(-e));
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = mul2(f[k], s);
+    if (e == MOST_E) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = make_float2(within_reach(f[k].x), within_reach(f[k].y));
+    }
     return make_uint2(to_e4m3x2(f[0].x, f[0].y) | to_e4m3x2(f[1].x, f[1].y) << 16,
                       to_e4m3x2(f[2].x, f[2].y) | to_e4m3x2(f[3].x, f[3].y) << 16);
   };

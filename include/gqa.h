@@ -448,8 +448,9 @@ int gqa_paged_append_rotary(const gqa_bf16* q, int64_t q_stride, const gqa_bf16*
  * of 1 at least): the row's exponent + 127. A value is its e4m3 times
  * 2^exponent. The exponent is the least integer in [-100, 120] with |x| <= 448 *
  * 2^exponent for all finite x of the row, so that the one rounding is that to
- * e4m3 (ties to even), and reading back is exact. What is not finite is held
- * as NaN. The rest as in gqa_pages. Values and scales lie in memory of their
+ * e4m3 (ties to even; at exponent 120 to 240 at most, as 256 * 2^120 is no float),
+ * and reading back is exact. What is not finite is held as NaN. The rest as in
+ * gqa_pages. Values and scales lie in memory of their
  * own (k and v may interleave, and k_scale and v_scale). */
 typedef struct gqa_fp8_pages {
   uint8_t* k;
