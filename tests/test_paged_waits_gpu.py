@@ -10,6 +10,7 @@ from tests import paged as P
 from tests import paged8 as Q
 from tests.test_paged_fp8_gpu import check_decode
 from tests.test_paged_gpu import ints
+from tests.test_paged_shared_gpu import Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -58,4 +59,24 @@ def test_waits_of_the_8_bit_decode(gen, heads, n_kv, page, lens, waits):
         G.paged_decode_fp8(q, start, *cache, out=out, workspace=ws)
         assert G.device_status(ws) == 0
         check_decode(out, q, rows)
+    assert (guard[[0, -1]] == 9.0).all()
+
+
+@pytest.mark.parametrize("heads,n_kv,prefix,members", [(32, 8, 40_000, 16), (16, 1, 100_000, 40)])
+def test_waits_of_shared_rows(gen, heads, n_kv, prefix, members):
+    """A prefix of many tiles a CTA: its products, softmaxes and copies wait for one another at each."""
+    ws = G.make_paged_workspace()
+    x = Batch(gen, n_kv, 64, [(prefix, [prefix + 30 * i for i in range(members)])])
+    assert x.pays
+    q = P.normal(gen, members, heads, P.D)
+    guard = torch.full((members + 2, heads, P.D), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[1:-1]
+    for _ in range(3):
+        given_up(lambda: G.paged_decode_shared(q, *x.args(), out=out, workspace=ws), (x.k_pages, x.v_pages))
+        assert G.device_status(ws, clear=True) == 2
+        assert (guard[[0, -1]] == 9.0).all()
+        ws.zero_()
+        G.paged_decode_shared(q, *x.args(), out=out, workspace=ws)
+        assert G.device_status(ws) == 0
+        x.check(out, q)
     assert (guard[[0, -1]] == 9.0).all()
