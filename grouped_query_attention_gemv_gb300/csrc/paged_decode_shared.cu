@@ -875,7 +875,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, JOIN_CTAS) shared_join_kernel
     float2 ml = make_float2(-INFINITY, 0.f);
     const bool own = k >= s.prefixes;
     const int part = own ? s.own + (k - s.prefixes) * a.n_rep : s.prefix + k * (NQ * ROWS);
-    if (real && k < all && part >= 0 && (own ? part + h < a.own_rows : s.at + h >= 0 && s.at + h < s.span && part + s.span <= a.part_rows)) {
+    if (real && k < all && part >= 0 &&
+        (own ? part < a.own_rows - h
+             : s.at >= 0 && s.at <= a.part_rows && s.at + h < s.span && s.span <= a.part_rows - part)) {
       ml = reinterpret_cast<const float2*>(own ? a.own_ml : a.part_ml)[part + (own ? 0 : s.at) + h];
       at = own ? a.own_at + (part + h) * (HEAD_DIM / 4) : part * (HEAD_DIM / 4) + s.at + h;
       apart = own ? 1 : s.span;
