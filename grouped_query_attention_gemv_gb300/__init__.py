@@ -692,7 +692,9 @@ def paged_decode_shared(q, start_pos, cu_groups, prefix_rows, k_pages, v_pages, 
     cu_groups[g+1]-1 (device int32 [G+1], non-decreasing; sequences outside are
     in no group) have cache rows 0..prefix_rows[g]-1 (device int32 [G]) in
     common, on the same pages or on copies. A sequence that does not see its
-    group's whole prefix is attended by itself."""
+    group's whole prefix is attended by itself, and so are all where sharing
+    would save too little or is not provided for: with more than 1,024 groups, or
+    more than 28,672 query rows (B x heads)."""
     if out is None or workspace is None:
         out, workspace = _defaults(q, "q", out, workspace, stream)
     r = (_paged or _binding()).paged_decode_shared(q, start_pos, cu_groups, prefix_rows, k_pages, v_pages, block_table,

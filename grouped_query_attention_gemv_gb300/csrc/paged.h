@@ -122,12 +122,16 @@ struct SharedParts {
 constexpr int SHARED_MAX_GROUPS = 1024;  // groups that are looked at
 constexpr int SHARED_MAX_ROWS = 28672;   // query rows of a batch that shares (the workspace's room)
 // Cache rows (of one KV head) that sharing has to save, or it is not done: those
-// that are really not read. It takes 14 us at least, of which 4 to plan and 4 to
-// join. Measured, plain and shared, 8 KV heads, 4 query heads each, own rows up to
-// 50: 60,000 rows saved (16 sequences under 500 rows) 8.9 and 14.1 us, 120,000 (16
-// under 1,000) 12.5 and 14.9, 144,000 (4 under 6,000) 17.4 and 17.4, 156,000 (16
-// under 1,300) 14.3 and 15.1, 173,600 (32 under 700) 16.1 and 14.3; up to 400:
-// 156,000 16.8 and 16.3, 173,600 18.3 and 16.8.
+// that are really not read. It takes 15 us at least, of which 4 to plan and 4 to
+// join. Measured, plain and shared, own rows up to 50, 100,000 / 150,000 / 200,000
+// rows saved: 8 KV heads of 4 query heads, 4 sequences 14.2 and 17.1 us / 18.9 and
+// 18.4 / 22.1 and 20.3, 16 sequences 10.7 and 16.8 / 14.1 and 16.5 / 16.8 and 17.8,
+// 32 sequences 12.5 and 16.5 / 15.0 and 17.0 / 17.3 and 16.7; 32 KV heads of 1, 16
+// sequences 12.9 and 14.8 / 15.3 and 16.0 / 17.5 and 16.3; 4 KV heads of 16, 16
+// sequences 18.2 and 20.3 / 21.5 and 20.7 / 24.5 and 22.6; one KV head of 16, 4
+// sequences 31.9 and 25.9 / 37.2 and 30.7 / 40.8 and 34.1, 64 sequences 18.2 and
+// 20.2 / 20.7 and 20.7 / 23.9 and 21.1. One number is within 2.5 us of the better
+// way but for few sequences of 16 heads on one KV head (6).
 constexpr unsigned long long SHARED_LEAST_ROWS = 150000;
 
 // One new token per sequence over the pages.
