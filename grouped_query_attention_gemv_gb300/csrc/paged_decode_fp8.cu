@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
   int* last = pre + p.B + 1;  // last row of each sequence
   __shared__ Shared sh;
   __shared__ uint64_t full[WARPS][STAGES];
+  __shared__ int gave_up;  // a wait did
+  if (threadIdx.x == 0) gave_up = 0;
 
   if (lane < STAGES) mbar_init(smem_u32(&full[warp][lane]), 1);
   fence_barrier_init();
@@ -403,7 +405,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     }
   }
   // A CTA that gave up joins nothing, and counts at no ticket.
-  if (__syncthreads_or(!ok)) return;
+  if (!ok) gave_up = 1;
+  __syncthreads();
+  if (gave_up) return;
   join_parts(
       sh, reinterpret_cast<float*>(smem), split, blockIdx.x, c0, c1, n_rep, p.part_o, p.part_ml, p.tickets,
       [&](int e) -> const float* {
