@@ -97,6 +97,10 @@ constexpr uint32_t TMEM_COLS = 512;
 // terms) of Q tiles 0 and 1, then O of both
 constexpr uint32_t S_COLS = 128, O_COL = 256, O_COLS = 128;
 constexpr float RESCALE_LOG2 = 8.f;
+// The exponent of a score is s x scale - m in one rounding, m = m_ref x scale rounded:
+// off by half a step of m for all alike, which cancels, but past 2^30 is no
+// exponent any more. From here on m_ref is taken off the scores instead.
+constexpr float FAR = 0x1p24f;
 
 // A CTA's piece of an item: KV head g, sequences seq0 .. seq0 + nseq - 1, key
 // tiles j0 .. j0 + n - 1 of the prefix's `end` keys, read by sequence lead's
@@ -686,6 +690,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float m_ref = -INFINITY;  // max the current P values and O are taken against (raw score units)
       float l = 0.f;
       float m_limit = -INFINITY, neg = 0.f;  // max that P is still taken against m_ref with; -m_ref in log2 units
+      float far = 0.f;                       // m_ref, taken off beforehand, where `neg` would be past FAR (and is 0 then)
       for (int j = 0; j < n_t; ++j) {
         // S_j is there, and with it every product before it, P_{j-1} V_{j-1} among them
         if (!wait_bar(bs, bs.s_full[t], (cs + j) & 1)) {
@@ -732,6 +737,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               m_ref = mx;
               m_limit = mx + RESCALE_LOG2 / scale;
               neg = -mx * scale;
+              far = 0.f;
+              if (!(fabsf(neg) <= FAR)) {
+                far = mx;
+                neg = 0.f;
+              }
               l *= alpha;
             }
             if (j > 0) {
@@ -752,10 +762,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         // exponent arguments and the row sum two columns per instruction
         const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(neg, neg);
         float2 sum2 = make_float2(0.f, 0.f), sum3 = sum2;
+        const bool any_far = __any_sync(0xffffffffu, far != 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (works && (h == 0 || second)) {
             if (h == 1) load(1);
+            if (any_far) {
+#pragma unroll
+              for (int cc = 0; cc < HALF; ++cc) sr[cc] = __float_as_uint(__uint_as_float(sr[cc]) - far);
+            }
             uint32_t hi[HALF / 2], lo[HALF / 2];
 #pragma unroll
             for (int cc = 0; cc < HALF; cc += 4) {

@@ -81,3 +81,25 @@ def test_an_infinite_value_of_little_weight_is_an_infinity(gen, ws, below):
         assert (o[:, 4:, 9] == math.inf).all() and (o[:, 4:, 60] == -math.inf).all()
         o[:, 4:, [9, 60]] = 0.0
         assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("size", [2.0 ** 8, 2.0 ** 12, 2.0 ** 14, 2.0 ** 15, 2.0 ** 20, 2.0 ** 50])
+def test_scores_of_any_size(gen, ws, size):
+    """Queries and keys of up to 2^50: one key has all the weight, its values come
+    back as they are, but where the second is near: a score is 8 product steps of
+    17 x 2^-23 of its terms off, in sum some twice the largest score, below 2^-10 of it."""
+    p = 6000
+    x = Batch(gen, 2, 64, [(p, [p + 5 * i for i in range(18)])])
+    assert x.pays
+    q = P.normal(gen, 18, 8, P.D, scale=size)
+    k_pages = (x.k_pages.float() * size).bfloat16()
+    start, cu, prefix, _, *rest = x.args()
+    out = G.paged_decode_shared(q, start, cu, prefix, k_pages, *rest, workspace=ws)
+    assert G.last_launch_count() == 2 and G.device_status(ws) == 0
+    for b, (k, v) in enumerate(x.rows):
+        for h in range(8):
+            s = (k[:, h // 4].double() * size) @ q[b, h].double() * P.D ** -0.5
+            top = s.topk(2)
+            if float(top.values[0] - top.values[1]) > 40 + float(top.values[0]) * 2.0 ** -10:
+                assert torch.equal(out[b, h], v[int(top.indices[0]), h // 4]), f"sequence {b}, head {h}"
+    assert torch.isfinite(out).all()
