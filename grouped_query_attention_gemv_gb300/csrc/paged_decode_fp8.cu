@@ -17,10 +17,11 @@
 //     largest dim to [2^14, 2^15): 11 bits for the 8 of bf16, exact down to
 //     2^-28 of the largest dim, 2^-39 of it off below.
 //   * A score is the product times the key's scale, in fp32. Values' scales go
-//     into the probabilities, as exponents: 2^(s + e - M + 15) with M the
-//     running max of s + e, so that the largest term has all bits whatever the
-//     scales, and 11 bits (f16) are left of each down to 2^-29 of it. The sum
-//     of probabilities has its own running max of s.
+//     into the probabilities, as exponents: 2^(s - m + e - M + 15) with m the
+//     running max of s, M that of s - m + e, so that the largest term has all bits
+//     whatever the scales, and 11 bits (f16) are left of each down to 2^-29 of it.
+//     e is added to what is left of s once m is taken off: to a score in the
+//     thousands it would be added with a rounding that shows in the result.
 //   * The waits on the copies are bounded (gqa_set_wait_limit_ns). One that gives up
 //     records DEV_WAIT_TIMEOUT; its CTA lets issued copies land and joins nothing.
 // Measured (GB300, 6.8 TB/s copied): 93 to 101 us for 559 MB (64 sequences of
@@ -287,26 +288,31 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         for (int e = 0; e < 2; ++e) {
           float x[4], y[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k)
             x[k] = gr + 8 * k <= left ? (sc[nt][k >> 1][(k & 1) * 2 + e] + sd[nt][k >> 1][(k & 1) * 2 + e]) * (ks[k] * q_scale[nt][e])
                                       : -INFINITY;
+          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = fmaxf(mx, m_run[nt][e]);
+          // scores that are all -inf leave the maximum there: no term, not a NaN
+          const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[k] -= ref;
             y[k] = x[k] + ve[k];
           }
-          float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), my = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          float my = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, o));
-          }
-          mx = fmaxf(mx, m_run[nt][e]);
-          my = fmaxf(my, v_run[nt][e]);
-          // scores that are all -inf leave the maximum there: no term, not a NaN
-          const float ref = mx == -INFINITY ? 0.f : mx, vref = my == -INFINITY ? 0.f : my;
-          al[e] = ex2_approx(v_run[nt][e] - vref);
+          for (int o = 4; o < 32; o <<= 1) my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, o));
+          const float before = v_run[nt][e] + (m_run[nt][e] - ref);
+          my = fmaxf(my, before);
+          const float vref = my == -INFINITY ? 0.f : my;
+          al[e] = ex2_approx(before - vref);
           float sum = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            sum += ex2_approx(x[k] - ref);
+            sum += ex2_approx(x[k]);
             pw[k >> 1][(k & 1) * 2 + e] = ex2_approx(y[k] - vref + P_EXP);
           }
           l_run[nt][e] = l_run[nt][e] * ex2_approx(m_run[nt][e] - ref) + sum;  // this lane's rows; summed over lanes at the end
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
-          to_m[nt][e] = v_run[nt][e] == -INFINITY ? 0.f : ex2_approx(v_run[nt][e] - m_run[nt][e] - P_EXP);
+          to_m[nt][e] = v_run[nt][e] == -INFINITY ? 0.f : ex2_approx(v_run[nt][e] - P_EXP);
         }
       if (seg.first >= a0 && seg.end <= a1) {
         __nv_bfloat16* out = p.out + static_cast<long long>(seg.row) * HEAD_DIM;

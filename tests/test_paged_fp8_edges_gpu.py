@@ -98,3 +98,30 @@ def test_decode_over_the_largest_values(gen, ws, n):
     assert torch.isfinite(out).all()
     assert ((out.double().abs() - want).abs() <= (P.BF16_HALF_STEP + 2.0 ** -10) * want).all()
     assert (out[..., :64] > 0).all() and (out[..., 64:] < 0).all()
+
+
+@pytest.mark.parametrize("size", [1, 2 ** 4, 2 ** 6, 2 ** 8, 2 ** 10, 2 ** 12, 2 ** 20, 2 ** 50])
+@pytest.mark.parametrize("heads,n_kv", [(8, 2), (16, 1)])
+def test_scores_of_any_size(gen, ws, size, heads, n_kv):
+    """Queries and keys of up to 2^50, values on scales 2^-3 to 2^3 of one another.
+    Where one key has all the weight, its values come back as they are, but where
+    the second is near: a score is 8 product steps of 17 x 2^-23 of its terms off,
+    in sum some twice the largest score, below 2^-10 of it."""
+    lens = [1, 40, 300, 5000, 2999, 17]
+    (k_pages, v_pages, k_scales, v_scales, table), rows = Q.fill(gen, lens, 16, n_kv)
+    k_scales.copy_((k_scales.int() + int(math.log2(size))).clamp(max=255).to(torch.uint8))
+    q = P.normal(gen, len(lens), heads, P.D, scale=1.5 * size)
+    out = G.paged_decode_fp8(q, ints([n - 1 for n in lens]), k_pages, v_pages, k_scales, v_scales, table, workspace=ws)
+    assert G.device_status(ws) == 0 and torch.isfinite(out).all()
+    alone = 0
+    for b, (k, v) in enumerate(rows):
+        for h in range(heads):
+            g = h * n_kv // heads
+            s = torch.sort((k[:, g] * size) @ q[b, h].double() * P.D ** -0.5, descending=True)
+            top, second = float(s.values[0]), float(s.values[1]) if len(s.values) > 1 else -math.inf
+            if top - second > 40 + abs(top) * 2.0 ** -10:
+                # the others weigh e^-40 each at most: nothing beside a value, but not nothing beside 0
+                tol = len(s.values) * math.exp(-40) * float(v.abs().max())
+                assert float((out[b, h].double() - v[int(s.indices[0]), g]).abs().max()) <= tol, f"sequence {b}, head {h}"
+                alone += 1
+    assert alone >= heads and (size < 2 ** 6 or alone > 3 * heads)
