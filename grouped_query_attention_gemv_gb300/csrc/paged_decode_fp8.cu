@@ -24,9 +24,9 @@
 //     thousands it would be added with a rounding that shows in the result.
 //   * The waits on the copies are bounded (gqa_set_wait_limit_ns). One that gives up
 //     records DEV_WAIT_TIMEOUT; its CTA lets issued copies land and joins nothing.
-// Measured (GB300, 6.8 TB/s copied): 93 to 101 us for 559 MB (64 sequences of
-// up to 8,192 rows), 49.4 to 53 for 271 MB (one of 131,072), 30.4 for 133 MB
-// (16 of 1,001, 32 KV heads), 11.1 for 33 MB (8 KV heads), 4.1 for one sequence
+// Measured (GB300, 6.8 TB/s copied): 93 to 102 us for 559 MB (64 sequences of
+// up to 8,192 rows), 49 to 53 for 271 MB (one of 131,072), 29.9 for 133 MB
+// (16 of 1,001, 32 KV heads), 11.5 for 33 MB (8 KV heads), 4.2 for one sequence
 // of 16 rows. What bounds the long ones is the memory at 128-byte rows 1 KB
 // apart: head-major pages ([page, KV head, row]) take 93.5 us where [page, row,
 // KV head] took 104. More in flight changes nothing (3 stages: 99.7 for 99.9) or
@@ -34,8 +34,8 @@
 // to evict first costs 5, 256-byte L2 promotion 20%. Eight KV heads side by side,
 // a warp each, so that neighbouring rows are read together, took 101 us where 96
 // (more parts to join, and the warps drift apart). With more than 8 query heads
-// per KV head the joins are longer and the two tiles of heads bound it: 33 us for
-// 88 MB.
+// per KV head the joins are longer and the two tiles of heads bound it: 30.7 us
+// for 88 MB.
 #include "decode_parts.cuh"
 #include "fp8.cuh"
 

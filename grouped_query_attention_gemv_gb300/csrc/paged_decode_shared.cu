@@ -15,7 +15,8 @@
 //   * P enters the product as two bf16 terms, as in paged_decode.cu: the upper 16
 //     bits and the rest, each over half of the columns of the scores that it
 //     comes from, O += hi V + lo V. A sequence is then as exact in a batch that
-//     shares as in one that does not, for a product of three more a tile.
+//     shares as in one that does not, for a third product: with prefixes of
+//     32,000 rows and more a tile takes 1.85 us for 1.54, with two Q tiles 2.25 for 1.76.
 //   * The key tiles of all items, ITEM_UNITS more for each, are cut into one equal
 //     range per CTA. A CTA's piece of an item leaves a part in the workspace,
 //     at (rows of the items before) + 256 x CTA: from one piece to the next
@@ -37,21 +38,23 @@
 //   warp 8        TMA producer: 128 / min(page, 128) boxes a tile, one lane each
 //   warps 9, 10   MMA issuers, one per Q tile
 //   warps 0-3/4-7 one softmax warpgroup per Q tile, one thread per row
-// Sums are fp32 of the probabilities before they are cut in two. Every wait is bounded (gqa_set_wait_limit_ns); one that
-// gives up records DEV_WAIT_TIMEOUT, lets issued copies and products finish and
-// frees TMEM before the CTA exits.
+// Sums are fp32 of the probabilities before they are cut in two. Every wait is
+// bounded (gqa_set_wait_limit_ns); one that gives up records DEV_WAIT_TIMEOUT, lets
+// issued copies and products finish and frees TMEM before the CTA exits.
 //
-// Measured (GB300, 6.8 TB/s copied): 33.7 us for 64 sequences with up to 512
-// rows of their own under a prefix of 8,000 (103 MB), 49.4 for 96 under
-// three prefixes of up to 4,095 (210 MB), 20.3 for 32 under 8,000 with up to 8
-// rows of their own. Of the first: 3.8 us to plan, then 3 to the first chunks and
-// 4 to the first scores, 15 to 20 of streaming and products at 4 to 5 TB/s
-// together, 1.2 for a part's way to memory, 6 from the last CTA's end to that of
-// the join. Three launches (prefixes, own rows, join) took 68.5; own rows joined
-// in their CTAs 53. Slower were: one Q tile's key tiles shared out between the
-// two issuers (70 us for 60: two stages do not hide the memory for both), and L2
-// asked for tiles ahead, once pages are looked up ahead (54 us for 48.5, a
-// prefix of 32,000).
+// Measured (GB300, 6.8 TB/s copied): 35.8 us for 64 sequences with up to 512
+// rows of their own under a prefix of 8,000 (103 MB), 49.7 for 96 under
+// three prefixes of up to 4,095 (210 MB), 22.8 for 32 under 8,000 with up to 8
+// rows of their own; 64 sequences with 16 query heads per KV head 37.2 (4 KV heads,
+// two prefixes of up to 6,000) and 25.9 (one, a prefix of 8,000), with one 95.6 (32
+// KV heads, a prefix of 8,000, 408 MB). Of the first, when P was one term (33.7):
+// 3.8 us to plan, then 3 to the first chunks and 4 to the first scores, 15 to 20 of
+// streaming and products at 4 to 5 TB/s together, 1.2 for a part's way to memory, 6
+// from the last CTA's end to that of the join. Three launches (prefixes, own rows,
+// join) took 68.5; own rows joined in their CTAs 53. Slower were: one Q tile's key
+// tiles shared out between the two issuers (70 us for 60: two stages do not hide
+// the memory for both), and L2 asked for tiles ahead, once pages are looked up ahead
+// (54 us for 48.5, a prefix of 32,000).
 #include <math.h>
 
 #include "decode_stream.cuh"
@@ -175,7 +178,8 @@ struct Groups {
 __device__ __forceinline__ void two_terms(float2 p, uint32_t& hi, uint32_t& lo) {
   const uint32_t u0 = __float_as_uint(p.x), u1 = __float_as_uint(p.y);
   hi = __byte_perm(u0, u1, 0x7632);
-  const float2 minus = make_float2(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u), __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u));
+  const float2 minus = make_float2(__uint_as_float((u0 & 0xffff0000u) ^ 0x80000000u),
+                                   __uint_as_float((u1 & 0xffff0000u) ^ 0x80000000u));
   const float2 rest = add2(fma2(p, make_float2(1.f + 0x1p-23f, 1.f + 0x1p-23f), minus), make_float2(0x1p-133f, 0x1p-133f));
   lo = pack_bf16(rest.x, rest.y);
 }
@@ -347,7 +351,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float tile = static_cast<float>(bs.tiles[0]) * ONE_TILE + static_cast<float>(bs.tiles[1]) * TWO_TILES;
     float cost = INFINITY;
     if (tid > 0 && tid <= grid && (tid < grid || chunks == 0)) {
-      const float own = chunks > 0 ? fmaxf(chunks * (NT > 1 ? WIDE_CHUNK : CHUNK) / (grid - tid), chunks * CHUNK_MEMORY) + OWN_MORE : 0.f;
+      const float chunk = (NT > 1 ? WIDE_CHUNK : CHUNK) / (grid - tid);
+      const float own = chunks > 0 ? chunks * fmaxf(chunk, CHUNK_MEMORY) + OWN_MORE : 0.f;
       cost = fmaxf(tile * a.n_kv / tid + PREFIX_MORE, own);
     }
     const unsigned least = __reduce_min_sync(0xffffffffu, __float_as_uint(cost));

@@ -19,9 +19,9 @@
 // dims. The largest |x| of a row is four exchanges of its 16 lanes. With many
 // tokens a warp takes several batches, so that the chain to the token's place
 // is walked less often.
-// Measured (GB300, 6.8 TB/s copied), 32 and 8 heads: 59.2 us for 7 prompts into
-// 8 bits (356 MB), 38.9 for 5 prompts into bf16, 64 dims turned (244 MB), 2.7
-// for one token, 2.8 for 64.
+// Measured (GB300, 6.8 TB/s copied), 32 and 8 heads: 59.6 us for 7 prompts into
+// 8 bits (356 MB), 38.7 for 5 prompts into bf16, 64 dims turned (244 MB), 2.8
+// for one token, 2.9 for 64.
 #include <math.h>
 
 #include "fp8.cuh"
